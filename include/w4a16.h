@@ -81,8 +81,9 @@ enum w4a16_path {
     W4A16_PATH_W4A8 = 5,       /* reported by w4a8_plan only: int8-activation tiles               */
     W4A16_PATH_GROUPED = 6,    /* reported by w4a16_grouped_plan only: one tile launch over the
                                   column tiles of every projection                                */
-    W4A16_PATH_PER_PROJECTION = 7 /* reported by w4a16_grouped_plan only: one w4a16_linear dispatch
+    W4A16_PATH_PER_PROJECTION = 7, /* reported by w4a16_grouped_plan only: one w4a16_linear dispatch
                                   per projection                                                  */
+    W4A16_PATH_MXFP4 = 8       /* reported by mxfp4_plan only: MXFP4 tiles                         */
 };
 
 /* Launch plan chosen by the dispatch policy (filled by w4a16_plan). */
@@ -393,6 +394,123 @@ uint64_t w4a8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t gr
  */
 int w4a8_linear(const uint16_t* x, const uint32_t* wq, const uint16_t* scales, const uint16_t* biases, uint16_t* y,
                 int64_t M, int64_t N, int64_t K, int32_t group, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * MXFP4: microscaled 4-bit floating point.  A row of K values is cut into blocks of 32; a block has
+ * one scale byte e, the factor 2^(e - 127) (255 is NaN), and 32 codes of 4 bits: a sign (bit 3), two
+ * exponent bits and one mantissa bit, the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.  It is the format
+ * that gfx950's scaled matrix instructions read.
+ *
+ *   codes   uint8 [R, K/2]    code k in byte k / 2, the lower index in the low half; 16-byte aligned
+ *   scales  uint8 [R, K/32]
+ *
+ * Ownership, streams, asynchrony and the status codes are those stated at the top of this file, and
+ * so is the rule that all checks come before any launch.  There is no `group` argument: the block is
+ * part of the format.  Limits: 1 <= rows, M, N <= 2^30, 32 <= K <= 2^20, K % 32 == 0; x, dy, dgate,
+ * dup, codes and the workspace 16-byte aligned, other bf16 buffers 2-byte aligned; an output that
+ * shares bytes with an input or another output returns W4A16_ERR_OVERLAP.
+ *
+ * A decoded weight is one of the 16 values times a power of two and is exact in bf16; scale bytes
+ * 253 and 254, which no quantizer of finite values below produces, can exceed bf16's range and then
+ * stand for infinities.  All sums are fp32, rounded to bf16 once.
+ */
+enum mxfp4_type { MXFP4_BF16 = 0, MXFP4_FP32 = 1 };
+
+enum mxfp4_op {
+    MXFP4_LINEAR = 0,            /* mxfp4_linear                                                  */
+    MXFP4_LINEAR_BACKWARD = 1,   /* mxfp4_linear_backward                                         */
+    MXFP4_QMM_A4 = 2,            /* qmm_mxfp4a4                                                   */
+    MXFP4A4_LINEAR = 3,          /* mxfp4a4_linear                                                */
+    MXFP4_GATE_UP = 4,           /* mxfp4_gate_up_swiglu                                          */
+    MXFP4_GATE_UP_BACKWARD = 5   /* mxfp4_gate_up_swiglu_backward                                 */
+};
+
+/*
+ * Quantize rows of x (bf16 or fp32, x_type) to MXFP4:
+ *
+ *     a = max |x| over the block,  e = max(floor(log2 a) - 2, -127) + 127  (0 where a = 0),
+ *     code = x / 2^(e - 127) rounded to the nearest magnitude, ties to the even mantissa bit, values
+ *            above 6 to 6, with the sign of x.
+ *
+ * A block that holds an infinity or a NaN becomes e = 255 with codes 0, which decodes to NaN.  One
+ * launch.  Errors: W4A16_ERR_NULL, _ERR_SHAPE, _ERR_ALIGN, _ERR_OVERLAP, _ERR_UNSUPPORTED (another
+ * x_type), _ERR_LAUNCH.
+ */
+int mxfp4_quantize_rows(const void* x, int32_t x_type, uint8_t* codes, uint8_t* scales, int64_t R, int64_t K,
+                        void* stream);
+
+/* The values of MXFP4 rows as bf16 [R, K] (exact); y 16-byte aligned.  One launch. */
+int mxfp4_dequantize_rows(const uint8_t* codes, const uint8_t* scales, uint16_t* y, int64_t R, int64_t K,
+                          void* stream);
+
+/*
+ * Launch plan of an MXFP4 operator (enum mxfp4_op; M activation rows, N weight rows, K values of a
+ * weight row; the gate / up backward reports the launch that computes dx).  split_k as for
+ * qmm_w4a16: 0 = policy, 1 = off, S > 1 = S slices of the contraction (clamped to its steps), whose
+ * fp32 partials are summed in slice order.  workspace_bytes is what the operator's call needs.
+ * num_cus as in w4a16_plan.  Pure host arithmetic.  Returns W4A16_OK, _ERR_NULL, _ERR_SHAPE,
+ * _ERR_UNSUPPORTED (an unknown op) or _ERR_DEVICE.
+ */
+int mxfp4_plan(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k, int32_t num_cus, w4a16_plan_t* out);
+
+/*
+ * Weight-only projection of bf16 activations: y = x . W^T with x [M, K], W [N, K] in MXFP4, y
+ * [M, N], any M >= 1.  With too little workspace a policy split is dropped (the unsplit plan
+ * computes the same within rounding); a forced one returns W4A16_ERR_WORKSPACE.
+ */
+int mxfp4_linear(const uint16_t* x, const uint8_t* codes, const uint8_t* scales, uint16_t* y, int64_t M, int64_t N,
+                 int64_t K, int32_t split_k, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of mxfp4_linear's input: dx = dy . W with dy [M, N], dx [M, K].  The weights are frozen
+ * codes and have no gradient.  N <= 2^20 (else W4A16_ERR_SHAPE).  Workspace as for mxfp4_linear;
+ * where N % 8 != 0 it also holds a copy of dy with padded rows, and W4A16_ERR_WORKSPACE is returned
+ * without room for that.
+ */
+int mxfp4_linear_backward(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, uint16_t* dx, int64_t M,
+                          int64_t N, int64_t K, int32_t split_k, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * Product of two MXFP4 operands on the scaled matrix cores: y = X . W^T with X [M, K] as xq, xs and
+ * W [N, K]; products are exact.  Workspace as for mxfp4_linear.
+ */
+int qmm_mxfp4a4(const uint8_t* xq, const uint8_t* xs, const uint8_t* codes, const uint8_t* scales, uint16_t* y,
+                int64_t M, int64_t N, int64_t K, int32_t split_k, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/*
+ * One-call projection with 4-bit activations: mxfp4_quantize_rows of bf16 x into the start of
+ * `workspace`, then qmm_mxfp4a4 with the rest of it for partials.  A missing workspace, or one
+ * without room for the activations, returns W4A16_ERR_WORKSPACE.  Nothing routes here by itself:
+ * 4-bit activations are the caller's choice.
+ */
+int mxfp4a4_linear(const uint16_t* x, const uint8_t* codes, const uint8_t* scales, uint16_t* y, int64_t M, int64_t N,
+                   int64_t K, int32_t split_k, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gated half of a feed-forward block with MXFP4 weights, both projections, activation and product in
+ * one tile kernel (as w4a16_gate_up_swiglu): h = silu(x . Wg^T) * (x . Wu^T), g and u never rounded.
+ * Workspace as for mxfp4_linear (twice the partials).
+ */
+int mxfp4_gate_up_swiglu(const uint16_t* x, const uint8_t* codes_gate, const uint8_t* scales_gate,
+                         const uint8_t* codes_up, const uint8_t* scales_up, uint16_t* h, int64_t M, int64_t N,
+                         int64_t K, int32_t split_k, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward pass from x and dh [M, N]; nothing is kept by the forward call, g and u are computed
+ * again.  With s = sigmoid(g):
+ *
+ *     dup = dh g s,   dgate = dh u s (1 + g (1 - s)),   dx = dgate . Wg + dup . Wu.
+ *
+ * dgate and dup [M, N] (the gradients of both projections' outputs, which adapters beside the frozen
+ * weights need) are rounded to bf16 once and dx [M, K] is computed from the rounded values.  N <= 2^20.
+ * split_k and the workspace concern the dx product (mxfp4_linear_backward, with two padded copies).
+ */
+int mxfp4_gate_up_swiglu_backward(const uint16_t* x, const uint8_t* codes_gate, const uint8_t* scales_gate,
+                                  const uint8_t* codes_up, const uint8_t* scales_up, const uint16_t* dh, uint16_t* dx,
+                                  uint16_t* dgate, uint16_t* dup, int64_t M, int64_t N, int64_t K, int32_t split_k,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

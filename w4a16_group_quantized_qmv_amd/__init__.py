@@ -121,6 +121,20 @@ def load():
     lib.w4a16_linear_grouped.restype = ctypes.c_int
     lib.w4a16_linear_grouped.argtypes = [u16p, i32, pp, pp, pp, pp, ctypes.POINTER(i64), i64, i64, i32, vp,
                                          ctypes.c_size_t, vp]
+    size = ctypes.c_size_t
+    for name, argtypes in {
+            "mxfp4_quantize_rows": [vp, i32, vp, vp, i64, i64, vp],
+            "mxfp4_dequantize_rows": [vp, vp, u16p, i64, i64, vp],
+            "mxfp4_plan": [i32, i64, i64, i64, i32, i32, ctypes.POINTER(Plan)],
+            "mxfp4_linear": [u16p, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
+            "mxfp4_linear_backward": [u16p, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
+            "qmm_mxfp4a4": [vp, vp, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
+            "mxfp4a4_linear": [u16p, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
+            "mxfp4_gate_up_swiglu": [u16p, vp, vp, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
+            "mxfp4_gate_up_swiglu_backward": [u16p, vp, vp, vp, vp, u16p, u16p, u16p, u16p, i64, i64, i64, i32, vp,
+                                              size, vp]}.items():
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = argtypes
     lib.w4a16_time_next_launch.restype = ctypes.c_int
     lib.w4a16_time_next_launch.argtypes = [vp, vp]
     _LIB = lib
@@ -632,3 +646,9 @@ class PreparedW4A8:
         if st != W4A16_OK:
             _raise_for(st, "w4a8_linear")
         return self.y
+
+
+from . import mxfp4 as _mxfp4  # noqa: E402  (uses the helpers above)
+from .mxfp4 import *  # noqa: E402,F401,F403
+
+__all__ += _mxfp4.__all__

@@ -4,10 +4,10 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <mutex>
 #include <stdint.h>
 
+#include "abi_common.h"
 #include "internal.h"
 #include "w4a16.h"
 
@@ -24,44 +24,11 @@ constexpr size_t kQmvWideSkinnyLds = 80 * 1024;
 constexpr int64_t kQmvPerRowMaxRows = 2;   // rows the per-row width-generic kernel serves
 constexpr int kQmvBitsWaves = 4;           // waves splitting K in the width-generic kernels
 constexpr int kSplitMinGroups = 4;        // fewest groups one split-K slice may own
-constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
-// Largest K: keeps every per-lane buffer offset of the kernels (at most 256 K bytes past a
-// wave's base) inside 32 bits.
-constexpr int64_t kMaxK = int64_t{1} << 20;
-
-std::atomic<int> g_cu_cache[64];
-
-int query_num_cus(int32_t* out) {
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return W4A16_ERR_DEVICE;
-    if (dev >= 0 && dev < 64) {
-        const int cached = g_cu_cache[dev].load(std::memory_order_relaxed);
-        if (cached > 0) {
-            *out = cached;
-            return W4A16_OK;
-        }
-    }
-    int cus = 0;
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-        return W4A16_ERR_DEVICE;
-    if (dev >= 0 && dev < 64) g_cu_cache[dev].store(cus, std::memory_order_relaxed);
-    *out = cus;
-    return W4A16_OK;
-}
-
 int check_shape(int64_t M, int64_t N, int64_t K, int32_t group) {
     if (M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxK) return W4A16_ERR_SHAPE;
     if (group != W4A16_GROUP) return W4A16_ERR_GROUP;
     if (K % W4A16_GROUP != 0) return W4A16_ERR_SHAPE;
     return W4A16_OK;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Byte ranges [p, p + n) of two buffers share at least one byte.
-bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    return na > 0 && nb > 0 && pa < pb + nb && pb < pa + na;
 }
 
 // Pointer checks of a projection y [M, N] = x [M, K] . dequant(wq [N, K * bits / 32])^T (shape
@@ -78,8 +45,6 @@ int check_buffers(const uint16_t* x, const uint32_t* wq, const uint16_t* s, cons
         return W4A16_ERR_OVERLAP;
     return W4A16_OK;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 void plan_qmv(int64_t M, int64_t N, int64_t K, int32_t cus, w4a16_plan_t* p) {
     // Measured on MI355X (K = 1024 .. 9728, N = 1024 .. 151936, M = 1 .. 16, random data): below
@@ -273,8 +238,6 @@ int make_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t path, int3
     out->num_cus = cus;
     return W4A16_OK;
 }
-
-int to_status(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_LAUNCH; }
 
 // a skinny plan of at most 16 rows runs the matvec kernels (tile_m = 16); otherwise tiles
 bool uses_qmv_kernels(const w4a16_plan_t& p) {

@@ -1,0 +1,56 @@
+// Host-side launchers of the MXFP4 kernels, shared between the C-ABI layer and the kernel files.
+#pragma once
+
+#include "internal.h"
+
+namespace w4a16 {
+
+constexpr int kMxBlock = 32;   // values of one block
+
+// Rows of x (bf16, or fp32 when x_fp32) as `blocks` consecutive blocks of 32 values.
+hipError_t launch_mx_quantize(const void* x, bool x_fp32, uint8_t* codes, uint8_t* scales, int64_t blocks,
+                              hipStream_t stream);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, uint16_t* y, int64_t blocks,
+                                hipStream_t stream);
+
+// Rows of N bf16 values as rows of ceil(N / 8) * 8, the rest zeros.
+hipError_t launch_mx_pad_rows(const uint16_t* x, uint16_t* y, int64_t M, int N, hipStream_t stream);
+
+// What a tile multiplies.
+enum class MxOperands {
+    kCodes,     // MXFP4 rows by MXFP4 rows, on the scaled matrix cores
+    kRows,      // bf16 rows by MXFP4 rows, contracted along the blocks
+    kColumns    // bf16 rows by MXFP4 columns: contracted across the weight rows
+};
+// What a tile does with the products.
+enum class MxEpilogue {
+    kStore,     // y = bf16(acc), or fp32 partials
+    kGlu,       // two weight sets: y = silu(g) * u
+    kGluGrad    // two weight sets and dh: the gradients of both projections
+};
+
+struct MxTileArgs {
+    const void* a[2];          // rows of the left operand (kColumns: one per weight set)
+    int64_t pitch;             // bytes of one of its rows
+    const uint8_t* a_scales;   // kCodes
+    const uint8_t* w[2];       // codes of the weight sets
+    const uint8_t* w_scales[2];
+    const uint16_t* dh;        // kGluGrad
+    uint16_t* y[2];            // output; kGluGrad: the gradients of the gate and of the up projection
+    float* ws;                 // fp32 partials [weight set][split][M][N] when split > 1
+    int M, N, L;               // output rows, output columns (of one weight set), contraction length
+    int sets;                  // weight sets (kColumns: summed over)
+    int split;                 // slices of the contraction
+};
+
+struct MxTileShape {
+    int bm, bn, waves;         // rows and weight rows of a workgroup's tile
+};
+constexpr int kNumMxTiles = 1;
+extern const MxTileShape kMxTiles[kNumMxTiles];
+// Values of the contraction in one pipeline step.
+inline int mx_step(MxOperands op) { return op == MxOperands::kCodes ? 512 : 64; }
+
+hipError_t launch_mx_tile(MxOperands op, MxEpilogue epi, int tile, const MxTileArgs& args, hipStream_t stream);
+
+}  // namespace w4a16

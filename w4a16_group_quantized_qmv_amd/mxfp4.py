@@ -1,0 +1,235 @@
+"""MXFP4 operators of ``libw4a16.so``: quantization, products, and the gated feed-forward block.
+
+The functions have the names of the C ABI and only marshal arguments, as the rest of the package.
+
+Tensor conventions (all on the GPU, contiguous):
+    x, dy, y, h, ...   torch.bfloat16 [rows, columns]
+    codes              torch.uint8    [R, K/2]    two codes per byte, the lower index in the low half
+    scales             torch.uint8    [R, K/32]   the factor 2^(byte - 127) of 32 values; 255 is NaN
+A weight matrix is its ``(codes, scales)`` pair with R = N output columns; K % 32 == 0.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import functools
+
+from . import _keep_for_stream, _raise_for, _stream_handle, _torch, Plan, load
+
+__all__ = [
+    "MXFP4_BLOCK", "MXFP4_LINEAR", "MXFP4_LINEAR_BACKWARD", "MXFP4_QMM_A4", "MXFP4A4_LINEAR", "MXFP4_GATE_UP",
+    "MXFP4_GATE_UP_BACKWARD", "PATH_MXFP4", "mxfp4_plan", "mxfp4_quantize_rows", "mxfp4_dequantize_rows",
+    "mxfp4_linear", "mxfp4_linear_backward", "qmm_mxfp4a4", "mxfp4a4_linear", "mxfp4_gate_up_swiglu",
+    "mxfp4_gate_up_swiglu_backward",
+]
+
+MXFP4_BLOCK = 32
+(MXFP4_LINEAR, MXFP4_LINEAR_BACKWARD, MXFP4_QMM_A4, MXFP4A4_LINEAR, MXFP4_GATE_UP,
+ MXFP4_GATE_UP_BACKWARD) = range(6)
+PATH_MXFP4 = 8
+
+
+def mxfp4_plan(op: int, M: int, N: int, K: int, split_k: int = 0, num_cus: int = 0) -> dict:
+    """Launch plan of an MXFP4 operator (``MXFP4_LINEAR`` and so on)."""
+    p = Plan()
+    _raise_for(load().mxfp4_plan(op, M, N, K, split_k, num_cus, ctypes.byref(p)), "mxfp4_plan")
+    return p.as_dict()
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(op, M, N, K, split_k, device):
+    """The plan's workspace bytes on this (current) device; the plan depends on nothing else."""
+    return int(mxfp4_plan(op, M, N, K, split_k)["workspace_bytes"])
+
+
+def _tensor(t, name, dtype, shape, device=None):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, not {device}")
+
+
+def _matrix(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {t.dim()} dimensions")
+    return t.shape
+
+
+def _weights(pair, name, device, like=None):
+    """Checks a (codes, scales) pair; returns (N, K)."""
+    torch = _torch()
+    codes, scales = pair
+    N, half = _matrix(codes, f"{name} codes")
+    K = 2 * half
+    if K == 0 or K % MXFP4_BLOCK:
+        raise ValueError(f"{name}: K={K} must be a positive multiple of {MXFP4_BLOCK}")
+    if like is not None and (N, K) != like:
+        raise ValueError(f"{name} must be [{like[0]}, {like[1]}], got [{N}, {K}]")
+    _tensor(codes, f"{name} codes", torch.uint8, (N, half), device)
+    _tensor(scales, f"{name} scales", torch.uint8, (N, K // MXFP4_BLOCK), device)
+    return N, K
+
+
+def _output(t, name, shape, device, dtype=None):
+    torch = _torch()
+    dtype = dtype or torch.bfloat16
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _tensor(t, name, dtype, shape, device)
+    return t
+
+
+def _call(name, op, dims, device, stream, workspace, own, args, split_k=0):
+    """One C-ABI call on ``device``: its workspace (allocated where the caller gave none), the stream,
+    the status.  ``own``: tensors allocated for this call."""
+    torch = _torch()
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(name, op, dims, device, stream, workspace, own, args, split_k)
+    tail = ()
+    if op is not None:
+        if split_k < 0:
+            raise ValueError(f"split_k={split_k} must not be negative")
+        need = _workspace_bytes(op, *dims, split_k, device.index)
+        ws, nbytes = None, 0
+        if need:
+            if workspace is None:
+                ws = torch.empty(need, dtype=torch.uint8, device=device)
+                own = (*own, ws)
+            else:
+                ws = workspace
+                if not ws.is_cuda or not ws.is_contiguous() or ws.device != device:
+                    raise ValueError(f"workspace must be a contiguous tensor on {device}")
+            nbytes = ws.numel() * ws.element_size()
+        tail = (split_k, None if ws is None else ws.data_ptr(), nbytes)
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    else:
+        handle = _stream_handle(stream)
+        _keep_for_stream(stream, device, *own)
+    _raise_for(getattr(load(), name)(*args, *dims, *tail, handle), name)
+
+
+def mxfp4_quantize_rows(x, codes=None, scales=None, stream=None):
+    """MXFP4 codes and scales of the rows of ``x`` (bf16 or fp32 ``[R, K]``); returns
+    ``(codes, scales)``.  A block holding an infinity or a NaN decodes to NaN."""
+    torch = _torch()
+    R, K = _matrix(x, "x")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    if K == 0 or K % MXFP4_BLOCK:
+        raise ValueError(f"K={K} must be a positive multiple of {MXFP4_BLOCK}")
+    _tensor(x, "x", x.dtype, (R, K))
+    own = [t is None for t in (codes, scales)]
+    codes = _output(codes, "codes", (R, K // 2), x.device, torch.uint8)
+    scales = _output(scales, "scales", (R, K // MXFP4_BLOCK), x.device, torch.uint8)
+    _call("mxfp4_quantize_rows", None, (R, K), x.device, stream, None,
+          tuple(t for t, o in zip((codes, scales), own) if o),
+          (x.data_ptr(), int(x.dtype == torch.float32), codes.data_ptr(), scales.data_ptr()))
+    return codes, scales
+
+
+def mxfp4_dequantize_rows(codes, scales, y=None, stream=None):
+    """The values of MXFP4 rows as bf16 ``[R, K]`` (exact); returns y."""
+    device = codes.device
+    R, K = _weights((codes, scales), "rows", device)
+    own = y is None
+    y = _output(y, "y", (R, K), device)
+    _call("mxfp4_dequantize_rows", None, (R, K), device, stream, None, (y,) if own else (),
+          (codes.data_ptr(), scales.data_ptr(), y.data_ptr()))
+    return y
+
+
+def _projection(name, op, x, codes, scales, y, split_k, workspace, stream):
+    torch = _torch()
+    M, columns = _matrix(x, "x")
+    device = x.device
+    N, K = _weights((codes, scales), "weight", device)
+    back = op == MXFP4_LINEAR_BACKWARD
+    _tensor(x, "dy" if back else "x", torch.bfloat16, (M, N if back else K))
+    own = y is None
+    y = _output(y, "dx" if back else "y", (M, K if back else N), device)
+    _call(name, op, (M, N, K), device, stream, workspace, (y,) if own else (),
+          (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr()), split_k)
+    return y
+
+
+def mxfp4_linear(x, codes, scales, y=None, split_k: int = 0, workspace=None, stream=None):
+    """Weight-only projection ``y = x . W^T`` of bf16 ``x [M, K]``; split_k as for ``qmm_w4a16``."""
+    return _projection("mxfp4_linear", MXFP4_LINEAR, x, codes, scales, y, split_k, workspace, stream)
+
+
+def mxfp4_linear_backward(dy, codes, scales, dx=None, split_k: int = 0, workspace=None, stream=None):
+    """Gradient of ``mxfp4_linear``'s input, ``dx = dy . W``; the weights are frozen."""
+    return _projection("mxfp4_linear_backward", MXFP4_LINEAR_BACKWARD, dy, codes, scales, dx, split_k, workspace,
+                       stream)
+
+
+def mxfp4a4_linear(x, codes, scales, y=None, split_k: int = 0, workspace=None, stream=None):
+    """Projection with 4-bit activations: ``x`` is quantized to MXFP4 in the call's workspace, the
+    product runs on the scaled matrix cores.  Returns y."""
+    return _projection("mxfp4a4_linear", MXFP4A4_LINEAR, x, codes, scales, y, split_k, workspace, stream)
+
+
+def qmm_mxfp4a4(xq, xs, codes, scales, y=None, split_k: int = 0, workspace=None, stream=None):
+    """``y = X . W^T`` of two MXFP4 operands (``xq``, ``xs`` from ``mxfp4_quantize_rows``)."""
+    device = xq.device
+    N, K = _weights((codes, scales), "weight", device)
+    M, _ = _matrix(xq, "xq")
+    _weights((xq, xs), "x", device, (M, K))
+    own = y is None
+    y = _output(y, "y", (M, N), device)
+    _call("qmm_mxfp4a4", MXFP4_QMM_A4, (M, N, K), device, stream, workspace, (y,) if own else (),
+          (xq.data_ptr(), xs.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr()), split_k)
+    return y
+
+
+def mxfp4_gate_up_swiglu(x, gate, up, h=None, split_k: int = 0, workspace=None, stream=None):
+    """``h = silu(x . Wg^T) * (x . Wu^T)`` in one kernel; ``gate`` and ``up`` are ``(codes, scales)``
+    pairs of one shape.  Returns h."""
+    torch = _torch()
+    M, _ = _matrix(x, "x")
+    device = x.device
+    N, K = _weights(gate, "gate", device)
+    _weights(up, "up", device, (N, K))
+    _tensor(x, "x", torch.bfloat16, (M, K))
+    own = h is None
+    h = _output(h, "h", (M, N), device)
+    _call("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), device, stream, workspace, (h,) if own else (),
+          (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), h.data_ptr()),
+          split_k)
+    return h
+
+
+def mxfp4_gate_up_swiglu_backward(x, gate, up, dh, dx=None, dgate=None, dup=None, split_k: int = 0, workspace=None,
+                                  stream=None):
+    """Backward pass of ``mxfp4_gate_up_swiglu`` from ``x`` and ``dh``; returns ``(dx, dgate, dup)``,
+    the last two the gradients of both projections' outputs.  The weights are frozen."""
+    torch = _torch()
+    M, _ = _matrix(x, "x")
+    device = x.device
+    N, K = _weights(gate, "gate", device)
+    _weights(up, "up", device, (N, K))
+    _tensor(x, "x", torch.bfloat16, (M, K))
+    _tensor(dh, "dh", torch.bfloat16, (M, N), device)
+    own = [t is None for t in (dx, dgate, dup)]
+    dx = _output(dx, "dx", (M, K), device)
+    dgate = _output(dgate, "dgate", (M, N), device)
+    dup = _output(dup, "dup", (M, N), device)
+    _call("mxfp4_gate_up_swiglu_backward", MXFP4_GATE_UP_BACKWARD, (M, N, K), device, stream, workspace,
+          tuple(t for t, o in zip((dx, dgate, dup), own) if o),
+          (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), dh.data_ptr(),
+           dx.data_ptr(), dgate.data_ptr(), dup.data_ptr()), split_k)
+    return dx, dgate, dup
