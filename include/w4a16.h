@@ -83,7 +83,8 @@ enum w4a16_path {
                                   column tiles of every projection                                */
     W4A16_PATH_PER_PROJECTION = 7, /* reported by w4a16_grouped_plan only: one w4a16_linear dispatch
                                   per projection                                                  */
-    W4A16_PATH_MXFP4 = 8       /* reported by mxfp4_plan only: MXFP4 tiles                         */
+    W4A16_PATH_MXFP4 = 8,      /* reported by mxfp4_plan only: MXFP4 tiles                         */
+    W4A16_PATH_MXFP4_QMV = 9   /* reported by mxfp4_plan only: the MXFP4 decode kernel             */
 };
 
 /* Launch plan chosen by the dispatch policy (filled by w4a16_plan). */

@@ -143,7 +143,7 @@ def test_check_finds_planted_mistakes():
 def test_plan_covers_the_output(op, M, N, K):
     p = w4.mxfp4_plan(OPS[op], M, N, K, 0, CUS)
     columns = K if "backward" in op else N
-    assert p["path"] in (w4.PATH_MXFP4,) and p["num_cus"] == CUS
+    assert p["path"] in (w4.PATH_MXFP4, w4.PATH_MXFP4_QMV) and p["num_cus"] == CUS
     assert p["grid_y"] * p["tile_m"] >= M > (p["grid_y"] - 1) * p["tile_m"]
     assert p["grid_x"] * p["tile_n"] >= columns > (p["grid_x"] - 1) * p["tile_n"]
     assert p["block_threads"] % 64 == 0 and p["block_threads"] <= 1024

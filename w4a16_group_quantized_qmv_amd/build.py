@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libw4a16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["abi.hip", "qmv.hip", "qmv_bits.hip", "qmv_burst.hip", "qmm.hip", "w4a8.hip",
-           "mxfp4_abi.hip", "mxfp4_rows.hip", "mxfp4_tile.hip"]
+           "mxfp4_abi.hip", "mxfp4_rows.hip", "mxfp4_tile.hip", "mxfp4_qmv.hip"]
 ARCH = "gfx950"
 
 

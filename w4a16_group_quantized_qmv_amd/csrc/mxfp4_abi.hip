@@ -58,6 +58,7 @@ struct Product {
     int sets;            // weight sets
     int tile;
     int split;
+    bool decode = false; // the decode kernel
 };
 
 // The product that an operator's last launch computes.
@@ -82,6 +83,15 @@ int64_t units_of(const Product& p) {
 }
 
 void choose(Product& p, int32_t split_k, int32_t cus) {
+    MxQmvShape q;
+    if (split_k == 0 && p.M <= kMxQmvRows &&
+        mx_qmv_shape(p.operands, p.sets, static_cast<int>(p.M), static_cast<int>(p.L), &q)) {
+        p.decode = true;
+        return;
+    }
+    // 256 x 256 tiles where they reach half of the compute units
+    p.tile = 1;
+    if (2 * tiles_of(p) < cus) p.tile = 0;
     const int64_t units = units_of(p), tiles = tiles_of(p);
     if (split_k > 0) {
         p.split = static_cast<int>(std::min<int64_t>(split_k, units));
@@ -123,6 +133,19 @@ int make_plan(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k, int3
     out->k_waves = 1;
     out->num_cus = cus;
     out->variant = p.tile;
+    if (p.decode) {
+        MxQmvShape q;
+        mx_qmv_shape(p.operands, p.sets, static_cast<int>(p.M), static_cast<int>(p.L), &q);
+        out->path = W4A16_PATH_MXFP4_QMV;
+        out->tile_m = q.rows;
+        out->tile_n = q.columns;
+        out->tile_k = kMxBlock;
+        out->grid_x = static_cast<int32_t>(ceil_div(p.N, q.columns));
+        out->grid_y = 1;
+        out->block_threads = 64 * q.waves;
+        out->k_waves = q.waves;
+        out->variant = q.batch;
+    }
     out->workspace_bytes = fixed_bytes(op, M, N, K) + partial_bytes(p);
     if (product) *product = p;
     return W4A16_OK;
@@ -165,6 +188,7 @@ int run_product(const Product& p, MxTileArgs args, void* partials, hipStream_t s
     args.split = p.split;
     args.ws = static_cast<float*>(partials);
     if (args.pitch == 0) args.pitch = p.operands == MxOperands::kCodes ? p.L / 2 : 2 * p.L;
+    if (p.decode) return to_status(launch_mx_qmv(p.operands, p.epilogue, args, stream));
     hipError_t e = launch_mx_tile(p.operands, p.epilogue, p.tile, args, stream);
     if (e != hipSuccess || p.split == 1) return to_status(e);
     return to_status(p.epilogue == MxEpilogue::kGlu ? launch_splitk_reduce_glu(args.ws, args.y[0], p.M * p.N, p.split, stream)

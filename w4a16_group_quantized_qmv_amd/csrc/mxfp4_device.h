@@ -52,6 +52,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// 1 / (1 + 2^(-z log2 e)) from the hardware's exponential and reciprocal, each within a step of fp32;
+// the product with log2 e is off by half a step of itself, |z| 2^-24 of the result at most.  2^large
+// is infinite and its reciprocal 0, the limit.
+__device__ __forceinline__ float mx_sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
+
 // Orders a wave's LDS writes before its own lanes' later reads (no other wave takes part).
 __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

@@ -46,10 +46,21 @@ struct MxTileArgs {
 struct MxTileShape {
     int bm, bn, waves;         // rows and weight rows of a workgroup's tile
 };
-constexpr int kNumMxTiles = 1;
+constexpr int kNumMxTiles = 2;
 extern const MxTileShape kMxTiles[kNumMxTiles];
 // Values of the contraction in one pipeline step.
 inline int mx_step(MxOperands op) { return op == MxOperands::kCodes ? 512 : 64; }
+
+// Decode rows: workgroups of `columns` weight rows whose `waves` waves take `share` units (1 KB of
+// codes) of the contraction each, `batch` of them in flight; `rows` activation row slots.
+constexpr int kMxQmvRows = 16;
+constexpr int kMxQmvWaves = 16;
+struct MxQmvShape {
+    int rows, columns, waves, share, batch;
+    size_t lds;
+};
+bool mx_qmv_shape(MxOperands op, int sets, int M, int K, MxQmvShape* out);
+hipError_t launch_mx_qmv(MxOperands op, MxEpilogue epi, const MxTileArgs& args, hipStream_t stream);
 
 hipError_t launch_mx_tile(MxOperands op, MxEpilogue epi, int tile, const MxTileArgs& args, hipStream_t stream);
 

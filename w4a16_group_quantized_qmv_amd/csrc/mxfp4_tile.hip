@@ -50,9 +50,8 @@ __device__ __forceinline__ void loads_done_barrier() {
     asm volatile("" ::: "memory");
 }
 
-__device__ __forceinline__ float sigmoid_f32(float z) { return 1.f / (1.f + expf(-z)); }
-
-template <MxOperands OP, MxEpilogue EPI, int BM, int BN, int WR, int WC>
+// WHOLE (kCodes): rows of scales are whole, aligned pieces of 16 bytes.
+template <MxOperands OP, MxEpilogue EPI, int BM, int BN, int WR, int WC, bool WHOLE>
 __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs p, int tiles_m, int tiles_n) {
     constexpr int NW = WR * WC, NT = 64 * NW;
     constexpr int MI = BM / WR / 32, NI = BN / WC / 32;      // 32 x 32 blocks of a wave
@@ -133,7 +132,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
                                              static_cast<int64_t>(p.M - m0) * left_row)
                                : ar0;
     auto issue_left = [&](int t, auto ic) {
-        const int set = kColumns && t >= set_steps ? 1 : 0;
+        const int set = kColumns && p.sets > 1 && t >= set_steps ? 1 : 0;
         issue_rows(set ? ar1 : ar0, a_off, left_row, a_stage(ic), t, t - set * set_steps,
                    std::integral_constant<int, A_LOADS>{});
     };
@@ -150,37 +149,40 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     static_assert(!(kCodes && kPair), "the pair decodes its weights");
     const uint32_t b_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * row_codes) +
                            128u * (a_chunk >> 2) + 16u * (a_chunk & 3);
-    // kRows: a thread takes whole blocks, unit u = tid + NT i is block u % 2 of row u / 2
+    // kRows: a thread takes whole blocks.  A wave has both blocks of 32 rows, two lanes a row,
+    // the even rows in its first half: eight lanes' writes then fall into eight different chunks.
     constexpr int UNITS = OP == MxOperands::kRows ? BN * 2 / NT : 1;
     static_assert(OP != MxOperands::kRows || BN * 2 % NT == 0, "whole units");
-    u32x4_t w_codes[UNITS];
-    uint32_t w_scale[UNITS];
+    auto unit_row = [&](int i) { return 32 * (wave + NW * i) + (lane & 30) + half; };
+    u32x4_t w_codes[2][UNITS];           // of two pipeline steps, by parity
+    uint32_t w_scale[2][UNITS];
     // kColumns: 8 rows x 4 columns of the step
     constexpr int GROUP_LANES = kColumns ? BN / 4 : 64;      // threads across the tile's columns
     static_assert(!kColumns || GROUP_LANES * 8 == NT, "one 8 x 4 unit per thread");
     const int t_rows = tid / GROUP_LANES, t_col = 4 * (tid % GROUP_LANES);
-    uint16_t t_codes[8];
-    uint32_t t_scale;
-    auto load_weights = [&](int t) {
+    uint16_t t_codes[2][8];
+    uint32_t t_scale[2];
+    auto load_weights = [&](int t, auto ic) {
+        constexpr int par = decltype(ic)::value;
         if constexpr (OP == MxOperands::kRows) {
-            const int blk = 2 * t + (tid & 1);
+            const int blk = 2 * t + (lane & 1);
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
-                const int r = (tid + NT * i) >> 1;
+                const int r = unit_row(i);
                 const int c = column_of(r);
                 // (a wave's units are 32 consecutive rows: one weight set)
                 const int s = __builtin_amdgcn_readfirstlane(set_of(r));
-                const uint32_t co = blk < blocks ? static_cast<uint32_t>(c * row_codes + 16 * (tid & 1)) : kOutside;
-                w_codes[i] = __builtin_bit_cast(
+                const uint32_t co = blk < blocks ? static_cast<uint32_t>(c * row_codes + 16 * (lane & 1)) : kOutside;
+                w_codes[par][i] = __builtin_bit_cast(
                     u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(s ? wr1 : wr0, co, 32 * t, 0));
                 const __amdgpu_buffer_rsrc_t sr =
                     mx_resource(p.w_scales[s] + static_cast<int64_t>(c0) * blocks, columns_left * blocks);
-                const uint32_t so = blk < blocks ? static_cast<uint32_t>(c * blocks + (tid & 1)) : kOutside;
-                w_scale[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so, 2 * t, 0);
+                const uint32_t so = blk < blocks ? static_cast<uint32_t>(c * blocks + (lane & 1)) : kOutside;
+                w_scale[par][i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so, 2 * t, 0);
             }
         }
         if constexpr (kColumns) {
-            const int set = t >= set_steps ? 1 : 0;
+            const int set = p.sets > 1 && t >= set_steps ? 1 : 0;
             const int64_t n = 64 * static_cast<int64_t>(t - set * set_steps);
             const __amdgpu_buffer_rsrc_t cr =
                 mx_resource(p.w[set] + n * row_codes + c0 / 2, (L - n) * row_codes - c0 / 2);
@@ -188,86 +190,86 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
                 mx_resource(p.w_scales[set] + n * blocks + c0 / kMxBlock, (L - n) * blocks - c0 / kMxBlock);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                t_codes[i] = __builtin_amdgcn_raw_buffer_load_b16(
+                t_codes[par][i] = __builtin_amdgcn_raw_buffer_load_b16(
                     cr, static_cast<uint32_t>((8 * t_rows + i) * row_codes + t_col / 2), 0, 0);
             // lane l of eight holds the scale of row l % 8; they are handed round below
-            t_scale = __builtin_amdgcn_raw_buffer_load_b8(
+            t_scale[par] = __builtin_amdgcn_raw_buffer_load_b8(
                 sr, static_cast<uint32_t>((8 * t_rows + (lane & 7)) * blocks + t_col / kMxBlock), 0, 0);
         }
     };
-    auto stash_weights = [&](auto ic) {
+    // decoding and staging, in four parts that the products of a step are spread over
+    uint32_t t_pairs[8][2];    // kColumns: rows, column pairs
+    auto stash_weights = [&](auto ic, auto qc) {
+        constexpr int q = decltype(qc)::value, par = decltype(ic)::value;
         uint8_t* dst = b_stage(ic);
         if constexpr (OP == MxOperands::kRows) {
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
-                const int r = (tid + NT * i) >> 1;
-                const float s = mx_scale(w_scale[i]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int c = (4 * (tid & 1) + q) ^ ((r >> 1) & 7);
-                    *reinterpret_cast<u32x4_t*>(dst + r * 128 + 16 * c) = mx_decode_word(w_codes[i][q], s);
-                }
+                const int r = unit_row(i);
+                const int c = (4 * (lane & 1) + q) ^ ((r >> 1) & 7);
+                *reinterpret_cast<u32x4_t*>(dst + r * 128 + 16 * c) = mx_decode_word(w_codes[par][i][q], mx_scale(w_scale[par][i]));
             }
         }
         if constexpr (kColumns) {
-            uint32_t v[8][2];    // rows, column pairs
             auto row = [&](auto rc) {
                 constexpr int i = decltype(rc)::value;
-                const float s = mx_scale(__builtin_amdgcn_ds_swizzle(static_cast<int>(t_scale), (i << 5) | 0x18));
-                v[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(t_codes[i], s, 0));
-                v[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(t_codes[i], s, 1));
+                const float s = mx_scale(__builtin_amdgcn_ds_swizzle(static_cast<int>(t_scale[par]), (i << 5) | 0x18));
+                t_pairs[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(t_codes[par][i], s, 0));
+                t_pairs[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(t_codes[par][i], s, 1));
             };
-            row(std::integral_constant<int, 0>{});
-            row(std::integral_constant<int, 1>{});
-            row(std::integral_constant<int, 2>{});
-            row(std::integral_constant<int, 3>{});
-            row(std::integral_constant<int, 4>{});
-            row(std::integral_constant<int, 5>{});
-            row(std::integral_constant<int, 6>{});
-            row(std::integral_constant<int, 7>{});
+            if constexpr (q < 2) {
+                row(std::integral_constant<int, 4 * (q & 1)>{});
+                row(std::integral_constant<int, 4 * (q & 1) + 1>{});
+                row(std::integral_constant<int, 4 * (q & 1) + 2>{});
+                row(std::integral_constant<int, 4 * (q & 1) + 3>{});
+            } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                u32x4_t out;
+                for (int k = 2 * (q & 1); k < 2 * (q & 1) + 2; ++k) {
+                    u32x4_t out;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    out[i] = __builtin_amdgcn_perm(v[2 * i + 1][k >> 1], v[2 * i][k >> 1],
-                                                   (k & 1) ? 0x07060302u : 0x05040100u);
-                const int r = t_col + k;
-                const int c = t_rows ^ (((r >> 1) ^ (r >> 4)) & 7);
-                *reinterpret_cast<u32x4_t*>(dst + r * 128 + 16 * c) = out;
+                    for (int i = 0; i < 4; ++i)
+                        out[i] = __builtin_amdgcn_perm(t_pairs[2 * i + 1][k >> 1], t_pairs[2 * i][k >> 1],
+                                                       (k & 1) ? 0x07060302u : 0x05040100u);
+                    const int r = t_col + k;
+                    const int c = t_rows ^ (((r >> 1) ^ (r >> 4)) & 7);
+                    *reinterpret_cast<u32x4_t*>(dst + r * 128 + 16 * c) = out;
+                }
             }
         }
     };
 
-    // ---- scales of both operands (kCodes): thread r < BM + BN keeps row r's next 16 bytes
-    static_assert(!kCodes || BM + BN <= NT, "one row of scales per thread");
+    // ---- scales of both operands (kCodes): thread r < BM + BN keeps row r's next 16 bytes, one
+    // load where rows are whole pieces of 16, a byte each elsewhere.  A byte past the row's last
+    // block is put to 0 (a finite scale: its codes are zeros).
+    static_assert(!kCodes || (BM + BN == NT && BM % 64 == 0), "one row of scales per thread, one operand per wave");
     u32x4_t s_next = {0, 0, 0, 0};
+    uint32_t s_bytes[!kCodes || WHOLE ? 1 : 16];
+    const bool s_left = kCodes && wave < BM / 64;
+    const int s_first = s_left ? m0 : c0;
+    const __amdgpu_buffer_rsrc_t s_rows =
+        mx_resource((s_left ? p.a_scales : p.w_scales[0]) + static_cast<int64_t>(s_first) * blocks,
+                    (static_cast<int64_t>(s_left ? p.M : p.N) - s_first) * blocks);
+    const uint32_t s_off = static_cast<uint32_t>((s_left ? tid : tid - BM) * blocks);
     auto load_scales = [&](int window) {
-        if constexpr (kCodes) {
-            const bool left = tid < BM;
-            const int r = left ? m0 + tid : c0 + tid - BM;
-            const int rows = left ? p.M : p.N;
-            const uint8_t* src = (left ? p.a_scales : p.w_scales[0]) + static_cast<int64_t>(r) * blocks + 16 * window;
-            s_next = u32x4_t{0, 0, 0, 0};
-            if (tid < BM + BN && r < rows) {
-                const int n = blocks - 16 * window;
+        if constexpr (kCodes && WHOLE) {
+            s_next = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     s_rows, 16 * window < blocks ? s_off : kOutside, 16 * window, 0));
+        } else if constexpr (kCodes) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t v = 0;
-                    if (4 * q + 4 <= n) {
-                        __builtin_memcpy(&v, src + 4 * q, 4);
-                    } else {
-                        for (int b = 0; b < n - 4 * q; ++b) v |= static_cast<uint32_t>(src[4 * q + b]) << (8 * b);
-                    }
-                    s_next[q] = v;
-                }
-            }
+            for (int e = 0; e < 16; ++e)
+                s_bytes[e] = __builtin_amdgcn_raw_buffer_load_b8(
+                    s_rows, 16 * window + e < blocks ? s_off : kOutside, 16 * window + e, 0);
         }
     };
     auto stash_scales = [&](int window) {
         if constexpr (kCodes) {
-            if (tid < BM + BN)
-                *reinterpret_cast<u32x4_t*>(sc + (window & 1) * (BM + BN) * 16 + tid * 16) = s_next;
+            if constexpr (!WHOLE) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    s_next[q] = s_bytes[4 * q] | s_bytes[4 * q + 1] << 8 | s_bytes[4 * q + 2] << 16 |
+                                s_bytes[4 * q + 3] << 24;
+            }
+            *reinterpret_cast<u32x4_t*>(sc + (window & 1) * (BM + BN) * 16 + tid * 16) = s_next;
         }
     };
 
@@ -283,92 +285,123 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     const int arow = wr * MI * 32 + (lane & 31), brow = wc * NI * 32 + (lane & 31);
     const int akey = (lane >> 1) & 7;
     const int bkey = kColumns ? (akey ^ ((lane >> 4) & 1)) : akey;
-    auto compute = [&](int t, auto ic) {
-        const uint8_t* as = a_stage(ic) + arow * 128;
-        const uint8_t* bs = b_stage(ic) + brow * 128;
-        uint32_t sa[MI], sb[NI];
+    // operands of two MFMA steps (by parity) and the scales of two pipeline steps; zeros at first, for
+    // the products that the first pipeline step makes of the step before it
+    u32x4_t af[2][MI], bf[2][NI];
+    uint32_t sa[2][MI], sb[2][NI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        af[1][i] = u32x4_t{0, 0, 0, 0};
+        sa[1][i] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        bf[1][i] = u32x4_t{0, 0, 0, 0};
+        sb[1][i] = 0;
+    }
+    auto read_scales = [&](int t, auto ic) {
         if constexpr (kCodes) {
+            constexpr int par = decltype(ic)::value;
             const uint8_t* s = sc + ((t >> 1) & 1) * (BM + BN) * 16 + 8 * half + 4 * (t & 1);
 #pragma unroll
-            for (int i = 0; i < MI; ++i) sa[i] = *reinterpret_cast<const uint32_t*>(s + (arow + 32 * i) * 16);
+            for (int i = 0; i < MI; ++i) sa[par][i] = *reinterpret_cast<const uint32_t*>(s + (arow + 32 * i) * 16);
 #pragma unroll
-            for (int j = 0; j < NI; ++j) sb[j] = *reinterpret_cast<const uint32_t*>(s + (BM + brow + 32 * j) * 16);
+            for (int j = 0; j < NI; ++j) sb[par][j] = *reinterpret_cast<const uint32_t*>(s + (BM + brow + 32 * j) * 16);
         }
-        auto sub = [&](auto jc) {
-            constexpr int j = decltype(jc)::value;
-            u32x4_t a[MI], b[NI];
+    };
+    auto read = [&](auto ic, auto jc) {
+        constexpr int j = decltype(jc)::value;
+        const uint8_t* as = a_stage(ic) + arow * 128;
+        const uint8_t* bs = b_stage(ic) + brow * 128;
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
-                a[i] = *reinterpret_cast<const u32x4_t*>(as + i * 4096 + 16 * ((4 * half + j) ^ akey));
+        for (int i = 0; i < MI; ++i)
+            af[j & 1][i] = *reinterpret_cast<const u32x4_t*>(as + i * 4096 + 16 * ((4 * half + j) ^ akey));
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                // row / 16 of block wc * NI + i: 2 (wc NI + i) + lane / 16 % 2
-                const int k = kColumns ? (bkey ^ ((2 * (wc * NI + i)) & 7)) : bkey;
-                b[i] = *reinterpret_cast<const u32x4_t*>(bs + i * 4096 + 16 * ((4 * half + j) ^ k));
+        for (int i = 0; i < NI; ++i) {
+            // row / 16 of block wc * NI + i: 2 (wc NI + i) + lane / 16 % 2
+            const int k = kColumns ? (bkey ^ ((2 * (wc * NI + i)) & 7)) : bkey;
+            bf[j & 1][i] = *reinterpret_cast<const u32x4_t*>(bs + i * 4096 + 16 * ((4 * half + j) ^ k));
+        }
+    };
+    auto multiply = [&](auto ic, auto jc) {
+        constexpr int j = decltype(jc)::value, par = decltype(ic)::value;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                if constexpr (kCodes)
+                    acc[i][k] = mx_mfma32<j>(bf[j & 1][k], sb[par][k], af[j & 1][i], sa[par][i], acc[i][k]);
+                else
+                    acc[i][k] = mfma32x32x16(__builtin_bit_cast(bf16x8_t, bf[j & 1][k]),
+                                             __builtin_bit_cast(bf16x8_t, af[j & 1][i]), acc[i][k]);
             }
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int k = 0; k < NI; ++k) {
-                    if constexpr (kCodes)
-                        acc[i][k] = mx_mfma32<j>(b[k], sb[k], a[i], sa[i], acc[i][k]);
-                    else
-                        acc[i][k] = mfma32x32x16(__builtin_bit_cast(bf16x8_t, b[k]), __builtin_bit_cast(bf16x8_t, a[i]),
-                                                 acc[i][k]);
-                }
-        };
-        sub(std::integral_constant<int, 0>{});
-        sub(std::integral_constant<int, 1>{});
-        sub(std::integral_constant<int, 2>{});
-        sub(std::integral_constant<int, 3>{});
     };
 
     // ---- pipeline: while step t is multiplied, step t + 1 goes to the other stage and the codes
-    // (scales) of the step (pair of steps) after it into registers
+    // (scales) of the step (pair of steps) after it into registers.  Nothing in a step is
+    // conditional: loads past the contraction's end read zeros, and what lies past a slice's end is
+    // staged and left.  (A branch after the products lets the compiler sink them past the next
+    // step's reads, at twice the registers.)
     auto stage_step = [&](int t, auto ic) {
         issue_left(t, ic);
         if constexpr (kCodes)
             issue_rows(wr0, b_off, row_codes, b_stage(ic), t, 0, std::integral_constant<int, B_LOADS>{});
     };
-    using Even = std::integral_constant<int, 0>;
-    using Odd = std::integral_constant<int, 1>;
-    if (t_begin < t_end) {
-        if constexpr (kCodes) {
-            load_scales(t_begin >> 1);
-            stash_scales(t_begin >> 1);
-        } else {
-            load_weights(t_begin);
-            stash_weights(Even{});
-            if (t_begin + 1 < t_end) load_weights(t_begin + 1);
-        }
-        stage_step(t_begin, Even{});
+    using Zero = std::integral_constant<int, 0>;
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using Three = std::integral_constant<int, 3>;
+    if constexpr (kCodes) {
+        load_scales(t_begin >> 1);
+        stash_scales(t_begin >> 1);
+    } else {
+        load_weights(t_begin, Zero{});
+        stash_weights(Zero{}, Zero{});
+        stash_weights(Zero{}, One{});
+        stash_weights(Zero{}, Two{});
+        stash_weights(Zero{}, Three{});
+        load_weights(t_begin + 1, One{});
     }
+    stage_step(t_begin, Zero{});
     auto step = [&](int t, auto ic, auto nc) {
         loads_done_barrier();
-        if constexpr (kCodes) {
-            // t is even exactly when ic is the even stage: slices start at a pair of steps
-            if constexpr (decltype(ic)::value == 0) {
-                if (t + 2 < t_end) load_scales((t >> 1) + 1);
-            }
-        }
-        if (t + 1 < t_end) {
-            stage_step(t + 1, nc);
-            if constexpr (!kCodes) {
-                stash_weights(nc);
-                if (t + 2 < t_end) load_weights(t + 2);
-            }
-        }
-        compute(t, ic);
-        if constexpr (kCodes && decltype(ic)::value == 1) {
-            if (t + 1 < t_end) stash_scales((t >> 1) + 1);
-        }
+        read_scales(t, ic);
+        read(ic, Zero{});
+        // every load of this step is issued here, a whole step before the wait for it
+        stage_step(t + 1, nc);
+        if constexpr (!kCodes)
+            load_weights(t + 2, ic);
+        else if constexpr (decltype(ic)::value == 0)
+            load_scales((t >> 1) + 1);
+        stash_weights(nc, Zero{});
+        multiply(nc, Three{});          // of step t - 1
+        __builtin_amdgcn_sched_barrier(0);
+        read(ic, One{});
+        stash_weights(nc, One{});
+        multiply(ic, Zero{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(ic, Two{});
+        stash_weights(nc, Two{});
+        multiply(ic, One{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(ic, Three{});
+        // t is even exactly when ic is the even stage: slices start at a pair of steps
+        if constexpr (kCodes && decltype(ic)::value == 1) stash_scales((t >> 1) + 1);
+        stash_weights(nc, Three{});
+        multiply(ic, Two{});
+        __builtin_amdgcn_sched_barrier(0);
     };
     int t = t_begin;
     for (; t + 2 <= t_end; t += 2) {
-        step(t, Even{}, Odd{});
-        step(t + 1, Odd{}, Even{});
+        step(t, Zero{}, One{});
+        step(t + 1, One{}, Zero{});
     }
-    if (t < t_end) step(t, Even{}, Odd{});
+    if (t < t_end) {
+        step(t, Zero{}, One{});
+        multiply(Zero{}, Three{});
+    } else {
+        multiply(One{}, Three{});
+    }
 
     // ---- epilogue.  Register r of a block: column 8 (r / 4) + 4 half + r % 4, row lane % 32.
     const int row0 = m0 + wr * MI * 32;
@@ -457,7 +490,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float g = acc[i][2 * j][4 * q + e];
-                        h[e] = g * sigmoid_f32(g) * acc[i][2 * j + 1][4 * q + e];
+                        h[e] = g * mx_sigmoid(g) * acc[i][2 * j + 1][4 * q + e];
                     }
                     put(j, q, pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]));
                 }
@@ -492,7 +525,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
                     for (int e = 0; e < 4; ++e) {
                         const float dh = bf16_bits_to_f32(static_cast<uint16_t>(d[e >> 1] >> (16 * (e & 1))));
                         const float g = acc[i][2 * j][4 * q + e], u = acc[i][2 * j + 1][4 * q + e];
-                        const float s = sigmoid_f32(g);
+                        const float s = mx_sigmoid(g);
                         acc[i][2 * j][4 * q + e] = dh * u * s * (1.f + g * (1.f - s));
                         acc[i][2 * j + 1][4 * q + e] = dh * g * s;
                     }
@@ -515,24 +548,41 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
 
 }  // namespace
 
-const MxTileShape kMxTiles[kNumMxTiles] = {{128, 128, 4}};
+const MxTileShape kMxTiles[kNumMxTiles] = {{128, 128, 4}, {256, 256, 8}};
 
-hipError_t launch_mx_tile(MxOperands op, MxEpilogue epi, int tile, const MxTileArgs& args, hipStream_t stream) {
-    const MxTileShape& s = kMxTiles[tile];
-    const int bc = epi == MxEpilogue::kStore ? s.bn : s.bn / 2;
-    const int tiles_m = (args.M + s.bm - 1) / s.bm, tiles_n = (args.N + bc - 1) / bc;
-    const dim3 grid(static_cast<uint32_t>(tiles_m) * tiles_n * args.split), block(64 * s.waves);
+namespace {
+
+template <int BM, int BN, int WR, int WC>
+hipError_t launch_shape(MxOperands op, MxEpilogue epi, const MxTileArgs& args, hipStream_t stream) {
+    const int bc = epi == MxEpilogue::kStore ? BN : BN / 2;
+    const int tiles_m = (args.M + BM - 1) / BM, tiles_n = (args.N + bc - 1) / bc;
+    const dim3 grid(static_cast<uint32_t>(tiles_m) * tiles_n * args.split), block(64 * WR * WC);
     auto run = [&](auto kernel) {
         W4A16_LAUNCH(kernel, grid, block, 0, stream, args, tiles_m, tiles_n);
         return hipGetLastError();
     };
     using O = MxOperands;
     using E = MxEpilogue;
-    if (op == O::kCodes) return run(mx_tile_kernel<O::kCodes, E::kStore, 128, 128, 2, 2>);
-    if (op == O::kColumns) return run(mx_tile_kernel<O::kColumns, E::kStore, 128, 128, 2, 2>);
-    if (epi == E::kGlu) return run(mx_tile_kernel<O::kRows, E::kGlu, 128, 128, 2, 2>);
-    if (epi == E::kGluGrad) return run(mx_tile_kernel<O::kRows, E::kGluGrad, 128, 128, 2, 2>);
-    return run(mx_tile_kernel<O::kRows, E::kStore, 128, 128, 2, 2>);
+    if (op == O::kCodes) {
+        const bool whole = args.L % 512 == 0 && ((reinterpret_cast<uintptr_t>(args.a_scales) |
+                                                  reinterpret_cast<uintptr_t>(args.w_scales[0])) & 15) == 0;
+        return whole ? run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, true>)
+                     : run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, false>);
+    }
+    if (op == O::kColumns) return run(mx_tile_kernel<O::kColumns, E::kStore, BM, BN, WR, WC, true>);
+    if (epi == E::kGlu) return run(mx_tile_kernel<O::kRows, E::kGlu, BM, BN, WR, WC, true>);
+    if (epi == E::kGluGrad) return run(mx_tile_kernel<O::kRows, E::kGluGrad, BM, BN, WR, WC, true>);
+    return run(mx_tile_kernel<O::kRows, E::kStore, BM, BN, WR, WC, true>);
+}
+
+}  // namespace
+
+hipError_t launch_mx_tile(MxOperands op, MxEpilogue epi, int tile, const MxTileArgs& args, hipStream_t stream) {
+    switch (tile) {
+        case 0: return launch_shape<128, 128, 2, 2>(op, epi, args, stream);
+        case 1: return launch_shape<256, 256, 2, 4>(op, epi, args, stream);
+        default: return hipErrorInvalidValue;
+    }
 }
 
 }  // namespace w4a16

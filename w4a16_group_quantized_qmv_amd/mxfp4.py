@@ -18,7 +18,7 @@ from . import _keep_for_stream, _raise_for, _stream_handle, _torch, Plan, load
 
 __all__ = [
     "MXFP4_BLOCK", "MXFP4_LINEAR", "MXFP4_LINEAR_BACKWARD", "MXFP4_QMM_A4", "MXFP4A4_LINEAR", "MXFP4_GATE_UP",
-    "MXFP4_GATE_UP_BACKWARD", "PATH_MXFP4", "mxfp4_plan", "mxfp4_quantize_rows", "mxfp4_dequantize_rows",
+    "MXFP4_GATE_UP_BACKWARD", "PATH_MXFP4", "PATH_MXFP4_QMV", "mxfp4_plan", "mxfp4_quantize_rows", "mxfp4_dequantize_rows",
     "mxfp4_linear", "mxfp4_linear_backward", "qmm_mxfp4a4", "mxfp4a4_linear", "mxfp4_gate_up_swiglu",
     "mxfp4_gate_up_swiglu_backward",
 ]
@@ -26,7 +26,7 @@ __all__ = [
 MXFP4_BLOCK = 32
 (MXFP4_LINEAR, MXFP4_LINEAR_BACKWARD, MXFP4_QMM_A4, MXFP4A4_LINEAR, MXFP4_GATE_UP,
  MXFP4_GATE_UP_BACKWARD) = range(6)
-PATH_MXFP4 = 8
+PATH_MXFP4, PATH_MXFP4_QMV = 8, 9
 
 
 def mxfp4_plan(op: int, M: int, N: int, K: int, split_k: int = 0, num_cus: int = 0) -> dict:
