@@ -482,8 +482,9 @@ int qmm_mxfp4a4(const uint8_t* xq, const uint8_t* xs, const uint8_t* codes, cons
 
 /*
  * One-call projection with 4-bit activations: mxfp4_quantize_rows of bf16 x into the start of
- * `workspace`, then qmm_mxfp4a4 with the rest of it for partials.  A missing workspace, or one
- * without room for the activations, returns W4A16_ERR_WORKSPACE.  Nothing routes here by itself:
+ * `workspace`, then qmm_mxfp4a4 with the rest of it for partials (the same results).  A missing
+ * workspace, or one without room for the activations, returns W4A16_ERR_WORKSPACE; up to 16 rows,
+ * without a forced split, one kernel quantizes on the way and no workspace is needed.  Nothing routes here by itself:
  * 4-bit activations are the caller's choice.
  */
 int mxfp4a4_linear(const uint16_t* x, const uint8_t* codes, const uint8_t* scales, uint16_t* y, int64_t M, int64_t N,

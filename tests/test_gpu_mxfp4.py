@@ -204,6 +204,77 @@ def test_linear_backward(lib, M, N, K, split):
     assert untouched()
 
 
+# many columns: the wide decode form, with ragged last blocks, and the 256 x 256 tiles
+WIDE_SIZES = [(1, 16400, 512), (3, 20007, 1536), (5, 16391, 1024), (16, 16384, 512)]
+LARGE_SIZES = [(520, 11000, 96), (300, 17001, 160), (257, 33000, 64)]
+
+
+@pytest.mark.parametrize("M,N,K", WIDE_SIZES)
+def test_many_columns_at_decode_rows(lib, M, N, K):
+    import torch
+    announce(f"mxfp4 wide decode M={M} N={N} K={K}")
+    rng = np.random.default_rng(M + N + K + 6)
+    w, wv = weight(rng, N, K)
+    x = bf16_values(rng.standard_normal((M, K)))
+    for op in (lib.MXFP4_LINEAR, lib.MXFP4_QMM_A4, lib.MXFP4A4_LINEAR):
+        p = lib.mxfp4_plan(op, M, N, K)
+        assert (p["path"], p["variant"]) == (lib.PATH_MXFP4_QMV, 0)
+    y, untouched = guarded(M, N, offset=1)
+    lib.mxfp4_linear(bf16(x), *w, y=y)
+    check(y, O.mx_linear(x, wv))
+    xq = lib.mxfp4_quantize_rows(bf16(x))
+    z = lib.qmm_mxfp4a4(*xq, *w)
+    check(z, O.mx_linear(O.mx_decode(*(t.cpu().numpy() for t in xq)), wv))
+    assert torch.equal(z, lib.mxfp4a4_linear(bf16(x), *w)) and untouched()
+    # scale rows that start at an odd address: the other form, the same products
+    odd = torch.cat([w[1].view(-1)[:1], w[1].view(-1)])[1:].view(w[1].shape)
+    check(lib.mxfp4_linear(bf16(x), w[0], odd), O.mx_linear(x, wv))
+    check(lib.qmm_mxfp4a4(*xq, w[0], odd), O.mx_linear(O.mx_decode(*(t.cpu().numpy() for t in xq)), wv))
+
+
+@pytest.mark.parametrize("M,N,K", LARGE_SIZES)
+def test_large_grids(lib, M, N, K):
+    announce(f"mxfp4 large grids M={M} N={N} K={K}")
+    rng = np.random.default_rng(M + N + K + 7)
+    assert lib.mxfp4_plan(lib.MXFP4_LINEAR, M, N, K)["tile_n"] == 256
+    w, wv = weight(rng, N, K)
+    x = bf16_values(rng.standard_normal((M, K)))
+    y, untouched = guarded(M, N)
+    check(lib.mxfp4_linear(bf16(x), *w, y=y), O.mx_linear(x, wv))
+    xq = lib.mxfp4_quantize_rows(bf16(x))
+    lib.qmm_mxfp4a4(*xq, *w, y=y)
+    check(y, O.mx_linear(O.mx_decode(*(t.cpu().numpy() for t in xq)), wv))
+    assert untouched()
+
+
+@pytest.mark.parametrize("M,N,K", [(1800, 72, 4800), (2000, 136, 4512)])
+def test_large_grids_backward(lib, M, N, K):
+    """The transposed product's 256 x 256 tiles: many rows and values, few weight rows."""
+    announce(f"mxfp4 large backward grids M={M} N={N} K={K}")
+    rng = np.random.default_rng(M + N + K + 8)
+    assert lib.mxfp4_plan(lib.MXFP4_LINEAR_BACKWARD, M, N, K)["tile_n"] == 256
+    w, wv = weight(rng, N, K)
+    dy = bf16_values(rng.standard_normal((M, N)))
+    dx, untouched = guarded(M, K)
+    check(lib.mxfp4_linear_backward(bf16(dy), *w, dx=dx), O.mx_linear_backward(dy, wv))
+    assert untouched()
+
+
+@pytest.mark.parametrize("M,N,K", [(520, 5600, 96), (600, 6001, 544)])
+def test_large_grids_gated(lib, M, N, K):
+    announce(f"mxfp4 large gated grids M={M} N={N} K={K}")
+    rng = np.random.default_rng(M + N + K + 9)
+    assert lib.mxfp4_plan(lib.MXFP4_GATE_UP, M, N, K)["tile_n"] == 128
+    x, gate, gv, up, uv = gated(rng, M, N, K)
+    h, untouched = guarded(M, N)
+    check(lib.mxfp4_gate_up_swiglu(bf16(x), gate, up, h=h), O.mx_gate_up(x, gv, uv))
+    dh = bf16_values(rng.standard_normal((M, N)))
+    got = lib.mxfp4_gate_up_swiglu_backward(bf16(x), gate, up, bf16(dh))
+    for g, expected in zip(got, O.mx_gate_up_backward(x, gv, uv, dh)):
+        check(g, expected)
+    assert untouched()
+
+
 def gated(rng, M, N, K):
     """Inputs whose gate values reach both ends of the sigmoid."""
     gate, gv = weight(rng, N, K, 118, 124)
@@ -454,6 +525,8 @@ def test_workspaces(lib):
         lib.mxfp4_linear(bf16(x), *w, split_k=4, workspace=short)
     with pytest.raises(ValueError, match="WORKSPACE"):
         lib.mxfp4a4_linear(bf16(x), *w, workspace=short)
+    few = bf16(x)[:3]                                      # decode rows need none
+    check(lib.mxfp4a4_linear(few, *w, workspace=short), O.mx_linear(O.mx_decode(*O.mx_encode(x[:3])), wv))
     with pytest.raises(ValueError, match="ALIGN"):
         lib.mxfp4_linear(bf16(x), *w, split_k=4, workspace=torch.empty(need // 4 + 1, device="cuda:0")[1:])
 

@@ -46,9 +46,15 @@ uint64_t padding_bytes(int32_t op, int64_t M, int64_t N) {
     if (!is_backward(op) || N % 8 == 0) return 0;
     return (op == MXFP4_GATE_UP_BACKWARD ? 2 : 1) * round256(static_cast<uint64_t>(M) * padded(N) * 2);
 }
+// The decode kernel serves the forward operators at up to 16 rows, unless a split is asked for; it
+// needs no workspace (4-bit activations are quantized on the way).
+bool decodes(int32_t op, int64_t M, int32_t split_k) {
+    return M <= kMxQmvRows && !is_backward(op) && split_k == 0;
+}
 // Workspace that an operator cannot do without (the rest is for partials).
-uint64_t fixed_bytes(int32_t op, int64_t M, int64_t N, int64_t K) {
-    return op == MXFP4A4_LINEAR ? activation_bytes(M, K) : padding_bytes(op, M, N);
+uint64_t fixed_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k) {
+    if (op == MXFP4A4_LINEAR) return decodes(op, M, split_k) ? 0 : activation_bytes(M, K);
+    return padding_bytes(op, M, N);
 }
 
 struct Product {
@@ -58,17 +64,18 @@ struct Product {
     int sets;            // weight sets
     int tile;
     int split;
-    bool decode = false; // the decode kernel
+    bool decode;         // the decode kernel
+    int cus;
 };
 
 // The product that an operator's last launch computes.
 Product product_of(int32_t op, int64_t M, int64_t N, int64_t K) {
     switch (op) {
-        case MXFP4_LINEAR: return {MxOperands::kRows, MxEpilogue::kStore, M, N, K, 1, 0, 1};
-        case MXFP4_LINEAR_BACKWARD: return {MxOperands::kColumns, MxEpilogue::kStore, M, K, N, 1, 0, 1};
-        case MXFP4_GATE_UP: return {MxOperands::kRows, MxEpilogue::kGlu, M, N, K, 2, 0, 1};
-        case MXFP4_GATE_UP_BACKWARD: return {MxOperands::kColumns, MxEpilogue::kStore, M, K, N, 2, 0, 1};
-        default: return {MxOperands::kCodes, MxEpilogue::kStore, M, N, K, 1, 0, 1};
+        case MXFP4_LINEAR: return {MxOperands::kRows, MxEpilogue::kStore, M, N, K, 1, 0, 1, false, 0};
+        case MXFP4_LINEAR_BACKWARD: return {MxOperands::kColumns, MxEpilogue::kStore, M, K, N, 1, 0, 1, false, 0};
+        case MXFP4_GATE_UP: return {MxOperands::kRows, MxEpilogue::kGlu, M, N, K, 2, 0, 1, false, 0};
+        case MXFP4_GATE_UP_BACKWARD: return {MxOperands::kColumns, MxEpilogue::kStore, M, K, N, 2, 0, 1, false, 0};
+        default: return {MxOperands::kCodes, MxEpilogue::kStore, M, N, K, 1, 0, 1, false, 0};
     }
 }
 
@@ -83,12 +90,7 @@ int64_t units_of(const Product& p) {
 }
 
 void choose(Product& p, int32_t split_k, int32_t cus) {
-    MxQmvShape q;
-    if (split_k == 0 && p.M <= kMxQmvRows &&
-        mx_qmv_shape(p.operands, p.sets, static_cast<int>(p.M), static_cast<int>(p.L), &q)) {
-        p.decode = true;
-        return;
-    }
+    if (p.decode) return;
     // 256 x 256 tiles where they reach half of the compute units
     p.tile = 1;
     if (2 * tiles_of(p) < cus) p.tile = 0;
@@ -118,6 +120,8 @@ int make_plan(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k, int3
         if (st != W4A16_OK) return st;
     }
     Product p = product_of(op, M, N, K);
+    p.decode = decodes(op, M, split_k);
+    p.cus = cus;
     choose(p, split_k, cus);
     if (tiles_of(p) * p.split >= kMaxGrid) return W4A16_ERR_SHAPE;
     const MxTileShape& s = kMxTiles[p.tile];
@@ -135,18 +139,18 @@ int make_plan(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k, int3
     out->variant = p.tile;
     if (p.decode) {
         MxQmvShape q;
-        mx_qmv_shape(p.operands, p.sets, static_cast<int>(p.M), static_cast<int>(p.L), &q);
+        mx_qmv_shape(p.operands, p.sets, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), cus, true, &q);
         out->path = W4A16_PATH_MXFP4_QMV;
         out->tile_m = q.rows;
         out->tile_n = q.columns;
         out->tile_k = kMxBlock;
-        out->grid_x = static_cast<int32_t>(ceil_div(p.N, q.columns));
+        out->grid_x = q.groups;
         out->grid_y = 1;
         out->block_threads = 64 * q.waves;
-        out->k_waves = q.waves;
-        out->variant = q.batch;
+        out->k_waves = q.wide ? 1 : q.waves;
+        out->variant = q.wide ? 0 : q.batch;
     }
-    out->workspace_bytes = fixed_bytes(op, M, N, K) + partial_bytes(p);
+    out->workspace_bytes = fixed_bytes(op, M, N, K, split_k) + partial_bytes(p);
     if (product) *product = p;
     return W4A16_OK;
 }
@@ -165,7 +169,7 @@ bool overlaps_codes(const void* y, uint64_t ny, const uint8_t* codes, const uint
 // forced one is an error; the operator's fixed part has to fit.
 int fit(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k, const void* workspace, size_t workspace_bytes,
         Product* p) {
-    const uint64_t used = fixed_bytes(op, M, N, K);
+    const uint64_t used = fixed_bytes(op, M, N, K, split_k);
     const bool usable = workspace && aligned(workspace, 16);
     const int missing = workspace && !usable ? W4A16_ERR_ALIGN : W4A16_ERR_WORKSPACE;
     if (used > 0 && (!usable || workspace_bytes < used)) return missing;
@@ -180,7 +184,7 @@ int fit(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k, const void
 }
 
 // Launch a fitted product and sum its slices; partials: the workspace after the fixed part.
-int run_product(const Product& p, MxTileArgs args, void* partials, hipStream_t stream) {
+int run_product(const Product& p, MxTileArgs args, void* partials, hipStream_t stream, bool quantize = false) {
     args.M = static_cast<int>(p.M);
     args.N = static_cast<int>(p.N);
     args.L = static_cast<int>(p.L);
@@ -188,7 +192,7 @@ int run_product(const Product& p, MxTileArgs args, void* partials, hipStream_t s
     args.split = p.split;
     args.ws = static_cast<float*>(partials);
     if (args.pitch == 0) args.pitch = p.operands == MxOperands::kCodes ? p.L / 2 : 2 * p.L;
-    if (p.decode) return to_status(launch_mx_qmv(p.operands, p.epilogue, args, stream));
+    if (p.decode) return to_status(launch_mx_qmv(p.operands, p.epilogue, quantize, args, p.cus, stream));
     hipError_t e = launch_mx_tile(p.operands, p.epilogue, p.tile, args, stream);
     if (e != hipSuccess || p.split == 1) return to_status(e);
     return to_status(p.epilogue == MxEpilogue::kGlu ? launch_splitk_reduce_glu(args.ws, args.y[0], p.M * p.N, p.split, stream)
@@ -232,7 +236,7 @@ int run_linear(int32_t op, const uint16_t* x, const uint8_t* codes, const uint8_
     args.w[0] = codes;
     args.w_scales[0] = scales;
     args.y[0] = y;
-    return run_product(p, args, after(workspace, fixed_bytes(op, M, N, K)), s);
+    return run_product(p, args, after(workspace, fixed_bytes(op, M, N, K, split_k)), s);
 }
 
 }  // namespace
@@ -320,16 +324,21 @@ int mxfp4a4_linear(const uint16_t* x, const uint8_t* codes, const uint8_t* scale
     st = fit(MXFP4A4_LINEAR, M, N, K, split_k, workspace, workspace_bytes, &p);
     if (st != W4A16_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
+    MxTileArgs args{};
+    args.w[0] = codes;
+    args.w_scales[0] = scales;
+    args.y[0] = y;
+    if (p.decode) {
+        args.a[0] = x;
+        args.pitch = 2 * K;
+        return run_product(p, args, nullptr, s, true);
+    }
     uint8_t* xq = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xq + round256(code_bytes(M, K));
     const hipError_t e = launch_mx_quantize(x, false, xq, xs, M * (K / kMxBlock), s);
     if (e != hipSuccess) return to_status(e);
-    MxTileArgs args{};
     args.a[0] = xq;
     args.a_scales = xs;
-    args.w[0] = codes;
-    args.w_scales[0] = scales;
-    args.y[0] = y;
     return run_product(p, args, after(workspace, activation_bytes(M, K)), s);
 }
 

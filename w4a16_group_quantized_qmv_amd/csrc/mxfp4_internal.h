@@ -51,16 +51,22 @@ extern const MxTileShape kMxTiles[kNumMxTiles];
 // Values of the contraction in one pipeline step.
 inline int mx_step(MxOperands op) { return op == MxOperands::kCodes ? 512 : 64; }
 
-// Decode rows: workgroups of `columns` weight rows whose `waves` waves take `share` units (1 KB of
-// codes) of the contraction each, `batch` of them in flight; `rows` activation row slots.
+// Decode rows (at most 16).  `groups` workgroups.  Wide form: eight waves of 16-column blocks.  Else
+// workgroups of `columns` weight rows whose `waves` waves take `share` units (1 KB of codes) of the
+// contraction each, `batch` of them in flight; `rows` activation row slots.  `lds` dynamic bytes.
+// whole: the scale rows start on 16 bytes (the wide form loads them so).
 constexpr int kMxQmvRows = 16;
 constexpr int kMxQmvWaves = 16;
+constexpr int kMxWideWaves = 8;
 struct MxQmvShape {
-    int rows, columns, waves, share, batch;
+    bool wide;
+    int groups, rows, columns, waves, share, batch;
     size_t lds;
 };
-bool mx_qmv_shape(MxOperands op, int sets, int M, int K, MxQmvShape* out);
-hipError_t launch_mx_qmv(MxOperands op, MxEpilogue epi, const MxTileArgs& args, hipStream_t stream);
+bool mx_qmv_shape(MxOperands op, int sets, int M, int N, int K, int cus, bool whole, MxQmvShape* out);
+// quantize (kCodes): the activations are bf16 rows, quantized on the way.
+hipError_t launch_mx_qmv(MxOperands op, MxEpilogue epi, bool quantize, const MxTileArgs& args, int cus,
+                         hipStream_t stream);
 
 hipError_t launch_mx_tile(MxOperands op, MxEpilogue epi, int tile, const MxTileArgs& args, hipStream_t stream);
 

@@ -22,6 +22,8 @@
 
 #include <algorithm>
 
+#include <type_traits>
+
 namespace w4a16 {
 namespace {
 
@@ -32,10 +34,48 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t qmv_resource(const void* base,
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(n), 0x00020000);
 }
 
+// Activations of the decode kernels.
+enum class MxX { kBf16, kCodes, kQuantize };   // as they are, MXFP4, or bf16 quantized to MXFP4 on the way
+
+// A lane's block of 32 bf16 values, in order, as an MXFP4 operand and its scale byte (the rule of
+// mx_quantize_kernel).
+__device__ __forceinline__ u32x4_t quantize_block(const u32x4_t (&v)[4], uint32_t& e) {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t top = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2_t, v[j][i] & 0x7FFF7FFFu));
+    const uint32_t field = static_cast<uint32_t>(max(top[0], top[1])) >> 7;
+    e = field == 255u ? 255u : (field > 2u ? field - 2u : 0u);
+    const float scale = mx_scale(e);
+    u32x4_t r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // (through locals: a vector element as the operand of a bit cast stands for element 0)
+        const uint32_t v0 = v[j][0], v1 = v[j][1], v2 = v[j][2], v3 = v[j][3];
+        uint32_t w = 0;
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, v0), scale, 0);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, v1), scale, 1);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, v2), scale, 2);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, v3), scale, 3);
+        r[j] = e == 255u ? 0u : w;
+    }
+    return r;
+}
+
+__device__ __forceinline__ f32x4_t mx_mfma16(const u32x4_t& a, uint32_t sa, const u32x4_t& b, uint32_t sb,
+                                             const f32x4_t& c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(a), mx_operand(b), c, 4, 4, 0,
+                                                            static_cast<int>(sa), 0, static_cast<int>(sb));
+}
+
 // ROWS: activation rows that an instance holds (1, 2, 4, 8 or 16); NP: weight sets; UB: units in flight.
-template <bool CODES, int ROWS, int NP, int UB>
+template <MxX X, int ROWS, int NP, int UB>
 __global__ __launch_bounds__(1024) void mx_qmv_kernel(const MxTileArgs p, int share) {
     constexpr int S = ROWS <= 4 ? 4 : 16 / ROWS, C = 16 / S;
+    constexpr bool CODES = X == MxX::kCodes;
     constexpr int XL = CODES ? 1 : (ROWS * S + 3) / 4;        // activation loads of a unit
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -97,10 +137,7 @@ __global__ __launch_bounds__(1024) void mx_qmv_kernel(const MxTileArgs p, int sh
         for (int i = 0; i < UB; ++i) {
             if constexpr (CODES) {
 #pragma unroll
-                for (int s = 0; s < NP; ++s)
-                    acc[s] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        mx_operand(codes[i][s]), mx_operand(xv[i][0]), acc[s], 4, 4, 0, static_cast<int>(scale[i][s]), 0,
-                        static_cast<int>(xscale[i]));
+                for (int s = 0; s < NP; ++s) acc[s] = mx_mfma16(codes[i][s], scale[i][s], xv[i][0], xscale[i], acc[s]);
             } else {
 #pragma unroll
                 for (int j = 0; j < XL; ++j) {
@@ -113,14 +150,22 @@ __global__ __launch_bounds__(1024) void mx_qmv_kernel(const MxTileArgs p, int sh
                 wave_lds_fence();
                 const int m = min(rc, ROWS - 1), col = slice * C + m;
                 const uint8_t* row = xs + (m * S + slice) * 256;
+                u32x4_t x[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(row + 16 * (((4 * q + j) ^ col) & 15));
+                for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const u32x4_t*>(row + 16 * (((4 * q + j) ^ col) & 15));
+                if constexpr (X == MxX::kQuantize) {
+                    uint32_t e;
+                    const u32x4_t xq = quantize_block(x, e);
 #pragma unroll
-                    for (int s = 0; s < NP; ++s)
-                        acc[s] = mfma16x16x32(
-                            __builtin_bit_cast(bf16x8_t, mx_decode_word(codes[i][s][j], mx_scale(scale[i][s]))),
-                            __builtin_bit_cast(bf16x8_t, x), acc[s]);
+                    for (int s = 0; s < NP; ++s) acc[s] = mx_mfma16(codes[i][s], scale[i][s], xq, e, acc[s]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int s = 0; s < NP; ++s)
+                            acc[s] = mfma16x16x32(
+                                __builtin_bit_cast(bf16x8_t, mx_decode_word(codes[i][s][j], mx_scale(scale[i][s]))),
+                                __builtin_bit_cast(bf16x8_t, x[j]), acc[s]);
                 }
                 if (i + 1 < UB || u0 + UB < u_end) wave_lds_fence();
             }
@@ -152,53 +197,220 @@ __global__ __launch_bounds__(1024) void mx_qmv_kernel(const MxTileArgs p, int sh
     }
 }
 
+// `into` with lanes 8 .. 15 (BANKS 0xC) or 0 .. 7 (0x3) of every sixteen replaced by the other eight
+// lanes of `from` (DPP row_ror:8).
+template <int BANKS>
+__device__ __forceinline__ uint32_t half_row_move(uint32_t into, uint32_t from) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(static_cast<int>(into), static_cast<int>(from), 0x128, 0xF, BANKS, false));
+}
+
+// The wide form: many columns (a vocabulary head).  A wave streams whole blocks of 16 columns, S = 1,
+// a window of 512 values (256 consecutive bytes of each column and its 16 scale bytes) at a time with
+// the next window in flight; the activations are staged once per workgroup, which takes blocks until
+// none is left.  A load takes 128 bytes of eight columns rather than 64 of sixteen: half lines
+// streamed past the cache measured 48.5 us against 41 on the 151936 x 2560 head, and 8 lane moves
+// per 2 KB put the blocks where the matrix instruction wants them.  K is a multiple of 512 and the scale rows are 16-byte aligned.
+template <MxX X>
+__global__ __launch_bounds__(64 * kMxWideWaves) void mx_qmv_wide_kernel(const MxTileArgs p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    const int blocks = p.L / kMxBlock, row_codes = blocks * 16, windows = blocks / 16;
+    const int first = (blockIdx.x * kMxWideWaves + wave), stride = gridDim.x * kMxWideWaves;
+    const int column_blocks = (p.N + 15) / 16;
+
+    // x in LDS.  kBf16: rows of 2 K bytes, 16-byte chunk c of row m at c ^ m (the low four bits).
+    // Else codes, rows of K / 2 bytes with chunk c at c ^ m, and then scale rows of K / 32 bytes.
+    const int rows = p.M;
+    const int x_pitch = X == MxX::kBf16 ? 2 * p.L : p.L / 2;
+    uint8_t* xs_scale = lds + rows * x_pitch;
+    if constexpr (X == MxX::kBf16) {
+        const int chunks = p.L / 8;
+        for (int t = threadIdx.x; t < rows * chunks; t += 64 * kMxWideWaves) {
+            const int m = t / chunks, c = t - m * chunks;
+            *reinterpret_cast<u32x4_t*>(lds + m * x_pitch + 16 * (c ^ m)) =
+                load16(static_cast<const uint8_t*>(p.a[0]) + m * p.pitch + 16 * c);
+        }
+    } else {
+        for (int t = threadIdx.x; t < rows * blocks; t += 64 * kMxWideWaves) {
+            const int m = t / blocks, c = t - m * blocks;
+            u32x4_t v;
+            uint32_t e;
+            if constexpr (X == MxX::kCodes) {
+                v = load16(static_cast<const uint8_t*>(p.a[0]) + m * p.pitch + 16 * c);
+                e = p.a_scales[m * blocks + c];
+            } else {
+                u32x4_t x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = load16(static_cast<const uint8_t*>(p.a[0]) + m * p.pitch + 64 * c + 16 * j);
+                v = quantize_block(x, e);
+            }
+            *reinterpret_cast<u32x4_t*>(lds + m * x_pitch + 16 * (c ^ m)) = v;
+            xs_scale[m * blocks + c] = static_cast<uint8_t>(e);
+        }
+    }
+    __syncthreads();
+
+    u32x4_t codes[2][4], scales[2];
+    auto load = [&](int block, int window, auto ic) {
+        constexpr int par = decltype(ic)::value;
+        const int64_t c0 = 16 * static_cast<int64_t>(block), left = block < column_blocks ? p.N - c0 : 0;
+        const __amdgpu_buffer_rsrc_t cr = qmv_resource(p.w[0] + c0 * row_codes, left * row_codes);
+        const __amdgpu_buffer_rsrc_t sr = qmv_resource(p.w_scales[0] + c0 * blocks, left * blocks);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            codes[par][i] = __builtin_bit_cast(
+                u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                             cr, ((r & 7) + 8 * (i & 1)) * row_codes + 16 * (q + 4 * (r >> 3) + 8 * (i >> 1)), 256 * window,
+                             kStreamedOnce));
+        scales[par] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(sr, r * blocks, 16 * window, 0));
+    };
+    const int m = min(r, rows - 1);
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    int block = first, window = 0;
+    auto next = [&](int& b, int& w) {
+        if (++w == windows) {
+            w = 0;
+            b += stride;
+        }
+    };
+    auto use = [&](int window, auto ic) {
+        constexpr int par = decltype(ic)::value;
+        // from whole lines to the operands: loads 2 h and 2 h + 1 hold blocks 8 h .. 8 h + 7 of columns
+        // 0 .. 7 and 8 .. 15, the operands blocks 8 h .. and 8 h + 4 .. of all sixteen
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const uint32_t low = codes[par][i][d], high = codes[par][i + 1][d];
+                codes[par][i][d] = half_row_move<0xC>(low, high);
+                codes[par][i + 1][d] = half_row_move<0x3>(high, low);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = 16 * window + 4 * i + q;               // this lane's block of the row
+            const uint32_t e = (scales[par][i] >> (8 * q)) & 0xFFu;
+            if constexpr (X == MxX::kBf16) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(lds + m * x_pitch + 16 * ((4 * b + j) ^ m));
+                    acc = mfma16x16x32(__builtin_bit_cast(bf16x8_t, mx_decode_word(codes[par][i][j], mx_scale(e))),
+                                       __builtin_bit_cast(bf16x8_t, x), acc);
+                }
+            } else {
+                const u32x4_t x = *reinterpret_cast<const u32x4_t*>(lds + m * x_pitch + 16 * (b ^ m));
+                acc = mx_mfma16(codes[par][i], e, x, xs_scale[m * blocks + b], acc);
+            }
+        }
+    };
+    auto finish = [&](int block) {
+        const int n = 16 * block + 4 * q;
+        if (r < rows && n < p.N) {
+            uint16_t* out = p.y[0] + static_cast<size_t>(r) * p.N + n;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < p.N) out[e] = f32_to_bf16_bits(acc[e]);
+        }
+        acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    };
+    using Even = std::integral_constant<int, 0>;
+    using Odd = std::integral_constant<int, 1>;
+    load(block, window, Even{});
+    auto turn = [&](auto ic, auto nc) {
+        int b = block, w = window;
+        next(b, w);
+        load(b, w, nc);
+        use(window, ic);
+        if (w == 0) finish(block);
+        block = b;
+        window = w;
+    };
+    while (block < column_blocks) {
+        turn(Even{}, Odd{});
+        if (block >= column_blocks) break;
+        turn(Odd{}, Even{});
+    }
+}
+
 }  // namespace
 
-bool mx_qmv_shape(MxOperands op, int sets, int M, int K, MxQmvShape* out) {
+bool mx_qmv_shape(MxOperands op, int sets, int M, int N, int K, int cus, bool whole, MxQmvShape* out) {
     if (M > kMxQmvRows || op == MxOperands::kColumns) return false;
     const bool codes = op == MxOperands::kCodes;
-    out->rows = M <= 1 && !codes ? 1 : M <= 2 && !codes ? 2 : M <= 4 ? 4 : M <= 8 ? 8 : 16;
+    // The wide form where its waves find several blocks each and the activations leave room for two
+    // workgroups per compute unit.
+    const size_t x_bytes = static_cast<size_t>(M) * (codes ? K / 2 + K / kMxBlock : 2 * K);
+    const int column_blocks = (N + 15) / 16;
+    out->wide = whole && sets == 1 && K % 512 == 0 && x_bytes <= 80 * 1024 && column_blocks >= 4 * cus;
+    if (out->wide) {
+        const int resident = std::min<int>(3, static_cast<int>(160 * 1024 / x_bytes));
+        out->groups = std::min((column_blocks + kMxWideWaves - 1) / kMxWideWaves, resident * cus);
+        out->rows = 16;
+        out->columns = 16;
+        out->waves = kMxWideWaves;
+        out->share = out->batch = 4;
+        out->lds = x_bytes;
+        return true;
+    }
+    out->rows = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : M <= 8 ? 8 : 16;
     const int S = out->rows <= 4 ? 4 : 16 / out->rows;
     out->columns = 16 / S;
+    out->groups = (N + out->columns - 1) / out->columns;
     const int units = (K / kMxBlock + 4 * S - 1) / (4 * S);
     out->share = (units + kMxQmvWaves - 1) / kMxQmvWaves;
     out->waves = (units + out->share - 1) / out->share;
-    out->batch = out->share == 1 ? 1 : out->share == 2 ? 2 : 4;
-    const size_t x = codes ? 0 : static_cast<size_t>(out->rows) * S * 256 * out->waves;
+    const int turns = (out->share + 3) / 4;
+    out->batch = (out->share + turns - 1) / turns;
+    const size_t x = static_cast<size_t>(out->rows) * S * 256 * out->waves;
     const size_t sums = static_cast<size_t>(sets) * out->waves * S * out->columns * out->columns * sizeof(float);
     out->lds = std::max(x, sums);
     return true;
 }
 
-hipError_t launch_mx_qmv(MxOperands op, MxEpilogue epi, const MxTileArgs& args, hipStream_t stream) {
+hipError_t launch_mx_qmv(MxOperands op, MxEpilogue epi, bool quantize, const MxTileArgs& args, int cus,
+                         hipStream_t stream) {
     MxQmvShape s;
     const int sets = epi == MxEpilogue::kGlu ? 2 : 1;
-    if (!mx_qmv_shape(op, sets, args.M, args.L, &s)) return hipErrorInvalidValue;
-    const dim3 grid((args.N + s.columns - 1) / s.columns), block(64 * s.waves);
+    const bool whole = (reinterpret_cast<uintptr_t>(args.w_scales[0]) & 15) == 0;
+    if (!mx_qmv_shape(op, sets, args.M, args.N, args.L, cus, whole, &s)) return hipErrorInvalidValue;
+    const dim3 grid(s.groups), block(64 * s.waves);
     auto run = [&](auto kernel) {
         W4A16_LAUNCH(kernel, grid, block, s.lds, stream, args, s.share);
         return hipGetLastError();
     };
     auto batched = [&](auto cc, auto rc, auto nc) {
-        constexpr bool codes = decltype(cc)::value;
+        constexpr MxX x = decltype(cc)::value;
         constexpr int rows = decltype(rc)::value, np = decltype(nc)::value;
-        if (s.batch == 1) return run(mx_qmv_kernel<codes, rows, np, 1>);
-        if (s.batch == 2) return run(mx_qmv_kernel<codes, rows, np, 2>);
-        return run(mx_qmv_kernel<codes, rows, np, 4>);
+        if (s.batch == 1) return run(mx_qmv_kernel<x, rows, np, 1>);
+        if (s.batch == 2) return run(mx_qmv_kernel<x, rows, np, 2>);
+        if (s.batch == 3) return run(mx_qmv_kernel<x, rows, np, 3>);
+        return run(mx_qmv_kernel<x, rows, np, 4>);
     };
     auto sized = [&](auto cc, auto nc) {
-        if constexpr (!decltype(cc)::value) {
+        if constexpr (decltype(cc)::value != MxX::kCodes) {
             if (s.rows == 1) return batched(cc, std::integral_constant<int, 1>{}, nc);
             if (s.rows == 2) return batched(cc, std::integral_constant<int, 2>{}, nc);
         }
-        if (s.rows == 4) return batched(cc, std::integral_constant<int, 4>{}, nc);
+        if (s.rows <= 4) return batched(cc, std::integral_constant<int, 4>{}, nc);
         if (s.rows == 8) return batched(cc, std::integral_constant<int, 8>{}, nc);
         return batched(cc, std::integral_constant<int, 16>{}, nc);
     };
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
-    if (op == MxOperands::kCodes) return sized(std::true_type{}, One{});
-    return sets == 2 ? sized(std::false_type{}, Two{}) : sized(std::false_type{}, One{});
+    using Bf16 = std::integral_constant<MxX, MxX::kBf16>;
+    using Codes = std::integral_constant<MxX, MxX::kCodes>;
+    using Quantize = std::integral_constant<MxX, MxX::kQuantize>;
+    if (s.wide) {
+        auto wide = [&](auto kernel) {
+            W4A16_LAUNCH(kernel, dim3(s.groups), dim3(64 * kMxWideWaves), s.lds, stream, args);
+            return hipGetLastError();
+        };
+        if (op == MxOperands::kRows) return wide(mx_qmv_wide_kernel<MxX::kBf16>);
+        return quantize ? wide(mx_qmv_wide_kernel<MxX::kQuantize>) : wide(mx_qmv_wide_kernel<MxX::kCodes>);
+    }
+    if (op == MxOperands::kCodes) return quantize ? sized(Quantize{}, One{}) : sized(Codes{}, One{});
+    return sets == 2 ? sized(Bf16{}, Two{}) : sized(Bf16{}, One{});
 }
 
 }  // namespace w4a16

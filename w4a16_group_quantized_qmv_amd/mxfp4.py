@@ -42,9 +42,29 @@ def _workspace_bytes(op, M, N, K, split_k, device):
     return int(mxfp4_plan(op, M, N, K, split_k)["workspace_bytes"])
 
 
-def _tensor(t, name, dtype, shape, device=None):
+@functools.lru_cache(maxsize=None)
+def _bound():
+    """What every call needs, looked up once: torch, its stream query, and the library's functions."""
+    import types
     torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    lib = load()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        def raw(index):
+            return torch.cuda.current_stream(index).cuda_stream
+    return types.SimpleNamespace(torch=torch, tensor=torch.Tensor, bf16=torch.bfloat16, fp32=torch.float32,
+                                 u8=torch.uint8, empty=torch.empty, stream=raw,
+                                 current_device=torch.cuda.current_device,
+                                 fn={n: getattr(lib, n) for n in __all__ if hasattr(lib, n)})
+
+
+def _tensor(t, name, dtype, shape, device=None):
+    """Checks a tensor; every condition in one expression for the calls that are right."""
+    b = _bound()
+    if (isinstance(t, b.tensor) and t.dtype == dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return
+    if not isinstance(t, b.tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -54,39 +74,38 @@ def _tensor(t, name, dtype, shape, device=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, not {device}")
+    raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, not {device}")
 
 
 def _matrix(t, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _bound().tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {t.dim()} dimensions")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {len(shape)} dimensions")
+    return shape
 
 
 def _weights(pair, name, device, like=None):
     """Checks a (codes, scales) pair; returns (N, K)."""
-    torch = _torch()
     codes, scales = pair
-    N, half = _matrix(codes, f"{name} codes")
+    N, half = _matrix(codes, name)
     K = 2 * half
     if K == 0 or K % MXFP4_BLOCK:
         raise ValueError(f"{name}: K={K} must be a positive multiple of {MXFP4_BLOCK}")
     if like is not None and (N, K) != like:
         raise ValueError(f"{name} must be [{like[0]}, {like[1]}], got [{N}, {K}]")
-    _tensor(codes, f"{name} codes", torch.uint8, (N, half), device)
-    _tensor(scales, f"{name} scales", torch.uint8, (N, K // MXFP4_BLOCK), device)
+    u8 = _bound().u8
+    _tensor(codes, name, u8, (N, half), device)
+    _tensor(scales, name, u8, (N, K // MXFP4_BLOCK), device)
     return N, K
 
 
 def _output(t, name, shape, device, dtype=None):
-    torch = _torch()
-    dtype = dtype or torch.bfloat16
+    b = _bound()
+    dtype = dtype or b.bf16
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return b.empty(shape, dtype=dtype, device=device)
     _tensor(t, name, dtype, shape, device)
     return t
 
@@ -94,55 +113,59 @@ def _output(t, name, shape, device, dtype=None):
 def _call(name, op, dims, device, stream, workspace, own, args, split_k=0):
     """One C-ABI call on ``device``: its workspace (allocated where the caller gave none), the stream,
     the status.  ``own``: tensors allocated for this call."""
-    torch = _torch()
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
+    b = _bound()
+    index = device.index
+    if index != b.current_device():
+        with b.torch.cuda.device(device):
             return _call(name, op, dims, device, stream, workspace, own, args, split_k)
-    tail = ()
     if op is not None:
         if split_k < 0:
             raise ValueError(f"split_k={split_k} must not be negative")
-        need = _workspace_bytes(op, *dims, split_k, device.index)
-        ws, nbytes = None, 0
-        if need:
+        need = _workspace_bytes(op, *dims, split_k, index)
+        if not need:
+            args += (*dims, split_k, None, 0)
+        else:
             if workspace is None:
-                ws = torch.empty(need, dtype=torch.uint8, device=device)
-                own = (*own, ws)
-            else:
-                ws = workspace
-                if not ws.is_cuda or not ws.is_contiguous() or ws.device != device:
-                    raise ValueError(f"workspace must be a contiguous tensor on {device}")
-            nbytes = ws.numel() * ws.element_size()
-        tail = (split_k, None if ws is None else ws.data_ptr(), nbytes)
+                workspace = b.empty(need, dtype=b.u8, device=device)
+                own = (*own, workspace)
+            elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != device:
+                raise ValueError(f"workspace must be a contiguous tensor on {device}")
+            args += (*dims, split_k, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    else:
+        args += dims
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = b.stream(index)
     else:
         handle = _stream_handle(stream)
         _keep_for_stream(stream, device, *own)
-    _raise_for(getattr(load(), name)(*args, *dims, *tail, handle), name)
+    status = b.fn[name](*args, handle)
+    if status:
+        _raise_for(status, name)
 
 
 def mxfp4_quantize_rows(x, codes=None, scales=None, stream=None):
     """MXFP4 codes and scales of the rows of ``x`` (bf16 or fp32 ``[R, K]``); returns
     ``(codes, scales)``.  A block holding an infinity or a NaN decodes to NaN."""
-    torch = _torch()
+    b = _bound()
     R, K = _matrix(x, "x")
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    if x.dtype != b.bf16 and x.dtype != b.fp32:
         raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
     if K == 0 or K % MXFP4_BLOCK:
         raise ValueError(f"K={K} must be a positive multiple of {MXFP4_BLOCK}")
     _tensor(x, "x", x.dtype, (R, K))
-    own = [t is None for t in (codes, scales)]
-    codes = _output(codes, "codes", (R, K // 2), x.device, torch.uint8)
-    scales = _output(scales, "scales", (R, K // MXFP4_BLOCK), x.device, torch.uint8)
-    _call("mxfp4_quantize_rows", None, (R, K), x.device, stream, None,
-          tuple(t for t, o in zip((codes, scales), own) if o),
-          (x.data_ptr(), int(x.dtype == torch.float32), codes.data_ptr(), scales.data_ptr()))
+    device = x.device
+    given = (codes, scales)
+    codes = _output(codes, "codes", (R, K // 2), device, b.u8)
+    scales = _output(scales, "scales", (R, K // MXFP4_BLOCK), device, b.u8)
+    _call("mxfp4_quantize_rows", None, (R, K), device, stream, None,
+          [t for t, g in zip((codes, scales), given) if g is None] if stream is not None else (),
+          (x.data_ptr(), int(x.dtype == b.fp32), codes.data_ptr(), scales.data_ptr()))
     return codes, scales
 
 
 def mxfp4_dequantize_rows(codes, scales, y=None, stream=None):
     """The values of MXFP4 rows as bf16 ``[R, K]`` (exact); returns y."""
+    _matrix(codes, "codes")
     device = codes.device
     R, K = _weights((codes, scales), "rows", device)
     own = y is None
@@ -153,12 +176,11 @@ def mxfp4_dequantize_rows(codes, scales, y=None, stream=None):
 
 
 def _projection(name, op, x, codes, scales, y, split_k, workspace, stream):
-    torch = _torch()
-    M, columns = _matrix(x, "x")
+    M, _ = _matrix(x, "x")
     device = x.device
     N, K = _weights((codes, scales), "weight", device)
     back = op == MXFP4_LINEAR_BACKWARD
-    _tensor(x, "dy" if back else "x", torch.bfloat16, (M, N if back else K))
+    _tensor(x, "dy" if back else "x", _bound().bf16, (M, N if back else K))
     own = y is None
     y = _output(y, "dx" if back else "y", (M, K if back else N), device)
     _call(name, op, (M, N, K), device, stream, workspace, (y,) if own else (),
@@ -185,9 +207,9 @@ def mxfp4a4_linear(x, codes, scales, y=None, split_k: int = 0, workspace=None, s
 
 def qmm_mxfp4a4(xq, xs, codes, scales, y=None, split_k: int = 0, workspace=None, stream=None):
     """``y = X . W^T`` of two MXFP4 operands (``xq``, ``xs`` from ``mxfp4_quantize_rows``)."""
+    M, _ = _matrix(xq, "xq")
     device = xq.device
     N, K = _weights((codes, scales), "weight", device)
-    M, _ = _matrix(xq, "xq")
     _weights((xq, xs), "x", device, (M, K))
     own = y is None
     y = _output(y, "y", (M, N), device)
@@ -199,12 +221,11 @@ def qmm_mxfp4a4(xq, xs, codes, scales, y=None, split_k: int = 0, workspace=None,
 def mxfp4_gate_up_swiglu(x, gate, up, h=None, split_k: int = 0, workspace=None, stream=None):
     """``h = silu(x . Wg^T) * (x . Wu^T)`` in one kernel; ``gate`` and ``up`` are ``(codes, scales)``
     pairs of one shape.  Returns h."""
-    torch = _torch()
     M, _ = _matrix(x, "x")
     device = x.device
     N, K = _weights(gate, "gate", device)
     _weights(up, "up", device, (N, K))
-    _tensor(x, "x", torch.bfloat16, (M, K))
+    _tensor(x, "x", _bound().bf16, (M, K))
     own = h is None
     h = _output(h, "h", (M, N), device)
     _call("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), device, stream, workspace, (h,) if own else (),
@@ -217,13 +238,12 @@ def mxfp4_gate_up_swiglu_backward(x, gate, up, dh, dx=None, dgate=None, dup=None
                                   stream=None):
     """Backward pass of ``mxfp4_gate_up_swiglu`` from ``x`` and ``dh``; returns ``(dx, dgate, dup)``,
     the last two the gradients of both projections' outputs.  The weights are frozen."""
-    torch = _torch()
     M, _ = _matrix(x, "x")
     device = x.device
     N, K = _weights(gate, "gate", device)
     _weights(up, "up", device, (N, K))
-    _tensor(x, "x", torch.bfloat16, (M, K))
-    _tensor(dh, "dh", torch.bfloat16, (M, N), device)
+    _tensor(x, "x", _bound().bf16, (M, K))
+    _tensor(dh, "dh", _bound().bf16, (M, N), device)
     own = [t is None for t in (dx, dgate, dup)]
     dx = _output(dx, "dx", (M, K), device)
     dgate = _output(dgate, "dgate", (M, N), device)
