@@ -413,7 +413,7 @@ int w4a8_linear(const uint16_t* x, const uint32_t* wq, const uint16_t* scales, c
  *
  * A decoded weight is one of the 16 values times a power of two and is exact in bf16; scale bytes
  * 253 and 254, which no quantizer of finite values below produces, can exceed bf16's range and then
- * stand for infinities.  All sums are fp32, rounded to bf16 once.
+ * are not defined in the products.  All sums are fp32, rounded to bf16 once.
  */
 enum mxfp4_type { MXFP4_BF16 = 0, MXFP4_FP32 = 1 };
 

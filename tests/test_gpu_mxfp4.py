@@ -147,7 +147,7 @@ def test_dequantize_every_code_and_scale(lib):
 # tails of a half and of a whole step, and shapes with a policy split
 SIZES = [(1, 1, 32), (1, 7, 64), (2, 33, 96), (3, 130, 160), (5, 100, 544), (8, 257, 512), (9, 64, 1120),
          (16, 300, 416), (17, 129, 1056), (31, 72, 2560), (33, 500, 288), (64, 64, 64), (127, 130, 608),
-         (129, 127, 320), (130, 1000, 416), (300, 264, 736), (1, 2560, 9728), (4, 1024, 2560)]
+         (129, 127, 320), (130, 1000, 416), (300, 264, 736), (109, 1485, 2592), (35, 112, 1312), (1, 2560, 9728), (4, 1024, 2560)]
 BACK_SIZES = SIZES[:-2] + [(1, 1000, 2560), (130, 1003, 416)]
 
 
@@ -204,9 +204,11 @@ def test_linear_backward(lib, M, N, K, split):
     assert untouched()
 
 
-# many columns: the wide decode form, with ragged last blocks, and the 256 x 256 tiles
+# many columns: the wide decode form, with ragged last blocks, and the grids of the large tiles
 WIDE_SIZES = [(1, 16400, 512), (3, 20007, 1536), (5, 16391, 1024), (16, 16384, 512)]
-LARGE_SIZES = [(520, 11000, 96), (300, 17001, 160), (257, 33000, 64)]
+LARGE_SIZES = [(773, 13176, 96), (522, 13265, 96), (961, 10881, 544), (300, 17001, 160)]
+LARGE_BACK_SIZES = [(2323, 72, 4928), (1298, 72, 5952), (321, 75, 5408)]
+LARGE_GATED_SIZES = [(390, 11227, 96), (257, 10998, 96), (2325, 72, 4896), (1422, 75, 5408), (201, 2000, 1376)]
 
 
 @pytest.mark.parametrize("M,N,K", WIDE_SIZES)
@@ -236,7 +238,6 @@ def test_many_columns_at_decode_rows(lib, M, N, K):
 def test_large_grids(lib, M, N, K):
     announce(f"mxfp4 large grids M={M} N={N} K={K}")
     rng = np.random.default_rng(M + N + K + 7)
-    assert lib.mxfp4_plan(lib.MXFP4_LINEAR, M, N, K)["tile_n"] == 256
     w, wv = weight(rng, N, K)
     x = bf16_values(rng.standard_normal((M, K)))
     y, untouched = guarded(M, N)
@@ -247,12 +248,10 @@ def test_large_grids(lib, M, N, K):
     assert untouched()
 
 
-@pytest.mark.parametrize("M,N,K", [(1800, 72, 4800), (2000, 136, 4512)])
+@pytest.mark.parametrize("M,N,K", LARGE_BACK_SIZES)
 def test_large_grids_backward(lib, M, N, K):
-    """The transposed product's 256 x 256 tiles: many rows and values, few weight rows."""
     announce(f"mxfp4 large backward grids M={M} N={N} K={K}")
     rng = np.random.default_rng(M + N + K + 8)
-    assert lib.mxfp4_plan(lib.MXFP4_LINEAR_BACKWARD, M, N, K)["tile_n"] == 256
     w, wv = weight(rng, N, K)
     dy = bf16_values(rng.standard_normal((M, N)))
     dx, untouched = guarded(M, K)
@@ -260,11 +259,10 @@ def test_large_grids_backward(lib, M, N, K):
     assert untouched()
 
 
-@pytest.mark.parametrize("M,N,K", [(520, 5600, 96), (600, 6001, 544)])
+@pytest.mark.parametrize("M,N,K", LARGE_GATED_SIZES)
 def test_large_grids_gated(lib, M, N, K):
     announce(f"mxfp4 large gated grids M={M} N={N} K={K}")
     rng = np.random.default_rng(M + N + K + 9)
-    assert lib.mxfp4_plan(lib.MXFP4_GATE_UP, M, N, K)["tile_n"] == 128
     x, gate, gv, up, uv = gated(rng, M, N, K)
     h, untouched = guarded(M, N)
     check(lib.mxfp4_gate_up_swiglu(bf16(x), gate, up, h=h), O.mx_gate_up(x, gv, uv))
@@ -273,6 +271,18 @@ def test_large_grids_gated(lib, M, N, K):
     for g, expected in zip(got, O.mx_gate_up_backward(x, gv, uv, dh)):
         check(g, expected)
     assert untouched()
+
+
+@pytest.mark.parametrize("op,sizes", [
+    ("MXFP4_LINEAR", "SIZES LARGE_SIZES"), ("MXFP4_QMM_A4", "SIZES LARGE_SIZES"),
+    ("MXFP4_GATE_UP", "SIZES LARGE_GATED_SIZES"), ("MXFP4_LINEAR_BACKWARD", "BACK_SIZES LARGE_BACK_SIZES"),
+    ("MXFP4_GATE_UP_BACKWARD", "BACK_SIZES LARGE_GATED_SIZES")])
+def test_sizes_reach_every_tile(lib, op, sizes):
+    """The size lists above cover the four tile shapes, split and not, of every operator's policy."""
+    plans = [lib.mxfp4_plan(getattr(lib, op), *s) for name in sizes.split() for s in globals()[name]]
+    tiles = {p["variant"] for p in plans if p["path"] == lib.PATH_MXFP4}
+    splits = {p["split_k"] > 1 for p in plans if p["path"] == lib.PATH_MXFP4}
+    assert tiles == {0, 1, 2, 3} and splits == {False, True}, (tiles, splits)
 
 
 def gated(rng, M, N, K):

@@ -16,6 +16,9 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, uin
 // Rows of N bf16 values as rows of ceil(N / 8) * 8, the rest zeros.
 hipError_t launch_mx_pad_rows(const uint16_t* x, uint16_t* y, int64_t M, int N, hipStream_t stream);
 
+// Sums of split-K partials [sets][split][MN], in slice order: y = bf16(sum), or silu(sum) * sum of two.
+hipError_t launch_mx_sum(const float* ws, uint16_t* y, int sets, int64_t MN, int split, hipStream_t stream);
+
 // What a tile multiplies.
 enum class MxOperands {
     kCodes,     // MXFP4 rows by MXFP4 rows, on the scaled matrix cores
@@ -46,10 +49,12 @@ struct MxTileArgs {
 struct MxTileShape {
     int bm, bn, waves;         // rows and weight rows of a workgroup's tile
 };
-constexpr int kNumMxTiles = 2;
+constexpr int kNumMxTiles = 4;
 extern const MxTileShape kMxTiles[kNumMxTiles];
-// Values of the contraction in one pipeline step.
-inline int mx_step(MxOperands op) { return op == MxOperands::kCodes ? 512 : 64; }
+// Values of the contraction in one pipeline step, and in the unit that split-K distributes (a pair of
+// steps where two steps' weights or scales are loaded together).
+inline int mx_step(MxOperands op) { return op == MxOperands::kCodes ? 256 : 64; }
+inline int mx_unit(MxOperands op) { return op == MxOperands::kCodes ? 512 : op == MxOperands::kRows ? 128 : 64; }
 
 // Decode rows (at most 16).  `groups` workgroups.  Wide form: eight waves of 16-column blocks.  Else
 // workgroups of `columns` weight rows whose `waves` waves take `share` units (1 KB of codes) of the

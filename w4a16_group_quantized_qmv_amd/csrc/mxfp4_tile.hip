@@ -43,15 +43,18 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_resource(const void* base, 
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(n), 0x00020000);
 }
 
-// All of this wave's loads have arrived and all waves are here.
+// All but the last PENDING loads of this wave have arrived, its LDS accesses are done, and all waves
+// are here.
+template <int PENDING>
 __device__ __forceinline__ void loads_done_barrier() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    static_assert(PENDING <= 63, "the counter of outstanding loads has six bits");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PENDING) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
-// WHOLE (kCodes): rows of scales are whole, aligned pieces of 16 bytes.
-template <MxOperands OP, MxEpilogue EPI, int BM, int BN, int WR, int WC, bool WHOLE>
+// WHOLE: the rows of scales are whole, aligned pieces of 16 bytes (kCodes) or of 4 (kRows).
+template <MxOperands OP, MxEpilogue EPI, int BM, int BN, int WR, int WC, int STAGES, bool WHOLE>
 __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs p, int tiles_m, int tiles_n) {
     constexpr int NW = WR * WC, NT = 64 * NW;
     constexpr int MI = BM / WR / 32, NI = BN / WC / 32;      // 32 x 32 blocks of a wave
@@ -61,14 +64,33 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     static_assert(!kPair || (NI % 2 == 0 && !kColumns), "both weight sets of an element in one wave");
     constexpr int BC = kPair ? BN / 2 : BN;                  // output columns of the tile
 
-    // one object per stage, so that a direct load into one is not taken for an input of reads of the other
+    // one object per stage, so that a direct load into one is not taken for an input of reads of the others
+    static_assert(STAGES == 2 || STAGES == 4, "a pair of steps has one parity of stages");
+    constexpr bool kDeep = STAGES == 4;
     __shared__ __attribute__((aligned(16))) uint8_t a0[BM * 128];
     __shared__ __attribute__((aligned(16))) uint8_t a1[BM * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t a2[kDeep ? BM * 128 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t a3[kDeep ? BM * 128 : 16];
     __shared__ __attribute__((aligned(16))) uint8_t b0[BN * 128];
     __shared__ __attribute__((aligned(16))) uint8_t b1[BN * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t sc[kCodes ? 2 * (BM + BN) * 16 : 16];
-    auto a_stage = [&](auto ic) -> uint8_t* { if constexpr (decltype(ic)::value == 0) return a0; else return a1; };
-    auto b_stage = [&](auto ic) -> uint8_t* { if constexpr (decltype(ic)::value == 0) return b0; else return b1; };
+    __shared__ __attribute__((aligned(16))) uint8_t b2[kDeep && kCodes ? BN * 128 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t b3[kDeep && kCodes ? BN * 128 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t sc[kCodes ? 2 * NT * 16 : 16];
+    auto a_stage = [&](auto ic) -> uint8_t* {
+        constexpr int i = decltype(ic)::value % STAGES;
+        if constexpr (i == 0) return a0;
+        else if constexpr (i == 1) return a1;
+        else if constexpr (i == 2) return a2;
+        else return a3;
+    };
+    // decoded weights are staged one step ahead: two stages
+    auto b_stage = [&](auto ic) -> uint8_t* {
+        constexpr int i = decltype(ic)::value % (kCodes ? STAGES : 2);
+        if constexpr (i == 0) return b0;
+        else if constexpr (i == 1) return b1;
+        else if constexpr (i == 2) return b2;
+        else return b3;
+    };
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -96,9 +118,11 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
         t_begin = 2 * w0;
         t_end = 2 * w1 - (w1 == windows && rest > 0 && rest <= 4 ? 1 : 0);
     } else {
-        const int steps = kColumns ? set_steps * p.sets : set_steps;
-        t_begin = static_cast<int>(static_cast<int64_t>(z) * steps / p.split);
-        t_end = static_cast<int>(static_cast<int64_t>(z + 1) * steps / p.split);
+        // kRows: slices are pairs of steps
+        constexpr int unit = OP == MxOperands::kRows ? 2 : 1;
+        const int units = (kColumns ? set_steps * p.sets : set_steps + 1) / unit;
+        t_begin = unit * static_cast<int>(static_cast<int64_t>(z) * units / p.split);
+        t_end = unit * static_cast<int>(static_cast<int64_t>(z + 1) * units / p.split);
     }
 
     // ---- left operand: direct loads, instruction i of this wave fills rows 8 (wave + NW i) .. + 7
@@ -111,10 +135,10 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
         bool inside;
         uint32_t at;
         if constexpr (kCodes) {
-            inside = 16 * (t >> 1) + 4 * (t & 1) + 8 * (a_chunk >> 2) + (a_chunk & 3) < blocks;
+            inside = t < t_end && 16 * (t >> 1) + 4 * (t & 1) + 8 * (a_chunk >> 2) + (a_chunk & 3) < blocks;
             at = 256u * (t >> 1) + 64u * (t & 1);
         } else {
-            inside = 64 * step + 8 * a_chunk < L;
+            inside = t < t_end && 64 * step + 8 * a_chunk < L;
             at = 128u * step;
         }
 #pragma unroll
@@ -149,127 +173,130 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     static_assert(!(kCodes && kPair), "the pair decodes its weights");
     const uint32_t b_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * row_codes) +
                            128u * (a_chunk >> 2) + 16u * (a_chunk & 3);
-    // kRows: a thread takes whole blocks.  A wave has both blocks of 32 rows, two lanes a row,
-    // the even rows in its first half: eight lanes' writes then fall into eight different chunks.
-    constexpr int UNITS = OP == MxOperands::kRows ? BN * 2 / NT : 1;
-    static_assert(OP != MxOperands::kRows || BN * 2 % NT == 0, "whole units");
-    auto unit_row = [&](int i) { return 32 * (wave + NW * i) + (lane & 30) + half; };
-    u32x4_t w_codes[2][UNITS];           // of two pipeline steps, by parity
-    uint32_t w_scale[2][UNITS];
-    // kColumns: 8 rows x 4 columns of the step
-    constexpr int GROUP_LANES = kColumns ? BN / 4 : 64;      // threads across the tile's columns
-    static_assert(!kColumns || GROUP_LANES * 8 == NT, "one 8 x 4 unit per thread");
-    const int t_rows = tid / GROUP_LANES, t_col = 4 * (tid % GROUP_LANES);
-    uint16_t t_codes[2][8];
-    uint32_t t_scale[2];
-    auto load_weights = [&](int t, auto ic) {
-        constexpr int par = decltype(ic)::value;
-        if constexpr (OP == MxOperands::kRows) {
-            const int blk = 2 * t + (lane & 1);
+    // Decoded weights: a thread takes one block (16 bytes of codes) of every step, unit tid.
+    //  kColumns: rows of the step side by side, block u % (BN / 32) of row u / (BN / 32): whole 128-byte
+    //    lines; loaded STAGES steps ahead.
+    //  kRows: two blocks per row and step would be 32-byte pieces of 128-byte lines, so two steps are
+    //    loaded at once, four lanes on the four blocks of a row.  Loads 0 and 1 of a lane are two rows;
+    //    lanes 0 and 1 of four keep the first and lanes 2 and 3 the second row for both steps, and get
+    //    (DPP quad_perm 2 3 0 1) what the others loaded of it.  The rows' order makes eight lanes' writes
+    //    fall into eight different chunks.  A lane's four scale bytes of two steps are one word.
+    constexpr bool kRows = OP == MxOperands::kRows;
+    static_assert(kCodes || BN * 2 == NT, "one block per thread and step");
+    constexpr int ROW_BLOCKS = BN / 32;                       // kColumns: blocks of a row of the tile
+    const int quad = lane >> 2, upper = (lane >> 1) & 1;
+    auto quad_row = [&](int i) { return 32 * wave + 2 * (i + 2 * (quad & 7)) + (quad >> 3); };
+    const int unit_row = kRows ? quad_row(upper) : tid / ROW_BLOCKS;
+    const int unit_block = kRows ? lane & 1 : tid % ROW_BLOCKS;
+    constexpr int kCodeSets = kColumns ? STAGES : 4;          // kRows: two pairs of loads
+    u32x4_t w_codes[kCodeSets];
+    uint32_t w_scale[kColumns ? STAGES : kRows && !WHOLE ? 4 : 2];
+    // (a wave's rows are 32 consecutive ones: one weight set)
+    const int own_set = kRows ? set_of(32 * wave) : 0;
+    const __amdgpu_buffer_rsrc_t own_codes = own_set ? wr1 : wr0;
+    const __amdgpu_buffer_rsrc_t own_scales =
+        mx_resource(p.w_scales[own_set] + static_cast<int64_t>(c0) * blocks, columns_left * blocks);
+    // kRows: the blocks of steps t and t + 1 (t even) into slot SLOT
+    auto load_pair = [&](int t, auto slot) {
+        if constexpr (kRows) {
+            constexpr int at = decltype(slot)::value;
+            const int first = 2 * t;
 #pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                const int r = unit_row(i);
-                const int c = column_of(r);
-                // (a wave's units are 32 consecutive rows: one weight set)
-                const int s = __builtin_amdgcn_readfirstlane(set_of(r));
-                const uint32_t co = blk < blocks ? static_cast<uint32_t>(c * row_codes + 16 * (lane & 1)) : kOutside;
-                w_codes[par][i] = __builtin_bit_cast(
-                    u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(s ? wr1 : wr0, co, 32 * t, 0));
-                const __amdgpu_buffer_rsrc_t sr =
-                    mx_resource(p.w_scales[s] + static_cast<int64_t>(c0) * blocks, columns_left * blocks);
-                const uint32_t so = blk < blocks ? static_cast<uint32_t>(c * blocks + (lane & 1)) : kOutside;
-                w_scale[par][i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so, 2 * t, 0);
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t co = first + (lane & 3) < blocks
+                                        ? static_cast<uint32_t>(column_of(quad_row(i)) * row_codes + 16 * (lane & 3))
+                                        : kOutside;
+                w_codes[2 * at + i] =
+                    __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(own_codes, co, 16 * first, 0));
+            }
+            const uint32_t so = static_cast<uint32_t>(column_of(unit_row) * blocks);
+            if constexpr (WHOLE) {
+                w_scale[at] = __builtin_amdgcn_raw_buffer_load_b32(own_scales, first < blocks ? so : kOutside, first, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    w_scale[2 * at + i] = __builtin_amdgcn_raw_buffer_load_b8(
+                        own_scales, first + 2 * i + unit_block < blocks ? so + unit_block : kOutside, first + 2 * i, 0);
             }
         }
+    };
+    // kColumns: the blocks of step t into slot SLOT
+    auto load_step = [&](int t, auto slot) {
         if constexpr (kColumns) {
+            constexpr int at = decltype(slot)::value % STAGES;
             const int set = p.sets > 1 && t >= set_steps ? 1 : 0;
             const int64_t n = 64 * static_cast<int64_t>(t - set * set_steps);
             const __amdgpu_buffer_rsrc_t cr =
                 mx_resource(p.w[set] + n * row_codes + c0 / 2, (L - n) * row_codes - c0 / 2);
             const __amdgpu_buffer_rsrc_t sr =
                 mx_resource(p.w_scales[set] + n * blocks + c0 / kMxBlock, (L - n) * blocks - c0 / kMxBlock);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                t_codes[par][i] = __builtin_amdgcn_raw_buffer_load_b16(
-                    cr, static_cast<uint32_t>((8 * t_rows + i) * row_codes + t_col / 2), 0, 0);
-            // lane l of eight holds the scale of row l % 8; they are handed round below
-            t_scale[par] = __builtin_amdgcn_raw_buffer_load_b8(
-                sr, static_cast<uint32_t>((8 * t_rows + (lane & 7)) * blocks + t_col / kMxBlock), 0, 0);
+            const bool inside = c0 / kMxBlock + unit_block < blocks;
+            w_codes[at] = __builtin_bit_cast(
+                u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                             cr, inside ? static_cast<uint32_t>(unit_row * row_codes + 16 * unit_block) : kOutside, 0, 0));
+            w_scale[at] = __builtin_amdgcn_raw_buffer_load_b8(
+                sr, inside ? static_cast<uint32_t>(unit_row * blocks + unit_block) : kOutside, 0, 0);
         }
     };
-    // decoding and staging, in four parts that the products of a step are spread over
-    uint32_t t_pairs[8][2];    // kColumns: rows, column pairs
+    // Decoding and staging a step (its number modulo four), in four parts that the products of the
+    // step before are spread over.  kColumns stages rows of BN values as they come; the operand reads
+    // transpose them (16-byte chunk c of row n at c ^ 4 (n % 4) ^ (n + c / 16) % 2: conflict-free for
+    // the writes and for reads of 4 rows x 32 columns).
     auto stash_weights = [&](auto ic, auto qc) {
-        constexpr int q = decltype(qc)::value, par = decltype(ic)::value;
+        constexpr int n = decltype(ic)::value, q = decltype(qc)::value;
         uint8_t* dst = b_stage(ic);
-        if constexpr (OP == MxOperands::kRows) {
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                const int r = unit_row(i);
-                const int c = (4 * (lane & 1) + q) ^ ((r >> 1) & 7);
-                *reinterpret_cast<u32x4_t*>(dst + r * 128 + 16 * c) = mx_decode_word(w_codes[par][i][q], mx_scale(w_scale[par][i]));
-            }
+        if constexpr (kRows) {
+            constexpr int pair = n / 2 % 2, odd = n % 2;
+            const uint32_t mine = w_codes[2 * pair + odd][q], other = w_codes[2 * pair + 1 - odd][q];
+            const uint32_t moved = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(other), 0x4E, 0xF, 0xF, true));
+            const uint32_t w = upper == odd ? mine : moved;
+            const uint32_t e = WHOLE ? (w_scale[pair] >> (8 * (2 * odd + unit_block))) & 0xFFu : w_scale[2 * pair * !WHOLE + odd];
+            const int c = (4 * unit_block + q) ^ ((unit_row >> 1) & 7);
+            *reinterpret_cast<u32x4_t*>(dst + unit_row * 128 + 16 * c) = mx_decode_word(w, mx_scale(e));
         }
         if constexpr (kColumns) {
-            auto row = [&](auto rc) {
-                constexpr int i = decltype(rc)::value;
-                const float s = mx_scale(__builtin_amdgcn_ds_swizzle(static_cast<int>(t_scale[par]), (i << 5) | 0x18));
-                t_pairs[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(t_codes[par][i], s, 0));
-                t_pairs[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(t_codes[par][i], s, 1));
-            };
-            if constexpr (q < 2) {
-                row(std::integral_constant<int, 4 * (q & 1)>{});
-                row(std::integral_constant<int, 4 * (q & 1) + 1>{});
-                row(std::integral_constant<int, 4 * (q & 1) + 2>{});
-                row(std::integral_constant<int, 4 * (q & 1) + 3>{});
-            } else {
-#pragma unroll
-                for (int k = 2 * (q & 1); k < 2 * (q & 1) + 2; ++k) {
-                    u32x4_t out;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        out[i] = __builtin_amdgcn_perm(t_pairs[2 * i + 1][k >> 1], t_pairs[2 * i][k >> 1],
-                                                       (k & 1) ? 0x07060302u : 0x05040100u);
-                    const int r = t_col + k;
-                    const int c = t_rows ^ (((r >> 1) ^ (r >> 4)) & 7);
-                    *reinterpret_cast<u32x4_t*>(dst + r * 128 + 16 * c) = out;
-                }
-            }
+            constexpr int at = n % STAGES;
+            const int c = (4 * unit_block + q) ^ (4 * (unit_row & 3)) ^ ((unit_row + unit_block / 4) & 1);
+            *reinterpret_cast<u32x4_t*>(dst + unit_row * (2 * BN) + 16 * c) =
+                mx_decode_word(w_codes[at][q], mx_scale(w_scale[at]));
         }
     };
 
     // ---- scales of both operands (kCodes): thread r < BM + BN keeps row r's next 16 bytes, one
     // load where rows are whole pieces of 16, a byte each elsewhere.  A byte past the row's last
     // block is put to 0 (a finite scale: its codes are zeros).
-    static_assert(!kCodes || (BM + BN == NT && BM % 64 == 0), "one row of scales per thread, one operand per wave");
-    u32x4_t s_next = {0, 0, 0, 0};
-    uint32_t s_bytes[!kCodes || WHOLE ? 1 : 16];
+    static_assert(!kCodes || (BM + BN <= NT && BM % 64 == 0), "one row of scales per thread, one operand per wave");
+    constexpr int PAIRS = STAGES / 2;
+    u32x4_t s_next[PAIRS];               // of the next pairs of steps
+    uint32_t s_bytes[PAIRS][!kCodes || WHOLE ? 1 : 16];
     const bool s_left = kCodes && wave < BM / 64;
     const int s_first = s_left ? m0 : c0;
     const __amdgpu_buffer_rsrc_t s_rows =
         mx_resource((s_left ? p.a_scales : p.w_scales[0]) + static_cast<int64_t>(s_first) * blocks,
                     (static_cast<int64_t>(s_left ? p.M : p.N) - s_first) * blocks);
     const uint32_t s_off = static_cast<uint32_t>((s_left ? tid : tid - BM) * blocks);
-    auto load_scales = [&](int window) {
+    auto load_scales = [&](int window, auto ic) {
+        constexpr int pair = decltype(ic)::value / 2 % PAIRS;
         if constexpr (kCodes && WHOLE) {
-            s_next = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+            s_next[pair] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
                                                      s_rows, 16 * window < blocks ? s_off : kOutside, 16 * window, 0));
         } else if constexpr (kCodes) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                s_bytes[e] = __builtin_amdgcn_raw_buffer_load_b8(
+                s_bytes[pair][e] = __builtin_amdgcn_raw_buffer_load_b8(
                     s_rows, 16 * window + e < blocks ? s_off : kOutside, 16 * window + e, 0);
         }
     };
-    auto stash_scales = [&](int window) {
+    auto stash_scales = [&](int window, auto ic) {
+        constexpr int pair = decltype(ic)::value / 2 % PAIRS;
         if constexpr (kCodes) {
             if constexpr (!WHOLE) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    s_next[q] = s_bytes[4 * q] | s_bytes[4 * q + 1] << 8 | s_bytes[4 * q + 2] << 16 |
-                                s_bytes[4 * q + 3] << 24;
+                    s_next[pair][q] = s_bytes[pair][4 * q] | s_bytes[pair][4 * q + 1] << 8 |
+                                      s_bytes[pair][4 * q + 2] << 16 | s_bytes[pair][4 * q + 3] << 24;
             }
-            *reinterpret_cast<u32x4_t*>(sc + (window & 1) * (BM + BN) * 16 + tid * 16) = s_next;
+            *reinterpret_cast<u32x4_t*>(sc + (window & 1) * NT * 16 + tid * 16) = s_next[pair];
         }
     };
 
@@ -281,28 +308,30 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-    // chunk c of this lane's row of block b: rows of a block share (r / 2) % 8; kColumns adds 2 b
+    // Chunk c of this lane's row of a block; rows of a block share (r / 2) % 8.
     const int arow = wr * MI * 32 + (lane & 31), brow = wc * NI * 32 + (lane & 31);
-    const int akey = (lane >> 1) & 7;
-    const int bkey = kColumns ? (akey ^ ((lane >> 4) & 1)) : akey;
-    // operands of two MFMA steps (by parity) and the scales of two pipeline steps; zeros at first, for
-    // the products that the first pipeline step makes of the step before it
+    const int key = (lane >> 1) & 7;
+    // kColumns: a transposing read gives lane i of sixteen column i of 4 rows x 16 columns, of which it
+    // addresses 4 columns of row i / 4
+    const int t_row = 32 * half + ((lane & 15) >> 2);
+    const int t_low = 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+    // The products lag one MFMA step behind the reads, across the barrier too, so that an LDS read has
+    // MFMAs to hide under.  Operands of two MFMA steps and scales of two pipeline steps, by parity; zeros
+    // at first, for the products that the first pipeline step makes of the one before it.
     u32x4_t af[2][MI], bf[2][NI];
     uint32_t sa[2][MI], sb[2][NI];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        af[1][i] = u32x4_t{0, 0, 0, 0};
-        sa[1][i] = 0;
-    }
+    for (int i = 0; i < MI; ++i) af[1][i] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        bf[1][i] = u32x4_t{0, 0, 0, 0};
-        sb[1][i] = 0;
-    }
+    for (int i = 0; i < NI; ++i) bf[1][i] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sa[1][i] = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) sb[1][i] = 0;
     auto read_scales = [&](int t, auto ic) {
         if constexpr (kCodes) {
-            constexpr int par = decltype(ic)::value;
-            const uint8_t* s = sc + ((t >> 1) & 1) * (BM + BN) * 16 + 8 * half + 4 * (t & 1);
+            constexpr int par = decltype(ic)::value & 1;
+            const uint8_t* s = sc + ((t >> 1) & 1) * NT * 16 + 8 * half + 4 * (t & 1);
 #pragma unroll
             for (int i = 0; i < MI; ++i) sa[par][i] = *reinterpret_cast<const uint32_t*>(s + (arow + 32 * i) * 16);
 #pragma unroll
@@ -315,16 +344,26 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
         const uint8_t* bs = b_stage(ic) + brow * 128;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
-            af[j & 1][i] = *reinterpret_cast<const u32x4_t*>(as + i * 4096 + 16 * ((4 * half + j) ^ akey));
+            af[j & 1][i] = *reinterpret_cast<const u32x4_t*>(as + i * 4096 + 16 * ((4 * half + j) ^ key));
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            // row / 16 of block wc * NI + i: 2 (wc NI + i) + lane / 16 % 2
-            const int k = kColumns ? (bkey ^ ((2 * (wc * NI + i)) & 7)) : bkey;
-            bf[j & 1][i] = *reinterpret_cast<const u32x4_t*>(bs + i * 4096 + 16 * ((4 * half + j) ^ k));
+            if constexpr (kColumns) {
+                typedef short s16x4_t __attribute__((ext_vector_type(4)));
+                typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4;
+                const int cb = wc * NI + i, a = (lane & 15) >> 2;
+                const int chunk = ((4 * cb) ^ (4 * a)) + (t_low ^ ((a + cb / 4) & 1));
+                const uint8_t* at = b_stage(ic) + (t_row + 8 * j) * (2 * BN) + 16 * chunk + 8 * (lane & 1);
+                // rows 8 (4 half + j) + 0 .. 3 and + 4 .. 7
+                const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at));
+                const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at + 4 * 2 * BN));
+                bf[j & 1][i] = __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            } else {
+                bf[j & 1][i] = *reinterpret_cast<const u32x4_t*>(bs + i * 4096 + 16 * ((4 * half + j) ^ key));
+            }
         }
     };
     auto multiply = [&](auto ic, auto jc) {
-        constexpr int j = decltype(jc)::value, par = decltype(ic)::value;
+        constexpr int j = decltype(jc)::value, par = decltype(ic)::value & 1;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -351,57 +390,86 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
     using Three = std::integral_constant<int, 3>;
+    // Loads of a step: the left operand (and codes) of the step AHEAD of it, then, in some steps, more:
+    // kCodes scales in even steps, kRows two steps' weights in odd ones, kColumns weights in each.
+    constexpr int AHEAD = STAGES - 1;
+    constexpr int kStepLoads = A_LOADS + (kCodes ? B_LOADS : 0);
+    constexpr auto more_loads = [](int parity) {
+        return kCodes ? (parity == 0 ? (WHOLE ? 1 : 16) : 0) : kRows ? (parity == 1 ? (WHOLE ? 3 : 4) : 0) : 2;
+    };
+    // loads issued after those that a step of this parity waits for
+    constexpr auto pending = [more_loads](int parity) {
+        int n = more_loads((parity + AHEAD) % 2);
+        for (int s = 1; s < AHEAD; ++s) n += kStepLoads + more_loads((parity + s) % 2);
+        return n;
+    };
+    // (all of the first loads are on their way before the first is waited for)
     if constexpr (kCodes) {
-        load_scales(t_begin >> 1);
-        stash_scales(t_begin >> 1);
+        load_scales(t_begin >> 1, Zero{});
+        if constexpr (kDeep) load_scales((t_begin >> 1) + 1, Two{});
     } else {
-        load_weights(t_begin, Zero{});
-        stash_weights(Zero{}, Zero{});
-        stash_weights(Zero{}, One{});
-        stash_weights(Zero{}, Two{});
-        stash_weights(Zero{}, Three{});
-        load_weights(t_begin + 1, One{});
+        load_pair(t_begin, Zero{});
+        load_step(t_begin, Zero{});
     }
     stage_step(t_begin, Zero{});
-    auto step = [&](int t, auto ic, auto nc) {
-        loads_done_barrier();
+    if constexpr (kDeep) {
+        stage_step(t_begin + 1, One{});
+        stage_step(t_begin + 2, Two{});
+    }
+    load_pair(t_begin + 2, One{});
+    load_step(t_begin + 1, One{});
+    if constexpr (kDeep) {
+        load_step(t_begin + 2, Two{});
+        load_step(t_begin + 3, Three{});
+    }
+    stash_scales(t_begin >> 1, Zero{});
+    stash_weights(Zero{}, Zero{});
+    stash_weights(Zero{}, One{});
+    stash_weights(Zero{}, Two{});
+    stash_weights(Zero{}, Three{});
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // step t, whose number modulo four is that of ic
+    auto step = [&](int t, auto ic) {
+        constexpr int i = decltype(ic)::value;
+        using Next = std::integral_constant<int, i + 1>;
+        using Ahead = std::integral_constant<int, i + AHEAD>;
+        using Before = std::integral_constant<int, i + 1>;                // (parity of step t - 1)
+        loads_done_barrier<pending(i % 2)>();
         read_scales(t, ic);
         read(ic, Zero{});
-        // every load of this step is issued here, a whole step before the wait for it
-        stage_step(t + 1, nc);
-        if constexpr (!kCodes)
-            load_weights(t + 2, ic);
-        else if constexpr (decltype(ic)::value == 0)
-            load_scales((t >> 1) + 1);
-        stash_weights(nc, Zero{});
-        multiply(nc, Three{});          // of step t - 1
+        // every load of this step is issued here, as long as possible before the wait for it
+        stage_step(t + AHEAD, Ahead{});
+        if constexpr (kCodes && i % 2 == 0) load_scales((t >> 1) + PAIRS, ic);
+        if constexpr (kRows && i % 2 == 1) load_pair(t + 3, std::integral_constant<int, (i + 3) / 2 % 2>{});
+        if constexpr (kColumns) load_step(t + STAGES, ic);
+        stash_weights(Next{}, Zero{});
+        multiply(Before{}, Three{});          // of step t - 1
         __builtin_amdgcn_sched_barrier(0);
         read(ic, One{});
-        stash_weights(nc, One{});
+        stash_weights(Next{}, One{});
         multiply(ic, Zero{});
         __builtin_amdgcn_sched_barrier(0);
         read(ic, Two{});
-        stash_weights(nc, Two{});
+        stash_weights(Next{}, Two{});
         multiply(ic, One{});
         __builtin_amdgcn_sched_barrier(0);
         read(ic, Three{});
-        // t is even exactly when ic is the even stage: slices start at a pair of steps
-        if constexpr (kCodes && decltype(ic)::value == 1) stash_scales((t >> 1) + 1);
-        stash_weights(nc, Three{});
+        if constexpr (kCodes && i % 2 == 1) stash_scales((t >> 1) + 1, Next{});
+        stash_weights(Next{}, Three{});
         multiply(ic, Two{});
         __builtin_amdgcn_sched_barrier(0);
     };
-    int t = t_begin;
-    for (; t + 2 <= t_end; t += 2) {
-        step(t, Zero{}, One{});
-        step(t + 1, One{}, Zero{});
+    // steps past the end, up to a whole round, have a left operand of zeros
+    constexpr int ROUND = kRows ? 4 : STAGES;
+    for (int t = t_begin; t < t_end; t += ROUND) {
+        step(t, Zero{});
+        step(t + 1, One{});
+        if constexpr (ROUND == 4) {
+            step(t + 2, Two{});
+            step(t + 3, Three{});
+        }
     }
-    if (t < t_end) {
-        step(t, Zero{}, One{});
-        multiply(Zero{}, Three{});
-    } else {
-        multiply(One{}, Three{});
-    }
+    multiply(One{}, Three{});
 
     // ---- epilogue.  Register r of a block: column 8 (r / 4) + 4 half + r % 4, row lane % 32.
     const int row0 = m0 + wr * MI * 32;
@@ -437,7 +505,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     constexpr int WCOLS = kPair ? NI * 16 : NI * 32;
     constexpr int PITCH = WCOLS * 2 + 16;
     static_assert((NW / 2) * 32 * PITCH <= BN * 128, "the waves' regions fit the weight stages");
-    loads_done_barrier();
+    loads_done_barrier<0>();
     uint8_t* region = ((wave & 1) ? b1 : b0) + (wave >> 1) * (32 * PITCH);
     const int col0 = c0 + (kPair ? wc * NI * 16 : wc * NI * 32);
     constexpr int PIECES = WCOLS / 8;                        // 16-byte pieces of a row
@@ -548,11 +616,11 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
 
 }  // namespace
 
-const MxTileShape kMxTiles[kNumMxTiles] = {{128, 128, 4}, {256, 256, 8}};
+const MxTileShape kMxTiles[kNumMxTiles] = {{128, 128, 4}, {256, 256, 8}, {64, 128, 4}, {192, 256, 8}};
 
 namespace {
 
-template <int BM, int BN, int WR, int WC>
+template <int BM, int BN, int WR, int WC, int STAGES>
 hipError_t launch_shape(MxOperands op, MxEpilogue epi, const MxTileArgs& args, hipStream_t stream) {
     const int bc = epi == MxEpilogue::kStore ? BN : BN / 2;
     const int tiles_m = (args.M + BM - 1) / BM, tiles_n = (args.N + bc - 1) / bc;
@@ -566,21 +634,31 @@ hipError_t launch_shape(MxOperands op, MxEpilogue epi, const MxTileArgs& args, h
     if (op == O::kCodes) {
         const bool whole = args.L % 512 == 0 && ((reinterpret_cast<uintptr_t>(args.a_scales) |
                                                   reinterpret_cast<uintptr_t>(args.w_scales[0])) & 15) == 0;
-        return whole ? run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, true>)
-                     : run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, false>);
+        return whole ? run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, STAGES, true>)
+                     : run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, STAGES, false>);
     }
-    if (op == O::kColumns) return run(mx_tile_kernel<O::kColumns, E::kStore, BM, BN, WR, WC, true>);
-    if (epi == E::kGlu) return run(mx_tile_kernel<O::kRows, E::kGlu, BM, BN, WR, WC, true>);
-    if (epi == E::kGluGrad) return run(mx_tile_kernel<O::kRows, E::kGluGrad, BM, BN, WR, WC, true>);
-    return run(mx_tile_kernel<O::kRows, E::kStore, BM, BN, WR, WC, true>);
+    if (op == O::kColumns) return run(mx_tile_kernel<O::kColumns, E::kStore, BM, BN, WR, WC, STAGES, true>);
+    // words of four scale bytes in every row
+    const bool words = args.L % 128 == 0 && ((reinterpret_cast<uintptr_t>(args.w_scales[0]) |
+                                              reinterpret_cast<uintptr_t>(args.w_scales[1])) & 3) == 0;
+    auto rows = [&](auto ec) {
+        constexpr E e = decltype(ec)::value;
+        return words ? run(mx_tile_kernel<O::kRows, e, BM, BN, WR, WC, STAGES, true>)
+                     : run(mx_tile_kernel<O::kRows, e, BM, BN, WR, WC, STAGES, false>);
+    };
+    if (epi == E::kGlu) return rows(std::integral_constant<E, E::kGlu>{});
+    if (epi == E::kGluGrad) return rows(std::integral_constant<E, E::kGluGrad>{});
+    return rows(std::integral_constant<E, E::kStore>{});
 }
 
 }  // namespace
 
 hipError_t launch_mx_tile(MxOperands op, MxEpilogue epi, int tile, const MxTileArgs& args, hipStream_t stream) {
     switch (tile) {
-        case 0: return launch_shape<128, 128, 2, 2>(op, epi, args, stream);
-        case 1: return launch_shape<256, 256, 2, 4>(op, epi, args, stream);
+        case 0: return launch_shape<128, 128, 2, 2, 2>(op, epi, args, stream);
+        case 1: return launch_shape<256, 256, 2, 4, 2>(op, epi, args, stream);
+        case 2: return launch_shape<64, 128, 2, 2, 4>(op, epi, args, stream);
+        case 3: return launch_shape<192, 256, 2, 4, 2>(op, epi, args, stream);
         default: return hipErrorInvalidValue;
     }
 }
