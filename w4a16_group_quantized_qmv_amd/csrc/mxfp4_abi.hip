@@ -98,7 +98,7 @@ struct TileCost {
 };
 constexpr TileCost kTileCost[3][kNumMxTiles] = {
     // 128 x 128        256 x 256      64 x 128          192 x 256
-    {{3.0, 0.73, 1.3}, {9.0, 1.54, 0}, {4.5, 0.45, 0.9}, {6.0, 1.45, 0}},     // kCodes (256 values a step)
+    {{3.0, 0.67, 1.2}, {9.0, 1.20, 0}, {4.5, 0.41, 0.85}, {6.0, 1.05, 0}},    // kCodes (256 values a step)
     {{5.0, 0.46, 1.0}, {10.0, 1.30, 0}, {5.0, 0.32, 0.54}, {8.0, 1.17, 0}},   // kRows (64)
     {{5.0, 0.64, 0.9}, {8.0, 1.42, 0}, {5.0, 0.54, 0.9}, {6.0, 1.32, 0}},     // kColumns (64)
 };

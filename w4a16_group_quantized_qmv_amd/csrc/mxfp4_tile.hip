@@ -20,8 +20,9 @@
 //    the codes are packed along the output columns.  A thread takes 8 weight rows x 4 columns
 //    (2 bytes of each row), decodes pairs of columns and exchanges halves with 16 byte permutes.
 //  * Of the 128 bytes, MFMA step j of lane half h takes chunk 4 h + j.  For codes a chunk is one
-//    block, and a pair of pipeline steps covers 16 blocks so distributed that a lane's four scale
-//    bytes per step are one aligned word: step i, half h, MFMA j is block 8 h + 4 i + j.
+//    block, so the four scale bytes that a lane needs in a pipeline step are one aligned word of the
+//    row's scales.  (Steps of whole 128-byte lines: taking 64 bytes from each of two lines, which also
+//    gives such words, is twice the requests to L2.)
 //  * The weights are the MFMA's row operand, so a lane's results are four consecutive output
 //    columns of one row; each wave turns its block through LDS and stores whole 16-byte pieces.
 //  * With two weight sets (gate and up) the 32-column blocks of the tile alternate between them, so
@@ -112,11 +113,9 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     const int set_steps = (L + 63) / 64;                     // bf16 operands
     int t_begin, t_end;
     if constexpr (kCodes) {
-        const int rest = blocks % 16, windows = (blocks + 15) / 16;
-        const int w0 = static_cast<int>(static_cast<int64_t>(z) * windows / p.split);
-        const int w1 = static_cast<int>(static_cast<int64_t>(z + 1) * windows / p.split);
-        t_begin = 2 * w0;
-        t_end = 2 * w1 - (w1 == windows && rest > 0 && rest <= 4 ? 1 : 0);
+        const int pairs = (blocks + 15) / 16;
+        t_begin = 2 * static_cast<int>(static_cast<int64_t>(z) * pairs / p.split);
+        t_end = min(2 * static_cast<int>(static_cast<int64_t>(z + 1) * pairs / p.split), (blocks + 7) / 8);
     } else {
         // kRows: slices are pairs of steps
         constexpr int unit = OP == MxOperands::kRows ? 2 : 1;
@@ -128,19 +127,11 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     // ---- left operand: direct loads, instruction i of this wave fills rows 8 (wave + NW i) .. + 7
     constexpr int A_LOADS = BM / (8 * NW);
     const int a_chunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
-    uint32_t a_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * left_row) +
-                     (kCodes ? 128u * (a_chunk >> 2) + 16u * (a_chunk & 3) : 16u * a_chunk);
+    const uint32_t a_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * left_row) + 16u * a_chunk;
     auto issue_rows = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t off, int pitch, uint8_t* dst, int t, int step,
                           auto loads) {
-        bool inside;
-        uint32_t at;
-        if constexpr (kCodes) {
-            inside = t < t_end && 16 * (t >> 1) + 4 * (t & 1) + 8 * (a_chunk >> 2) + (a_chunk & 3) < blocks;
-            at = 256u * (t >> 1) + 64u * (t & 1);
-        } else {
-            inside = t < t_end && 64 * step + 8 * a_chunk < L;
-            at = 128u * step;
-        }
+        const bool inside = t < t_end && (kCodes ? 8 * step + a_chunk < blocks : 64 * step + 8 * a_chunk < L);
+        const uint32_t at = 128u * step;
 #pragma unroll
         for (int i = 0; i < decltype(loads)::value; ++i) {
             uint8_t* to = dst + __builtin_amdgcn_readfirstlane((wave + NW * i) * 1024);
@@ -171,11 +162,10 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     // kCodes: direct loads as for the left operand (one weight set)
     constexpr int B_LOADS = kCodes ? BN / (8 * NW) : 1;
     static_assert(!(kCodes && kPair), "the pair decodes its weights");
-    const uint32_t b_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * row_codes) +
-                           128u * (a_chunk >> 2) + 16u * (a_chunk & 3);
+    const uint32_t b_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * row_codes) + 16u * a_chunk;
     // Decoded weights: a thread takes one block (16 bytes of codes) of every step, unit tid.
     //  kColumns: rows of the step side by side, block u % (BN / 32) of row u / (BN / 32): whole 128-byte
-    //    lines; loaded STAGES steps ahead.
+    //    lines; loaded four steps ahead (two: 128 x 128 tiles alone on their units took 0.65 us a step).
     //  kRows: two blocks per row and step would be 32-byte pieces of 128-byte lines, so two steps are
     //    loaded at once, four lanes on the four blocks of a row.  Loads 0 and 1 of a lane are two rows;
     //    lanes 0 and 1 of four keep the first and lanes 2 and 3 the second row for both steps, and get
@@ -188,9 +178,8 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     auto quad_row = [&](int i) { return 32 * wave + 2 * (i + 2 * (quad & 7)) + (quad >> 3); };
     const int unit_row = kRows ? quad_row(upper) : tid / ROW_BLOCKS;
     const int unit_block = kRows ? lane & 1 : tid % ROW_BLOCKS;
-    constexpr int kCodeSets = kColumns ? STAGES : 4;          // kRows: two pairs of loads
-    u32x4_t w_codes[kCodeSets];
-    uint32_t w_scale[kColumns ? STAGES : kRows && !WHOLE ? 4 : 2];
+    u32x4_t w_codes[4];                                       // four steps, or two pairs of loads
+    uint32_t w_scale[kColumns || !WHOLE ? 4 : 2];
     // (a wave's rows are 32 consecutive ones: one weight set)
     const int own_set = kRows ? set_of(32 * wave) : 0;
     const __amdgpu_buffer_rsrc_t own_codes = own_set ? wr1 : wr0;
@@ -223,7 +212,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     // kColumns: the blocks of step t into slot SLOT
     auto load_step = [&](int t, auto slot) {
         if constexpr (kColumns) {
-            constexpr int at = decltype(slot)::value % STAGES;
+            constexpr int at = decltype(slot)::value % 4;
             const int set = p.sets > 1 && t >= set_steps ? 1 : 0;
             const int64_t n = 64 * static_cast<int64_t>(t - set * set_steps);
             const __amdgpu_buffer_rsrc_t cr =
@@ -240,8 +229,9 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     };
     // Decoding and staging a step (its number modulo four), in four parts that the products of the
     // step before are spread over.  kColumns stages rows of BN values as they come; the operand reads
-    // transpose them (16-byte chunk c of row n at c ^ 4 (n % 4) ^ (n + c / 16) % 2: conflict-free for
-    // the writes and for reads of 4 rows x 32 columns).
+    // transpose them.  16-byte chunk c of row n lies at c ^ (c / 8) % 4 ^ 4 (n % 4) ^ 2 (n % 2):
+    // conflict-free for the writes (eight lanes on eight blocks of a row, or on four of two rows) and
+    // for reads of 4 rows x 32 columns.
     auto stash_weights = [&](auto ic, auto qc) {
         constexpr int n = decltype(ic)::value, q = decltype(qc)::value;
         uint8_t* dst = b_stage(ic);
@@ -255,8 +245,8 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
             *reinterpret_cast<u32x4_t*>(dst + unit_row * 128 + 16 * c) = mx_decode_word(w, mx_scale(e));
         }
         if constexpr (kColumns) {
-            constexpr int at = n % STAGES;
-            const int c = (4 * unit_block + q) ^ (4 * (unit_row & 3)) ^ ((unit_row + unit_block / 4) & 1);
+            constexpr int at = n % 4;
+            const int c = (4 * unit_block + (q ^ (unit_block >> 1))) ^ (4 * (unit_row & 3)) ^ (2 * (unit_row & 1));
             *reinterpret_cast<u32x4_t*>(dst + unit_row * (2 * BN) + 16 * c) =
                 mx_decode_word(w_codes[at][q], mx_scale(w_scale[at]));
         }
@@ -331,7 +321,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     auto read_scales = [&](int t, auto ic) {
         if constexpr (kCodes) {
             constexpr int par = decltype(ic)::value & 1;
-            const uint8_t* s = sc + ((t >> 1) & 1) * NT * 16 + 8 * half + 4 * (t & 1);
+            const uint8_t* s = sc + ((t >> 1) & 1) * NT * 16 + 8 * (t & 1) + 4 * half;
 #pragma unroll
             for (int i = 0; i < MI; ++i) sa[par][i] = *reinterpret_cast<const uint32_t*>(s + (arow + 32 * i) * 16);
 #pragma unroll
@@ -351,7 +341,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
                 typedef short s16x4_t __attribute__((ext_vector_type(4)));
                 typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4;
                 const int cb = wc * NI + i, a = (lane & 15) >> 2;
-                const int chunk = ((4 * cb) ^ (4 * a)) + (t_low ^ ((a + cb / 4) & 1));
+                const int chunk = ((4 * cb) ^ (4 * a)) + (t_low ^ ((cb / 2) & 3) ^ (2 * (a & 1)));
                 const uint8_t* at = b_stage(ic) + (t_row + 8 * j) * (2 * BN) + 16 * chunk + 8 * (lane & 1);
                 // rows 8 (4 half + j) + 0 .. 3 and + 4 .. 7
                 const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at));
@@ -384,7 +374,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     auto stage_step = [&](int t, auto ic) {
         issue_left(t, ic);
         if constexpr (kCodes)
-            issue_rows(wr0, b_off, row_codes, b_stage(ic), t, 0, std::integral_constant<int, B_LOADS>{});
+            issue_rows(wr0, b_off, row_codes, b_stage(ic), t, t, std::integral_constant<int, B_LOADS>{});
     };
     using Zero = std::integral_constant<int, 0>;
     using One = std::integral_constant<int, 1>;
@@ -418,10 +408,8 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     }
     load_pair(t_begin + 2, One{});
     load_step(t_begin + 1, One{});
-    if constexpr (kDeep) {
-        load_step(t_begin + 2, Two{});
-        load_step(t_begin + 3, Three{});
-    }
+    load_step(t_begin + 2, Two{});
+    load_step(t_begin + 3, Three{});
     stash_scales(t_begin >> 1, Zero{});
     stash_weights(Zero{}, Zero{});
     stash_weights(Zero{}, One{});
@@ -441,7 +429,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
         stage_step(t + AHEAD, Ahead{});
         if constexpr (kCodes && i % 2 == 0) load_scales((t >> 1) + PAIRS, ic);
         if constexpr (kRows && i % 2 == 1) load_pair(t + 3, std::integral_constant<int, (i + 3) / 2 % 2>{});
-        if constexpr (kColumns) load_step(t + STAGES, ic);
+        if constexpr (kColumns) load_step(t + 4, ic);
         stash_weights(Next{}, Zero{});
         multiply(Before{}, Three{});          // of step t - 1
         __builtin_amdgcn_sched_barrier(0);
@@ -460,7 +448,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
         __builtin_amdgcn_sched_barrier(0);
     };
     // steps past the end, up to a whole round, have a left operand of zeros
-    constexpr int ROUND = kRows ? 4 : STAGES;
+    constexpr int ROUND = kCodes ? STAGES : 4;
     for (int t = t_begin; t < t_end; t += ROUND) {
         step(t, Zero{});
         step(t + 1, One{});
