@@ -205,7 +205,7 @@ def test_linear_backward(lib, M, N, K, split):
 
 
 # many columns: the wide decode form, with ragged last blocks, and the grids of the large tiles
-WIDE_SIZES = [(1, 16400, 512), (3, 20007, 1536), (5, 16391, 1024), (16, 16384, 512)]
+WIDE_SIZES = [(1, 20500, 512), (3, 20007, 1536), (5, 12391, 1024), (16, 16384, 512), (16, 12300, 4608)]
 LARGE_SIZES = [(773, 13176, 96), (522, 13265, 96), (961, 10881, 544), (300, 17001, 160)]
 LARGE_BACK_SIZES = [(2323, 72, 4928), (1298, 72, 5952), (321, 75, 5408)]
 LARGE_GATED_SIZES = [(390, 11227, 96), (257, 10998, 96), (2325, 72, 4896), (1422, 75, 5408), (201, 2000, 1376)]
@@ -570,3 +570,123 @@ def test_refused_tensors(lib):
         lib.mxfp4_gate_up_swiglu(x, (codes, scales), (codes[:32], scales[:32]))
     with pytest.raises(ValueError, match="negative"):
         lib.mxfp4_linear(x, codes, scales, split_k=-1)
+
+
+def test_scales_at_odd_addresses_and_tiles(lib):
+    """Scale rows may start anywhere: the tiles' word and 16-byte loads give way to bytes."""
+    import torch
+    announce("mxfp4 odd scale addresses")
+    M, N, K = 40, 136, 1024
+    rng = np.random.default_rng(16)
+    (codes, scales), wv = weight(rng, N, K)
+    (up_codes, up_scales), uv = weight(rng, N, K, 118, 124)
+
+    def odd(s):
+        return torch.cat([s.view(-1)[:1], s.view(-1)])[1:].view(s.shape)
+    x = bf16_values(rng.standard_normal((M, K)))
+    check(lib.mxfp4_linear(bf16(x), codes, odd(scales)), O.mx_linear(x, wv))
+    xq = lib.mxfp4_quantize_rows(bf16(x))
+    xv = O.mx_decode(*(t.cpu().numpy() for t in xq))
+    check(lib.qmm_mxfp4a4(xq[0], odd(xq[1]), codes, scales), O.mx_linear(xv, wv))
+    check(lib.qmm_mxfp4a4(*xq, codes, odd(scales)), O.mx_linear(xv, wv))
+    check(lib.mxfp4_linear_backward(bf16(x[:, :N]), codes, odd(scales)), O.mx_linear_backward(x[:, :N], wv))
+    g = (up_codes, up_scales)
+    check(lib.mxfp4_gate_up_swiglu(bf16(x), g, (up_codes, odd(up_scales))), O.mx_gate_up(x, uv, uv))
+
+
+def test_prepared_calls(lib):
+    """Prepared calls equal the functions, launch after launch, on new contents of their tensors."""
+    import torch
+    announce("mxfp4 prepared calls")
+    rng = np.random.default_rng(17)
+    for M in (1, 12, 50):
+        w, _ = weight(rng, 136, 1056)
+        u, _ = weight(rng, 136, 1056, 118, 122)
+        x = bf16(rng.standard_normal((M, 1056)))
+        prepared = [lib.PreparedMxfp4Linear(x, *w, split_k=0), lib.PreparedMxfp4Linear(x, *w, split_k=3),
+                    lib.PreparedMxfp4Linear(x, *w, four_bit_activations=True), lib.PreparedMxfp4GateUp(x, w, u)]
+        for _ in range(2):
+            x.copy_(bf16(rng.standard_normal((M, 1056))))
+            expected = [lib.mxfp4_linear(x, *w), lib.mxfp4_linear(x, *w, split_k=3), lib.mxfp4a4_linear(x, *w),
+                        lib.mxfp4_gate_up_swiglu(x, w, u)]
+            for p, e in zip(prepared, expected):
+                assert torch.equal(p(), e)
+    with pytest.raises(ValueError, match="shape"):
+        lib.PreparedMxfp4Linear(x[:, :512].contiguous(), *w)
+    with pytest.raises(ValueError, match="WORKSPACE"):
+        lib.PreparedMxfp4Linear(x, *w, split_k=3, workspace=torch.empty(4, device="cuda:0"))()
+
+
+def test_timing_request_takes_the_product(lib):
+    """w4a16_time_next_launch times the product's kernel, not the quantization before it."""
+    import torch
+    announce("mxfp4 kernel timestamps")
+    rng = np.random.default_rng(18)
+    w, _ = weight(rng, 600, 1024)
+    x = bf16(rng.standard_normal((100, 1024)))
+    start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record(), stop.record()
+    lib.w4a16_time_next_launch(start, stop)
+    y = lib.mxfp4a4_linear(x, *w)
+    torch.cuda.synchronize()
+    assert 0 < start.elapsed_time(stop) < 100
+    assert torch.equal(y, lib.mxfp4a4_linear(x, *w))
+
+
+# ---------------------------------------------------------------------------- offsets beyond 32 bits
+
+def _sampled(rows):
+    return sorted({0, 1, rows // 2, rows - 2, rows - 1})
+
+
+def test_outputs_beyond_two_to_the_31(lib):
+    """More than 2^31 output elements: rows and columns at both ends."""
+    import torch
+    M, N, K = 16400, 131100, 32
+    announce(f"mxfp4_linear M={M} N={N}: {M * N} outputs")
+    assert M * N > 2 ** 31
+    g = torch.Generator(device="cuda:0").manual_seed(1)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda:0", generator=g)
+    scales = torch.randint(118, 124, (N, K // 32), dtype=torch.uint8, device="cuda:0", generator=g)
+    x = torch.randn(M, K, device="cuda:0", generator=g).to(torch.bfloat16)
+    y = lib.mxfp4_linear(x, codes, scales)
+    rows, cols = _sampled(M), _sampled(N)
+    wv = O.mx_decode(codes[cols].cpu().numpy(), scales[cols].cpu().numpy())
+    check(y[rows][:, cols], O.mx_linear(values(x[rows]), wv))
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_weights_beyond_four_gib(lib, M):
+    """More than 2^32 bytes of codes: the last weight rows, and the transposed product over all rows."""
+    import torch
+    N, K = 300000, 32768
+    announce(f"mxfp4_linear M={M}: {N * K // 2} bytes of codes")
+    assert N * K // 2 > 2 ** 32
+    g = torch.Generator(device="cuda:0").manual_seed(2)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda:0", generator=g)
+    scales = torch.randint(118, 124, (N, K // 32), dtype=torch.uint8, device="cuda:0", generator=g)
+    x = torch.randn(M, K, device="cuda:0", generator=g).to(torch.bfloat16)
+    cols = _sampled(N)
+    wv = O.mx_decode(codes[cols].cpu().numpy(), scales[cols].cpu().numpy())
+    check(lib.mxfp4_linear(x, codes, scales)[:, cols], O.mx_linear(values(x), wv))
+    xq = lib.mxfp4_quantize_rows(x)
+    check(lib.qmm_mxfp4a4(*xq, codes, scales)[:, cols], O.mx_linear(O.mx_decode(*(t.cpu().numpy() for t in xq)), wv))
+    # gradients of zero but in the sampled weight rows
+    dy = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda:0")
+    dy[:, cols] = torch.randn(M, len(cols), device="cuda:0", generator=g).to(torch.bfloat16)
+    check(lib.mxfp4_linear_backward(dy, codes, scales), O.mx_linear_backward(values(dy[:, cols]), wv))
+
+
+def test_rows_beyond_two_to_the_31(lib):
+    import torch
+    R, K = 66000, 32768
+    announce(f"mxfp4_quantize_rows {R * K} values")
+    assert R * K > 2 ** 31
+    g = torch.Generator(device="cuda:0").manual_seed(3)
+    x = torch.randn(R, K, device="cuda:0", generator=g, dtype=torch.bfloat16)
+    codes, scales = lib.mxfp4_quantize_rows(x)
+    back = lib.mxfp4_dequantize_rows(codes, scales)
+    for r in (0, R // 2, R - 1):
+        ref = O.mx_encode(values(x[r:r + 1]))
+        assert np.array_equal(codes[r:r + 1].cpu().numpy(), ref[0]) and np.array_equal(scales[r:r + 1].cpu().numpy(), ref[1])
+        assert np.array_equal(values(back[r:r + 1]), O.mx_decode(*ref))

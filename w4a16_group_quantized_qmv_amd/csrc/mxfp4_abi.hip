@@ -15,7 +15,7 @@ using namespace w4a16;
 
 // Rows and columns: a tile's row and column numbers stay inside 31 bits.
 constexpr int64_t kMaxMxDim = int64_t{1} << 30;
-constexpr int64_t kMaxGrid = int64_t{1} << 31;      // workgroups of one launch
+constexpr int64_t kMaxThreads = int64_t{1} << 32;   // threads of one launch stay below
 
 uint64_t round256(uint64_t v) { return (v + 255) / 256 * 256; }
 
@@ -46,14 +46,15 @@ uint64_t padding_bytes(int32_t op, int64_t M, int64_t N) {
     if (!is_backward(op) || N % 8 == 0) return 0;
     return (op == MXFP4_GATE_UP_BACKWARD ? 2 : 1) * round256(static_cast<uint64_t>(M) * padded(N) * 2);
 }
-// The decode kernel serves the forward operators at up to 16 rows, unless a split is asked for; it
-// needs no workspace (4-bit activations are quantized on the way).
-bool decodes(int32_t op, int64_t M, int32_t split_k) {
-    return M <= kMxQmvRows && !is_backward(op) && split_k == 0;
+// The decode kernel serves the forward operators at up to 16 rows, unless a split is asked for (or
+// four columns per workgroup would make too large a launch); it needs no workspace (4-bit activations
+// are quantized on the way).
+bool decodes(int32_t op, int64_t M, int64_t N, int32_t split_k) {
+    return M <= kMxQmvRows && !is_backward(op) && split_k == 0 && ceil_div(N, 4) * 64 * kMxQmvWaves < kMaxThreads;
 }
 // Workspace that an operator cannot do without (the rest is for partials).
 uint64_t fixed_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k) {
-    if (op == MXFP4A4_LINEAR) return decodes(op, M, split_k) ? 0 : activation_bytes(M, K);
+    if (op == MXFP4A4_LINEAR) return decodes(op, M, N, split_k) ? 0 : activation_bytes(M, K);
     return padding_bytes(op, M, N);
 }
 
@@ -151,11 +152,13 @@ int make_plan(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k, int3
         if (st != W4A16_OK) return st;
     }
     Product p = product_of(op, M, N, K);
-    p.decode = decodes(op, M, split_k);
+    p.decode = decodes(op, M, N, split_k);
     p.cus = cus;
     choose(p, split_k, cus);
-    if (tiles_of(p) * p.split >= kMaxGrid) return W4A16_ERR_SHAPE;
     const MxTileShape& s = kMxTiles[p.tile];
+    if (!p.decode && (tiles_of(p) * p.split * 64 * s.waves >= kMaxThreads ||
+                      (p.split > 1 && ceil_div(p.M * p.N, 4) >= kMaxThreads)))
+        return W4A16_ERR_SHAPE;
     out->path = W4A16_PATH_MXFP4;
     out->tile_m = s.bm;
     out->tile_n = p.epilogue == MxEpilogue::kStore ? s.bn : s.bn / 2;
@@ -209,7 +212,7 @@ int fit(int32_t op, int64_t M, int64_t N, int64_t K, int32_t split_k, const void
     if (st != W4A16_OK) return st;
     if (p->split > 1 && (!usable || workspace_bytes - used < partial_bytes(*p))) {
         if (split_k > 1) return missing;
-        p->split = 1;
+        return make_plan(op, M, N, K, 1, 0, &plan, p);
     }
     return W4A16_OK;
 }

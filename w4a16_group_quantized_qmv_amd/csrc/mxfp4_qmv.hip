@@ -211,6 +211,8 @@ __device__ __forceinline__ uint32_t half_row_move(uint32_t into, uint32_t from) 
 // none is left.  A load takes 128 bytes of eight columns rather than 64 of sixteen: half lines
 // streamed past the cache measured 48.5 us against 41 on the 151936 x 2560 head, and 8 lane moves
 // per 2 KB put the blocks where the matrix instruction wants them.  K is a multiple of 512 and the scale rows are 16-byte aligned.
+// (Two weight sets in turn, for the gated pair, measured 17 us against the other form's 9 to 12 on 9728
+// columns and as much on 16384.)
 template <MxX X>
 __global__ __launch_bounds__(64 * kMxWideWaves) void mx_qmv_wide_kernel(const MxTileArgs p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -338,11 +340,14 @@ __global__ __launch_bounds__(64 * kMxWideWaves) void mx_qmv_wide_kernel(const Mx
 bool mx_qmv_shape(MxOperands op, int sets, int M, int N, int K, int cus, bool whole, MxQmvShape* out) {
     if (M > kMxQmvRows || op == MxOperands::kColumns) return false;
     const bool codes = op == MxOperands::kCodes;
-    // The wide form where its waves find several blocks each and the activations leave room for two
-    // workgroups per compute unit.
+    // The wide form where its waves find work for a few of its latencies.  Measured (K = 2560; narrow /
+    // wide us): 8 rows of 8192 columns 7.6 / 9.3, of 12288 10.9 / 9.4, of 32768 22.8 / 11.1; 4 rows of
+    // 16384 10.2 / 9.6; one row of 16384 8.7 / 9.5, of 24576 11.6 / 10.3; 16 rows of 16384 with K = 4096
+    // (one workgroup per compute unit) 21.3 / 16.5.
     const size_t x_bytes = static_cast<size_t>(M) * (codes ? K / 2 + K / kMxBlock : 2 * K);
     const int column_blocks = (N + 15) / 16;
-    out->wide = whole && sets == 1 && K % 512 == 0 && x_bytes <= 80 * 1024 && column_blocks >= 4 * cus;
+    out->wide = whole && sets == 1 && K % 512 == 0 && x_bytes <= 160 * 1024 &&
+                column_blocks >= (M <= 1 ? 5 : M <= 4 ? 4 : 3) * static_cast<int64_t>(cus);
     if (out->wide) {
         const int resident = std::min<int>(3, static_cast<int>(160 * 1024 / x_bytes));
         out->groups = std::min((column_blocks + kMxWideWaves - 1) / kMxWideWaves, resident * cus);

@@ -20,7 +20,7 @@ __all__ = [
     "MXFP4_BLOCK", "MXFP4_LINEAR", "MXFP4_LINEAR_BACKWARD", "MXFP4_QMM_A4", "MXFP4A4_LINEAR", "MXFP4_GATE_UP",
     "MXFP4_GATE_UP_BACKWARD", "PATH_MXFP4", "PATH_MXFP4_QMV", "mxfp4_plan", "mxfp4_quantize_rows", "mxfp4_dequantize_rows",
     "mxfp4_linear", "mxfp4_linear_backward", "qmm_mxfp4a4", "mxfp4a4_linear", "mxfp4_gate_up_swiglu",
-    "mxfp4_gate_up_swiglu_backward",
+    "mxfp4_gate_up_swiglu_backward", "PreparedMxfp4Linear", "PreparedMxfp4GateUp",
 ]
 
 MXFP4_BLOCK = 32
@@ -42,9 +42,12 @@ def _workspace_bytes(op, M, N, K, split_k, device):
     return int(mxfp4_plan(op, M, N, K, split_k)["workspace_bytes"])
 
 
-@functools.lru_cache(maxsize=None)
-def _bound():
+_B = None
+
+
+def _bind():
     """What every call needs, looked up once: torch, its stream query, and the library's functions."""
+    global _B
     import types
     torch = _torch()
     lib = load()
@@ -52,16 +55,17 @@ def _bound():
     if raw is None:
         def raw(index):
             return torch.cuda.current_stream(index).cuda_stream
-    return types.SimpleNamespace(torch=torch, tensor=torch.Tensor, bf16=torch.bfloat16, fp32=torch.float32,
-                                 u8=torch.uint8, empty=torch.empty, stream=raw,
-                                 current_device=torch.cuda.current_device,
-                                 fn={n: getattr(lib, n) for n in __all__ if hasattr(lib, n)})
+    _B = types.SimpleNamespace(torch=torch, tensor=torch.Tensor, bf16=torch.bfloat16, fp32=torch.float32,
+                               u8=torch.uint8, empty=torch.empty, stream=raw,
+                               current_device=torch.cuda.current_device,
+                               fn={n: getattr(lib, n) for n in __all__ if hasattr(lib, n)})
+    return _B
 
 
 def _tensor(t, name, dtype, shape, device=None):
     """Checks a tensor; every condition in one expression for the calls that are right."""
-    b = _bound()
-    if (isinstance(t, b.tensor) and t.dtype == dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
+    b = _B or _bind()
+    if (t.__class__ is b.tensor and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
             and (device is None or t.device == device)):
         return
     if not isinstance(t, b.tensor):
@@ -74,11 +78,12 @@ def _tensor(t, name, dtype, shape, device=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, not {device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, not {device}")
 
 
 def _matrix(t, name):
-    if not isinstance(t, _bound().tensor):
+    if not isinstance(t, (_B or _bind()).tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     shape = t.shape
     if len(shape) != 2:
@@ -87,22 +92,30 @@ def _matrix(t, name):
 
 
 def _weights(pair, name, device, like=None):
-    """Checks a (codes, scales) pair; returns (N, K)."""
+    """Checks a (codes, scales) pair; returns (N, K).  What is right takes the first expression."""
     codes, scales = pair
+    b = _B or _bind()
+    if (codes.__class__ is b.tensor and scales.__class__ is b.tensor and codes.dtype is b.u8 and scales.dtype is b.u8
+            and codes.device == device and scales.device == device and device.type == "cuda"
+            and codes.is_contiguous() and scales.is_contiguous()):
+        shape = codes.shape
+        if len(shape) == 2:
+            N, half = shape
+            if half and not half % 16 and scales.shape == (N, half // 16) and (like is None or (N, 2 * half) == like):
+                return N, 2 * half
     N, half = _matrix(codes, name)
     K = 2 * half
     if K == 0 or K % MXFP4_BLOCK:
         raise ValueError(f"{name}: K={K} must be a positive multiple of {MXFP4_BLOCK}")
     if like is not None and (N, K) != like:
         raise ValueError(f"{name} must be [{like[0]}, {like[1]}], got [{N}, {K}]")
-    u8 = _bound().u8
-    _tensor(codes, name, u8, (N, half), device)
-    _tensor(scales, name, u8, (N, K // MXFP4_BLOCK), device)
+    _tensor(codes, name, b.u8, (N, half), device)
+    _tensor(scales, name, b.u8, (N, K // MXFP4_BLOCK), device)
     return N, K
 
 
 def _output(t, name, shape, device, dtype=None):
-    b = _bound()
+    b = _B or _bind()
     dtype = dtype or b.bf16
     if t is None:
         return b.empty(shape, dtype=dtype, device=device)
@@ -113,7 +126,7 @@ def _output(t, name, shape, device, dtype=None):
 def _call(name, op, dims, device, stream, workspace, own, args, split_k=0):
     """One C-ABI call on ``device``: its workspace (allocated where the caller gave none), the stream,
     the status.  ``own``: tensors allocated for this call."""
-    b = _bound()
+    b = _B or _bind()
     index = device.index
     if index != b.current_device():
         with b.torch.cuda.device(device):
@@ -146,7 +159,7 @@ def _call(name, op, dims, device, stream, workspace, own, args, split_k=0):
 def mxfp4_quantize_rows(x, codes=None, scales=None, stream=None):
     """MXFP4 codes and scales of the rows of ``x`` (bf16 or fp32 ``[R, K]``); returns
     ``(codes, scales)``.  A block holding an infinity or a NaN decodes to NaN."""
-    b = _bound()
+    b = _B or _bind()
     R, K = _matrix(x, "x")
     if x.dtype != b.bf16 and x.dtype != b.fp32:
         raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
@@ -180,7 +193,7 @@ def _projection(name, op, x, codes, scales, y, split_k, workspace, stream):
     device = x.device
     N, K = _weights((codes, scales), "weight", device)
     back = op == MXFP4_LINEAR_BACKWARD
-    _tensor(x, "dy" if back else "x", _bound().bf16, (M, N if back else K))
+    _tensor(x, "dy" if back else "x", (_B or _bind()).bf16, (M, N if back else K))
     own = y is None
     y = _output(y, "dx" if back else "y", (M, K if back else N), device)
     _call(name, op, (M, N, K), device, stream, workspace, (y,) if own else (),
@@ -225,7 +238,7 @@ def mxfp4_gate_up_swiglu(x, gate, up, h=None, split_k: int = 0, workspace=None, 
     device = x.device
     N, K = _weights(gate, "gate", device)
     _weights(up, "up", device, (N, K))
-    _tensor(x, "x", _bound().bf16, (M, K))
+    _tensor(x, "x", (_B or _bind()).bf16, (M, K))
     own = h is None
     h = _output(h, "h", (M, N), device)
     _call("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), device, stream, workspace, (h,) if own else (),
@@ -242,8 +255,8 @@ def mxfp4_gate_up_swiglu_backward(x, gate, up, dh, dx=None, dgate=None, dup=None
     device = x.device
     N, K = _weights(gate, "gate", device)
     _weights(up, "up", device, (N, K))
-    _tensor(x, "x", _bound().bf16, (M, K))
-    _tensor(dh, "dh", _bound().bf16, (M, N), device)
+    _tensor(x, "x", (_B or _bind()).bf16, (M, K))
+    _tensor(dh, "dh", (_B or _bind()).bf16, (M, N), device)
     own = [t is None for t in (dx, dgate, dup)]
     dx = _output(dx, "dx", (M, K), device)
     dgate = _output(dgate, "dgate", (M, N), device)
@@ -253,3 +266,69 @@ def mxfp4_gate_up_swiglu_backward(x, gate, up, dh, dx=None, dgate=None, dup=None
           (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), dh.data_ptr(),
            dx.data_ptr(), dgate.data_ptr(), dup.data_ptr()), split_k)
     return dx, dgate, dup
+
+
+class _Prepared:
+    """A call with fixed tensors, validated once; ``plan`` is its launch plan and ``workspace`` what it
+    needs of that.  ``__call__`` issues one C-ABI call on the stream current at construction."""
+
+    def _prepare(self, name, op, dims, device, args, split_k, workspace):
+        b = _B or _bind()
+        with b.torch.cuda.device(device):
+            self.plan = mxfp4_plan(op, *dims, split_k)
+        need = self.plan["workspace_bytes"]
+        if workspace is None and need:
+            workspace = b.empty(need, dtype=b.u8, device=device)
+        self.workspace = workspace
+        ptr, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                           workspace.numel() * workspace.element_size())
+        self._name, self._fn, self._device = name, b.fn[name], device
+        self._args = (*args, *dims, split_k, ptr, nbytes, b.stream(device.index))
+
+    def _run(self):
+        b = _B or _bind()
+        if self._device.index != b.current_device():
+            with b.torch.cuda.device(self._device):
+                status = self._fn(*self._args)
+        else:
+            status = self._fn(*self._args)
+        if status:
+            _raise_for(status, self._name)
+
+
+class PreparedMxfp4Linear(_Prepared):
+    """One projection with fixed tensors (see ``PreparedLinear``): ``mxfp4_linear``, or with
+    ``four_bit_activations`` ``mxfp4a4_linear``.  Calling it returns ``y``."""
+
+    def __init__(self, x, codes, scales, y=None, four_bit_activations: bool = False, split_k: int = 0, workspace=None):
+        M, _ = _matrix(x, "x")
+        N, K = _weights((codes, scales), "weight", x.device)
+        _tensor(x, "x", (_B or _bind()).bf16, (M, K))
+        self.M, self.N, self.K, self.y = M, N, K, _output(y, "y", (M, N), x.device)
+        self._keep = (x, codes, scales)
+        name, op = (("mxfp4a4_linear", MXFP4A4_LINEAR) if four_bit_activations else ("mxfp4_linear", MXFP4_LINEAR))
+        self._prepare(name, op, (M, N, K), x.device,
+                      (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), self.y.data_ptr()), split_k, workspace)
+
+    def __call__(self):
+        self._run()
+        return self.y
+
+
+class PreparedMxfp4GateUp(_Prepared):
+    """``mxfp4_gate_up_swiglu`` with fixed tensors (see ``PreparedGateUp``).  Calling it returns ``h``."""
+
+    def __init__(self, x, gate, up, h=None, split_k: int = 0, workspace=None):
+        M, _ = _matrix(x, "x")
+        N, K = _weights(gate, "gate", x.device)
+        _weights(up, "up", x.device, (N, K))
+        _tensor(x, "x", (_B or _bind()).bf16, (M, K))
+        self.M, self.N, self.K, self.h = M, N, K, _output(h, "h", (M, N), x.device)
+        self._keep = (x, *gate, *up)
+        self._prepare("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), x.device,
+                      (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(),
+                       self.h.data_ptr()), split_k, workspace)
+
+    def __call__(self):
+        self._run()
+        return self.h
