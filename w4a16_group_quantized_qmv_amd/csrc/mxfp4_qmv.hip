@@ -363,7 +363,11 @@ bool mx_qmv_shape(MxOperands op, int sets, int M, int N, int K, int cus, bool wh
     out->columns = 16 / S;
     out->groups = (N + out->columns - 1) / out->columns;
     const int units = (K / kMxBlock + 4 * S - 1) / (4 * S);
-    out->share = (units + kMxQmvWaves - 1) / kMxQmvWaves;
+    // Shares of three units (two at 16 rows, whose activations are four loads a unit): one unit a wave
+    // leaves more waves than are resident at once.  Measured, one / three units a wave, us: one row of
+    // 9728 x 2560 6.0 / 5.3, of 12000 x 2592 7.2 / 6.3, of 1024 x 2560 3.3 / 3.1; 8 rows of 9728 x 2560
+    // 9.2 / 7.9; 16 rows one / two / three 9.7 / 9.6 / 10.6.
+    out->share = std::max((units + kMxQmvWaves - 1) / kMxQmvWaves, std::min(units, out->rows <= 8 ? 3 : 2));
     out->waves = (units + out->share - 1) / out->share;
     const int turns = (out->share + 3) / 4;
     out->batch = (out->share + turns - 1) / turns;

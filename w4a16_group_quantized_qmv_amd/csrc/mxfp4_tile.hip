@@ -54,6 +54,9 @@ __device__ __forceinline__ void loads_done_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// Keeps the loads before it and after it in this order, and apart.
+__device__ __forceinline__ void load_fence() { asm volatile("" ::: "memory"); }
+
 // WHOLE: the rows of scales are whole, aligned pieces of 16 bytes (kCodes) or of 4 (kRows).
 template <MxOperands OP, MxEpilogue EPI, int BM, int BN, int WR, int WC, int STAGES, bool WHOLE>
 __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs p, int tiles_m, int tiles_n) {
@@ -197,15 +200,18 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
                                         : kOutside;
                 w_codes[2 * at + i] =
                     __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(own_codes, co, 16 * first, 0));
+                load_fence();
             }
             const uint32_t so = static_cast<uint32_t>(column_of(unit_row) * blocks);
             if constexpr (WHOLE) {
                 w_scale[at] = __builtin_amdgcn_raw_buffer_load_b32(own_scales, first < blocks ? so : kOutside, first, 0);
             } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i) {
                     w_scale[2 * at + i] = __builtin_amdgcn_raw_buffer_load_b8(
                         own_scales, first + 2 * i + unit_block < blocks ? so + unit_block : kOutside, first + 2 * i, 0);
+                    load_fence();
+                }
             }
         }
     };
@@ -272,9 +278,11 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
                                                      s_rows, 16 * window < blocks ? s_off : kOutside, 16 * window, 0));
         } else if constexpr (kCodes) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 16; ++e) {
                 s_bytes[pair][e] = __builtin_amdgcn_raw_buffer_load_b8(
                     s_rows, 16 * window + e < blocks ? s_off : kOutside, 16 * window + e, 0);
+                load_fence();
+            }
         }
     };
     auto stash_scales = [&](int window, auto ic) {
@@ -387,7 +395,8 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
     constexpr auto more_loads = [](int parity) {
         return kCodes ? (parity == 0 ? (WHOLE ? 1 : 16) : 0) : kRows ? (parity == 1 ? (WHOLE ? 3 : 4) : 0) : 2;
     };
-    // loads issued after those that a step of this parity waits for
+    // loads issued after those that a step of this parity waits for (load_fence keeps each a separate
+    // instruction, in this order)
     constexpr auto pending = [more_loads](int parity) {
         int n = more_loads((parity + AHEAD) % 2);
         for (int s = 1; s < AHEAD; ++s) n += kStepLoads + more_loads((parity + s) % 2);
@@ -427,6 +436,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
         read(ic, Zero{});
         // every load of this step is issued here, as long as possible before the wait for it
         stage_step(t + AHEAD, Ahead{});
+        load_fence();
         if constexpr (kCodes && i % 2 == 0) load_scales((t >> 1) + PAIRS, ic);
         if constexpr (kRows && i % 2 == 1) load_pair(t + 3, std::integral_constant<int, (i + 3) / 2 % 2>{});
         if constexpr (kColumns) load_step(t + 4, ic);
