@@ -107,8 +107,9 @@ constexpr TileCost kTileCost[3][kNumMxTiles] = {
 constexpr double kSplitCost = 3.5, kPartialCost = 2e-6;
 constexpr int64_t kMaxSplit = 8;
 
-// The tile and the split with the lowest modelled time.  Measured against the best of the sweep the
-// choice is within 6% on the shapes above.
+// The tile and the split with the lowest modelled time.  Against the best of a sweep of every tile and
+// split on 20 shapes of kRows and kColumns the choice is 1% behind on average and 10% at worst (1024 rows
+// of 9728 values on 2560 columns: 79 us unsplit against 72 in four slices).
 void choose(Product& p, int32_t split_k, int32_t cus) {
     if (p.decode) return;
     const int64_t units = units_of(p);

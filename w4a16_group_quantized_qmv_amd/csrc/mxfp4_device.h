@@ -21,6 +21,14 @@ namespace w4a16 {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
+constexpr uint32_t kOutside = 0x80000000u;   // a buffer offset that no resource here reaches: loads give 0
+
+// A buffer over `bytes` from base, cut at 2 GiB (offsets inside a tile stay below that).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_resource(const void* base, int64_t bytes) {
+    const int64_t n = bytes < 0 ? 0 : (bytes > 0x7FFFFFFFll ? 0x7FFFFFFFll : bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(n), 0x00020000);
+}
+
 __device__ __forceinline__ float mx_scale(uint32_t e) { return __uint_as_float(e << 23); }
 
 // Eight codes of one word as bf16, in order (four instructions).
@@ -54,7 +62,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // 1 / (1 + 2^(-z log2 e)) from the hardware's exponential and reciprocal, each within a step of fp32;
 // the product with log2 e is off by half a step of itself, |z| 2^-24 of the result at most.  2^large
-// is infinite and its reciprocal 0, the limit.
+// is infinite and its reciprocal 0, the limit; below -87 the hardware's reciprocal flushes a result
+// under 2^-126 to 0, which a sum in bf16 or fp32 beside any normal value does not see.
 __device__ __forceinline__ float mx_sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }

@@ -21,18 +21,10 @@
 #include "mxfp4_internal.h"
 
 #include <algorithm>
-
 #include <type_traits>
 
 namespace w4a16 {
 namespace {
-
-constexpr uint32_t kOutside = 0x80000000u;   // a buffer offset that no resource here reaches
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t qmv_resource(const void* base, int64_t bytes) {
-    const int64_t n = bytes < 0 ? 0 : (bytes > 0x7FFFFFFFll ? 0x7FFFFFFFll : bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(n), 0x00020000);
-}
 
 // Activations of the decode kernels.
 enum class MxX { kBf16, kCodes, kQuantize };   // as they are, MXFP4, or bf16 quantized to MXFP4 on the way
@@ -90,11 +82,11 @@ __global__ __launch_bounds__(1024) void mx_qmv_kernel(const MxTileArgs p, int sh
     __amdgpu_buffer_rsrc_t cr[NP], sr[NP];
 #pragma unroll
     for (int s = 0; s < NP; ++s) {
-        cr[s] = qmv_resource(p.w[s] + static_cast<int64_t>(c0) * row_codes, columns * row_codes);
-        sr[s] = qmv_resource(p.w_scales[s] + static_cast<int64_t>(c0) * blocks, columns * blocks);
+        cr[s] = mx_resource(p.w[s] + static_cast<int64_t>(c0) * row_codes, columns * row_codes);
+        sr[s] = mx_resource(p.w_scales[s] + static_cast<int64_t>(c0) * blocks, columns * blocks);
     }
-    const __amdgpu_buffer_rsrc_t xr = qmv_resource(p.a[0], static_cast<int64_t>(p.M) * p.pitch);
-    const __amdgpu_buffer_rsrc_t xsr = qmv_resource(p.a_scales, CODES ? static_cast<int64_t>(p.M) * blocks : 0);
+    const __amdgpu_buffer_rsrc_t xr = mx_resource(p.a[0], static_cast<int64_t>(p.M) * p.pitch);
+    const __amdgpu_buffer_rsrc_t xsr = mx_resource(p.a_scales, CODES ? static_cast<int64_t>(p.M) * blocks : 0);
     const int own_block = 4 * slice + q;                      // this lane's block of a unit
 
     f32x4_t acc[NP];
@@ -258,8 +250,8 @@ __global__ __launch_bounds__(64 * kMxWideWaves) void mx_qmv_wide_kernel(const Mx
     auto load = [&](int block, int window, auto ic) {
         constexpr int par = decltype(ic)::value;
         const int64_t c0 = 16 * static_cast<int64_t>(block), left = block < column_blocks ? p.N - c0 : 0;
-        const __amdgpu_buffer_rsrc_t cr = qmv_resource(p.w[0] + c0 * row_codes, left * row_codes);
-        const __amdgpu_buffer_rsrc_t sr = qmv_resource(p.w_scales[0] + c0 * blocks, left * blocks);
+        const __amdgpu_buffer_rsrc_t cr = mx_resource(p.w[0] + c0 * row_codes, left * row_codes);
+        const __amdgpu_buffer_rsrc_t sr = mx_resource(p.w_scales[0] + c0 * blocks, left * blocks);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             codes[par][i] = __builtin_bit_cast(

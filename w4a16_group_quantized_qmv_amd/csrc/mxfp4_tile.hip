@@ -10,25 +10,35 @@
 //
 // One frame serves all of them, because every staged row is 128 bytes per pipeline step: 64 bf16
 // values or 256 codes.
-//  * LDS holds BM rows of the left operand and BN rows of the weights, two stages.  The 16-byte
-//    chunk c of row r lies at c ^ ((r / 2) % 8): sixteen consecutive rows read one chunk from all
-//    sixteen 16-byte bank groups.  kColumns also folds r / 16 in, since its writes go four rows apart.
-//  * The left operand, and codes that need no decoding, go from memory to LDS directly.  Weights
-//    to be decoded are loaded into registers one step ahead, decoded (four instructions per eight
-//    values) and written to LDS once per workgroup, so the decoding is shared by all waves.
+//  * LDS holds stages of BM rows of the left operand and BN rows of the weights.  The 16-byte chunk c
+//    of row r lies at c ^ ((r / 2) % 8): sixteen consecutive rows read one chunk from all sixteen
+//    16-byte bank groups.
+//  * The left operand, and codes that need no decoding, go from memory to LDS directly.  Weights to
+//    be decoded are loaded into registers two to four steps ahead, decoded (four instructions per
+//    eight values) one step ahead and written to LDS once per workgroup, so that all waves share the
+//    decoding.  A step waits only for the loads that it uses (counted, in the order of issue).
 //  * kColumns needs, for one output column, eight consecutive contraction values in a lane, while
-//    the codes are packed along the output columns.  A thread takes 8 weight rows x 4 columns
-//    (2 bytes of each row), decodes pairs of columns and exchanges halves with 16 byte permutes.
+//    the codes are packed along the output columns.  Decoded rows are staged as they come, from
+//    whole 128-byte lines; the operand reads are the transposing ones.  (Bytes exchanged by permutes
+//    before the write, from 2-byte loads: 4096 x 9728 x 2560 took 252 us, this 208.)
 //  * Of the 128 bytes, MFMA step j of lane half h takes chunk 4 h + j.  For codes a chunk is one
 //    block, so the four scale bytes that a lane needs in a pipeline step are one aligned word of the
 //    row's scales.  (Steps of whole 128-byte lines: taking 64 bytes from each of two lines, which also
-//    gives such words, is twice the requests to L2.)
+//    gives such words, is twice the requests to L2; 66 us against 58 at 4096 x 9728 x 2560.)
 //  * The weights are the MFMA's row operand, so a lane's results are four consecutive output
 //    columns of one row; each wave turns its block through LDS and stores whole 16-byte pieces.
 //  * With two weight sets (gate and up) the 32-column blocks of the tile alternate between them, so
 //    a lane holds both products of the same element and the activation needs no exchange.
 //  * Split-K: slice z takes a contiguous run of steps and writes fp32 partials; the slices are
 //    summed in order by a second launch, so results do not depend on timing.
+//
+// Bound by the matrix cores from some 500 rows on, at the clock that the card keeps under them (1.9
+// to 2.06 GHz): the 16-bit kinds keep them busy 61 to 63% of the time, kCodes 39 to 45%.  On MI355X,
+// 4096 rows, 9728 x 2560 weights: kCodes 58 us (3.5 PF), kRows 190 to 205 us (1.0 PF; contraction of
+// 9728 or 2560), kColumns 208 us (0.98 PF), kGlu 340 us for both products (1.2 PF).  The rest is the
+// L2's latency and traffic: with the left operand's loads left out kRows took 161 us and kColumns 169.
+// Below, the number of workgroups bounds it (the cost model chooses among tiles and splits): kRows of
+// 512 rows 36 us, kGlu 47 to 52 us.
 #include "mxfp4_device.h"
 #include "mxfp4_internal.h"
 
@@ -36,13 +46,6 @@
 
 namespace w4a16 {
 namespace {
-
-constexpr uint32_t kOutside = 0x80000000u;   // a buffer offset that no resource here reaches
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_resource(const void* base, int64_t bytes) {
-    const int64_t n = bytes < 0 ? 0 : (bytes > 0x7FFFFFFFll ? 0x7FFFFFFFll : bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(n), 0x00020000);
-}
 
 // All but the last PENDING loads of this wave have arrived, its LDS accesses are done, and all waves
 // are here.
@@ -618,7 +621,12 @@ const MxTileShape kMxTiles[kNumMxTiles] = {{128, 128, 4}, {256, 256, 8}, {64, 12
 
 namespace {
 
-template <int BM, int BN, int WR, int WC, int STAGES>
+// Stages of the left operand; CODE_STAGES of the form that stages both operands as they come.  Four
+// stages cover a latency with three steps of loads, at the cost of a second workgroup beside: 64 x 128
+// keeps both.  192 x 256 fits four of the left operand and two of decoded weights into 160 KB (4096 x
+// 2560 with 9728 values: 198 us with two, 190 with four; kColumns 211 and 208), 256 x 256 does not;
+// 128 x 128 gained nothing from them.
+template <int BM, int BN, int WR, int WC, int STAGES, int CODE_STAGES>
 hipError_t launch_shape(MxOperands op, MxEpilogue epi, const MxTileArgs& args, hipStream_t stream) {
     const int bc = epi == MxEpilogue::kStore ? BN : BN / 2;
     const int tiles_m = (args.M + BM - 1) / BM, tiles_n = (args.N + bc - 1) / bc;
@@ -632,8 +640,8 @@ hipError_t launch_shape(MxOperands op, MxEpilogue epi, const MxTileArgs& args, h
     if (op == O::kCodes) {
         const bool whole = args.L % 512 == 0 && ((reinterpret_cast<uintptr_t>(args.a_scales) |
                                                   reinterpret_cast<uintptr_t>(args.w_scales[0])) & 15) == 0;
-        return whole ? run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, STAGES, true>)
-                     : run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, STAGES, false>);
+        return whole ? run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, CODE_STAGES, true>)
+                     : run(mx_tile_kernel<O::kCodes, E::kStore, BM, BN, WR, WC, CODE_STAGES, false>);
     }
     if (op == O::kColumns) return run(mx_tile_kernel<O::kColumns, E::kStore, BM, BN, WR, WC, STAGES, true>);
     // words of four scale bytes in every row
@@ -653,10 +661,10 @@ hipError_t launch_shape(MxOperands op, MxEpilogue epi, const MxTileArgs& args, h
 
 hipError_t launch_mx_tile(MxOperands op, MxEpilogue epi, int tile, const MxTileArgs& args, hipStream_t stream) {
     switch (tile) {
-        case 0: return launch_shape<128, 128, 2, 2, 2>(op, epi, args, stream);
-        case 1: return launch_shape<256, 256, 2, 4, 2>(op, epi, args, stream);
-        case 2: return launch_shape<64, 128, 2, 2, 4>(op, epi, args, stream);
-        case 3: return launch_shape<192, 256, 2, 4, 2>(op, epi, args, stream);
+        case 0: return launch_shape<128, 128, 2, 2, 2, 2>(op, epi, args, stream);
+        case 1: return launch_shape<256, 256, 2, 4, 2, 2>(op, epi, args, stream);
+        case 2: return launch_shape<64, 128, 2, 2, 4, 4>(op, epi, args, stream);
+        case 3: return launch_shape<192, 256, 2, 4, 4, 2>(op, epi, args, stream);
         default: return hipErrorInvalidValue;
     }
 }
