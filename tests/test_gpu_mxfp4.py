@@ -615,6 +615,11 @@ def test_prepared_calls(lib):
         lib.PreparedMxfp4Linear(x[:, :512].contiguous(), *w)
     with pytest.raises(ValueError, match="WORKSPACE"):
         lib.PreparedMxfp4Linear(x, *w, split_k=3, workspace=torch.empty(4, device="cuda:0"))()
+    room = torch.empty(1 << 20)
+    with pytest.raises(ValueError, match="workspace"):
+        lib.PreparedMxfp4Linear(x, *w, split_k=3, workspace=room)
+    with pytest.raises(ValueError, match="workspace"):
+        lib.PreparedMxfp4GateUp(x, w, u, split_k=2, workspace=room.cuda()[::2])
 
 
 def test_timing_request_takes_the_product(lib):

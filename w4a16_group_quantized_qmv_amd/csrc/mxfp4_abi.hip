@@ -110,7 +110,7 @@ constexpr int64_t kMaxSplit = 8;
 // The tile and the split with the lowest modelled time.  Against the best of a sweep of every tile and
 // split on 20 shapes of kRows and kColumns the choice is 1% behind on average and 10% at worst (1024 rows
 // of 9728 values on 2560 columns: 79 us unsplit against 72 in four slices).
-void choose(Product& p, int32_t split_k, int32_t cus) {
+void choose(Product& p, int32_t split_k, int64_t cus) {
     if (p.decode) return;
     const int64_t units = units_of(p);
     const int64_t steps = ceil_div(p.L, mx_step(p.operands)) * (p.operands == MxOperands::kColumns ? p.sets : 1);

@@ -62,8 +62,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // 1 / (1 + 2^(-z log2 e)) from the hardware's exponential and reciprocal, each within a step of fp32;
 // the product with log2 e is off by half a step of itself, |z| 2^-24 of the result at most.  2^large
-// is infinite and its reciprocal 0, the limit; below -87 the hardware's reciprocal flushes a result
-// under 2^-126 to 0, which a sum in bf16 or fp32 beside any normal value does not see.
+// is infinite and its reciprocal 0, the limit; below z = -87 the hardware's reciprocal
+// flushes a result under 2^-126 to 0, an error of 2^-126 at most.
 __device__ __forceinline__ float mx_sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }

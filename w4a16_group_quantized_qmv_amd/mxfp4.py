@@ -123,6 +123,11 @@ def _output(t, name, shape, device, dtype=None):
     return t
 
 
+def _check_workspace(workspace, device):
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+
+
 def _call(name, op, dims, device, stream, workspace, own, args, split_k=0):
     """One C-ABI call on ``device``: its workspace (allocated where the caller gave none), the stream,
     the status.  ``own``: tensors allocated for this call."""
@@ -141,8 +146,8 @@ def _call(name, op, dims, device, stream, workspace, own, args, split_k=0):
             if workspace is None:
                 workspace = b.empty(need, dtype=b.u8, device=device)
                 own = (*own, workspace)
-            elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != device:
-                raise ValueError(f"workspace must be a contiguous tensor on {device}")
+            else:
+                _check_workspace(workspace, device)
             args += (*dims, split_k, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     else:
         args += dims
@@ -279,6 +284,8 @@ class _Prepared:
         need = self.plan["workspace_bytes"]
         if workspace is None and need:
             workspace = b.empty(need, dtype=b.u8, device=device)
+        elif workspace is not None:
+            _check_workspace(workspace, device)
         self.workspace = workspace
         ptr, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
                                                            workspace.numel() * workspace.element_size())
