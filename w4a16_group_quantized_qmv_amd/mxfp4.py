@@ -42,33 +42,32 @@ def _workspace_bytes(op, M, N, K, split_k, device):
     return int(mxfp4_plan(op, M, N, K, split_k)["workspace_bytes"])
 
 
-_B = None
+# What every call needs, looked up once by _bind: torch, its types and queries, the library's functions.
+_T = _BF16 = _FP32 = _U8 = _empty = _raw_stream = _current = None
+_FN = {}
 
 
 def _bind():
-    """What every call needs, looked up once: torch, its stream query, and the library's functions."""
-    global _B
-    import types
+    global _T, _BF16, _FP32, _U8, _empty, _raw_stream, _current
     torch = _torch()
     lib = load()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        def raw(index):
+    _FN.update((n, getattr(lib, n)) for n in __all__ if hasattr(lib, n))
+    _BF16, _FP32, _U8, _empty = torch.bfloat16, torch.float32, torch.uint8, torch.empty
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is None:
+        def _raw_stream(index):
             return torch.cuda.current_stream(index).cuda_stream
-    _B = types.SimpleNamespace(torch=torch, tensor=torch.Tensor, bf16=torch.bfloat16, fp32=torch.float32,
-                               u8=torch.uint8, empty=torch.empty, stream=raw,
-                               current_device=torch.cuda.current_device,
-                               fn={n: getattr(lib, n) for n in __all__ if hasattr(lib, n)})
-    return _B
+    _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _T = torch.Tensor
 
 
-def _tensor(t, name, dtype, shape, device=None):
-    """Checks a tensor; every condition in one expression for the calls that are right."""
-    b = _B or _bind()
-    if (t.__class__ is b.tensor and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
-            and (device is None or t.device == device)):
+def _tensor(t, name, dtype, shape, index=None):
+    """Checks a tensor, on GPU ``index`` if that is given; every condition in one expression for the
+    calls that are right."""
+    if (t.__class__ is _T and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()
+            and (index is None or t.get_device() == index)):
         return
-    if not isinstance(t, b.tensor):
+    if not isinstance(t, _T):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -78,12 +77,15 @@ def _tensor(t, name, dtype, shape, device=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, not {device}")
+    if index is not None and t.get_device() != index:
+        where = f"cuda:{index}" if index >= 0 else "the CPU"
+        raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, another on {where}")
 
 
 def _matrix(t, name):
-    if not isinstance(t, (_B or _bind()).tensor):
+    if _T is None:
+        _bind()
+    if not isinstance(t, _T):
         raise TypeError(f"{name} must be a torch.Tensor")
     shape = t.shape
     if len(shape) != 2:
@@ -91,12 +93,10 @@ def _matrix(t, name):
     return shape
 
 
-def _weights(pair, name, device, like=None):
-    """Checks a (codes, scales) pair; returns (N, K).  What is right takes the first expression."""
-    codes, scales = pair
-    b = _B or _bind()
-    if (codes.__class__ is b.tensor and scales.__class__ is b.tensor and codes.dtype is b.u8 and scales.dtype is b.u8
-            and codes.device == device and scales.device == device and device.type == "cuda"
+def _weights(codes, scales, name, index, like=None):
+    """Checks codes and scales; returns (N, K).  What is right takes the first expression."""
+    if (codes.__class__ is _T and scales.__class__ is _T and codes.dtype is _U8 and scales.dtype is _U8
+            and 0 <= index == codes.get_device() == scales.get_device()
             and codes.is_contiguous() and scales.is_contiguous()):
         shape = codes.shape
         if len(shape) == 2:
@@ -109,34 +109,33 @@ def _weights(pair, name, device, like=None):
         raise ValueError(f"{name}: K={K} must be a positive multiple of {MXFP4_BLOCK}")
     if like is not None and (N, K) != like:
         raise ValueError(f"{name} must be [{like[0]}, {like[1]}], got [{N}, {K}]")
-    _tensor(codes, name, b.u8, (N, half), device)
-    _tensor(scales, name, b.u8, (N, K // MXFP4_BLOCK), device)
+    _tensor(codes, name, _U8, (N, half), index)
+    _tensor(scales, name, _U8, (N, K // MXFP4_BLOCK), index)
     return N, K
 
 
-def _output(t, name, shape, device, dtype=None):
-    b = _B or _bind()
-    dtype = dtype or b.bf16
+def _output(t, name, shape, x, dtype):
+    """An output beside ``x``: allocated, or checked if it is given."""
     if t is None:
-        return b.empty(shape, dtype=dtype, device=device)
-    _tensor(t, name, dtype, shape, device)
+        return x.new_empty(shape) if x.dtype is dtype else x.new_empty(shape, dtype=dtype)
+    _tensor(t, name, dtype, shape, x.get_device())
     return t
 
 
-def _check_workspace(workspace, device):
-    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+def _check_workspace(workspace, index):
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != index:
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
 
 
-def _call(name, op, dims, device, stream, workspace, own, args, split_k=0):
-    """One C-ABI call on ``device``: its workspace (allocated where the caller gave none), the stream,
+def _call(name, op, dims, index, stream, workspace, own, args, split_k=0):
+    """One C-ABI call on GPU ``index``: its workspace (allocated where the caller gave none), the stream,
     the status.  ``own``: tensors allocated for this call."""
-    b = _B or _bind()
-    index = device.index
-    if index != b.current_device():
-        with b.torch.cuda.device(device):
-            return _call(name, op, dims, device, stream, workspace, own, args, split_k)
-    if op is not None:
+    if index != _current():
+        with _torch().cuda.device(index):
+            return _call(name, op, dims, index, stream, workspace, own, args, split_k)
+    if op is None:
+        args += dims
+    else:
         if split_k < 0:
             raise ValueError(f"split_k={split_k} must not be negative")
         need = _workspace_bytes(op, *dims, split_k, index)
@@ -144,19 +143,16 @@ def _call(name, op, dims, device, stream, workspace, own, args, split_k=0):
             args += (*dims, split_k, None, 0)
         else:
             if workspace is None:
-                workspace = b.empty(need, dtype=b.u8, device=device)
+                workspace = _empty(need, dtype=_U8, device=f"cuda:{index}")
                 own = (*own, workspace)
             else:
-                _check_workspace(workspace, device)
+                _check_workspace(workspace, index)
             args += (*dims, split_k, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    else:
-        args += dims
     if stream is None:
-        handle = b.stream(index)
+        status = _FN[name](*args, _raw_stream(index))
     else:
-        handle = _stream_handle(stream)
-        _keep_for_stream(stream, device, *own)
-    status = b.fn[name](*args, handle)
+        _keep_for_stream(stream, _torch().device("cuda", index), *own)
+        status = _FN[name](*args, _stream_handle(stream))
     if status:
         _raise_for(status, name)
 
@@ -164,44 +160,42 @@ def _call(name, op, dims, device, stream, workspace, own, args, split_k=0):
 def mxfp4_quantize_rows(x, codes=None, scales=None, stream=None):
     """MXFP4 codes and scales of the rows of ``x`` (bf16 or fp32 ``[R, K]``); returns
     ``(codes, scales)``.  A block holding an infinity or a NaN decodes to NaN."""
-    b = _B or _bind()
     R, K = _matrix(x, "x")
-    if x.dtype != b.bf16 and x.dtype != b.fp32:
+    if x.dtype is not _BF16 and x.dtype is not _FP32:
         raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
     if K == 0 or K % MXFP4_BLOCK:
         raise ValueError(f"K={K} must be a positive multiple of {MXFP4_BLOCK}")
     _tensor(x, "x", x.dtype, (R, K))
-    device = x.device
     given = (codes, scales)
-    codes = _output(codes, "codes", (R, K // 2), device, b.u8)
-    scales = _output(scales, "scales", (R, K // MXFP4_BLOCK), device, b.u8)
-    _call("mxfp4_quantize_rows", None, (R, K), device, stream, None,
+    codes = _output(codes, "codes", (R, K // 2), x, _U8)
+    scales = _output(scales, "scales", (R, K // MXFP4_BLOCK), x, _U8)
+    _call("mxfp4_quantize_rows", None, (R, K), x.get_device(), stream, None,
           [t for t, g in zip((codes, scales), given) if g is None] if stream is not None else (),
-          (x.data_ptr(), int(x.dtype == b.fp32), codes.data_ptr(), scales.data_ptr()))
+          (x.data_ptr(), int(x.dtype is _FP32), codes.data_ptr(), scales.data_ptr()))
     return codes, scales
 
 
 def mxfp4_dequantize_rows(codes, scales, y=None, stream=None):
     """The values of MXFP4 rows as bf16 ``[R, K]`` (exact); returns y."""
     _matrix(codes, "codes")
-    device = codes.device
-    R, K = _weights((codes, scales), "rows", device)
+    index = codes.get_device()
+    R, K = _weights(codes, scales, "rows", index)
     own = y is None
-    y = _output(y, "y", (R, K), device)
-    _call("mxfp4_dequantize_rows", None, (R, K), device, stream, None, (y,) if own else (),
+    y = _output(y, "y", (R, K), codes, _BF16)
+    _call("mxfp4_dequantize_rows", None, (R, K), index, stream, None, (y,) if own else (),
           (codes.data_ptr(), scales.data_ptr(), y.data_ptr()))
     return y
 
 
 def _projection(name, op, x, codes, scales, y, split_k, workspace, stream):
     M, _ = _matrix(x, "x")
-    device = x.device
-    N, K = _weights((codes, scales), "weight", device)
+    index = x.get_device()
+    N, K = _weights(codes, scales, "weight", index)
     back = op == MXFP4_LINEAR_BACKWARD
-    _tensor(x, "dy" if back else "x", (_B or _bind()).bf16, (M, N if back else K))
+    _tensor(x, "dy" if back else "x", _BF16, (M, N if back else K))
     own = y is None
-    y = _output(y, "dx" if back else "y", (M, K if back else N), device)
-    _call(name, op, (M, N, K), device, stream, workspace, (y,) if own else (),
+    y = _output(y, "dx" if back else "y", (M, K if back else N), x, _BF16)
+    _call(name, op, (M, N, K), index, stream, workspace, (y,) if own else (),
           (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr()), split_k)
     return y
 
@@ -226,12 +220,12 @@ def mxfp4a4_linear(x, codes, scales, y=None, split_k: int = 0, workspace=None, s
 def qmm_mxfp4a4(xq, xs, codes, scales, y=None, split_k: int = 0, workspace=None, stream=None):
     """``y = X . W^T`` of two MXFP4 operands (``xq``, ``xs`` from ``mxfp4_quantize_rows``)."""
     M, _ = _matrix(xq, "xq")
-    device = xq.device
-    N, K = _weights((codes, scales), "weight", device)
-    _weights((xq, xs), "x", device, (M, K))
+    index = xq.get_device()
+    N, K = _weights(codes, scales, "weight", index)
+    _weights(xq, xs, "x", index, (M, K))
     own = y is None
-    y = _output(y, "y", (M, N), device)
-    _call("qmm_mxfp4a4", MXFP4_QMM_A4, (M, N, K), device, stream, workspace, (y,) if own else (),
+    y = _output(y, "y", (M, N), xq, _BF16)
+    _call("qmm_mxfp4a4", MXFP4_QMM_A4, (M, N, K), index, stream, workspace, (y,) if own else (),
           (xq.data_ptr(), xs.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr()), split_k)
     return y
 
@@ -240,13 +234,13 @@ def mxfp4_gate_up_swiglu(x, gate, up, h=None, split_k: int = 0, workspace=None, 
     """``h = silu(x . Wg^T) * (x . Wu^T)`` in one kernel; ``gate`` and ``up`` are ``(codes, scales)``
     pairs of one shape.  Returns h."""
     M, _ = _matrix(x, "x")
-    device = x.device
-    N, K = _weights(gate, "gate", device)
-    _weights(up, "up", device, (N, K))
-    _tensor(x, "x", (_B or _bind()).bf16, (M, K))
+    index = x.get_device()
+    N, K = _weights(*gate, "gate", index)
+    _weights(*up, "up", index, (N, K))
+    _tensor(x, "x", _BF16, (M, K))
     own = h is None
-    h = _output(h, "h", (M, N), device)
-    _call("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), device, stream, workspace, (h,) if own else (),
+    h = _output(h, "h", (M, N), x, _BF16)
+    _call("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), index, stream, workspace, (h,) if own else (),
           (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), h.data_ptr()),
           split_k)
     return h
@@ -257,16 +251,16 @@ def mxfp4_gate_up_swiglu_backward(x, gate, up, dh, dx=None, dgate=None, dup=None
     """Backward pass of ``mxfp4_gate_up_swiglu`` from ``x`` and ``dh``; returns ``(dx, dgate, dup)``,
     the last two the gradients of both projections' outputs.  The weights are frozen."""
     M, _ = _matrix(x, "x")
-    device = x.device
-    N, K = _weights(gate, "gate", device)
-    _weights(up, "up", device, (N, K))
-    _tensor(x, "x", (_B or _bind()).bf16, (M, K))
-    _tensor(dh, "dh", (_B or _bind()).bf16, (M, N), device)
+    index = x.get_device()
+    N, K = _weights(*gate, "gate", index)
+    _weights(*up, "up", index, (N, K))
+    _tensor(x, "x", _BF16, (M, K))
+    _tensor(dh, "dh", _BF16, (M, N), index)
     own = [t is None for t in (dx, dgate, dup)]
-    dx = _output(dx, "dx", (M, K), device)
-    dgate = _output(dgate, "dgate", (M, N), device)
-    dup = _output(dup, "dup", (M, N), device)
-    _call("mxfp4_gate_up_swiglu_backward", MXFP4_GATE_UP_BACKWARD, (M, N, K), device, stream, workspace,
+    dx = _output(dx, "dx", (M, K), x, _BF16)
+    dgate = _output(dgate, "dgate", (M, N), x, _BF16)
+    dup = _output(dup, "dup", (M, N), x, _BF16)
+    _call("mxfp4_gate_up_swiglu_backward", MXFP4_GATE_UP_BACKWARD, (M, N, K), index, stream, workspace,
           tuple(t for t, o in zip((dx, dgate, dup), own) if o),
           (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), dh.data_ptr(),
            dx.data_ptr(), dgate.data_ptr(), dup.data_ptr()), split_k)
@@ -277,25 +271,23 @@ class _Prepared:
     """A call with fixed tensors, validated once; ``plan`` is its launch plan and ``workspace`` what it
     needs of that.  ``__call__`` issues one C-ABI call on the stream current at construction."""
 
-    def _prepare(self, name, op, dims, device, args, split_k, workspace):
-        b = _B or _bind()
-        with b.torch.cuda.device(device):
+    def _prepare(self, name, op, dims, index, args, split_k, workspace):
+        with _torch().cuda.device(index):
             self.plan = mxfp4_plan(op, *dims, split_k)
         need = self.plan["workspace_bytes"]
         if workspace is None and need:
-            workspace = b.empty(need, dtype=b.u8, device=device)
+            workspace = _empty(need, dtype=_U8, device=f"cuda:{index}")
         elif workspace is not None:
-            _check_workspace(workspace, device)
+            _check_workspace(workspace, index)
         self.workspace = workspace
         ptr, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
                                                            workspace.numel() * workspace.element_size())
-        self._name, self._fn, self._device = name, b.fn[name], device
-        self._args = (*args, *dims, split_k, ptr, nbytes, b.stream(device.index))
+        self._name, self._fn, self._device = name, _FN[name], index
+        self._args = (*args, *dims, split_k, ptr, nbytes, _raw_stream(index))
 
     def _run(self):
-        b = _B or _bind()
-        if self._device.index != b.current_device():
-            with b.torch.cuda.device(self._device):
+        if self._device != _current():
+            with _torch().cuda.device(self._device):
                 status = self._fn(*self._args)
         else:
             status = self._fn(*self._args)
@@ -309,12 +301,12 @@ class PreparedMxfp4Linear(_Prepared):
 
     def __init__(self, x, codes, scales, y=None, four_bit_activations: bool = False, split_k: int = 0, workspace=None):
         M, _ = _matrix(x, "x")
-        N, K = _weights((codes, scales), "weight", x.device)
-        _tensor(x, "x", (_B or _bind()).bf16, (M, K))
-        self.M, self.N, self.K, self.y = M, N, K, _output(y, "y", (M, N), x.device)
+        N, K = _weights(codes, scales, "weight", x.get_device())
+        _tensor(x, "x", _BF16, (M, K))
+        self.M, self.N, self.K, self.y = M, N, K, _output(y, "y", (M, N), x, _BF16)
         self._keep = (x, codes, scales)
         name, op = (("mxfp4a4_linear", MXFP4A4_LINEAR) if four_bit_activations else ("mxfp4_linear", MXFP4_LINEAR))
-        self._prepare(name, op, (M, N, K), x.device,
+        self._prepare(name, op, (M, N, K), x.get_device(),
                       (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), self.y.data_ptr()), split_k, workspace)
 
     def __call__(self):
@@ -327,12 +319,12 @@ class PreparedMxfp4GateUp(_Prepared):
 
     def __init__(self, x, gate, up, h=None, split_k: int = 0, workspace=None):
         M, _ = _matrix(x, "x")
-        N, K = _weights(gate, "gate", x.device)
-        _weights(up, "up", x.device, (N, K))
-        _tensor(x, "x", (_B or _bind()).bf16, (M, K))
-        self.M, self.N, self.K, self.h = M, N, K, _output(h, "h", (M, N), x.device)
+        N, K = _weights(*gate, "gate", x.get_device())
+        _weights(*up, "up", x.get_device(), (N, K))
+        _tensor(x, "x", _BF16, (M, K))
+        self.M, self.N, self.K, self.h = M, N, K, _output(h, "h", (M, N), x, _BF16)
         self._keep = (x, *gate, *up)
-        self._prepare("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), x.device,
+        self._prepare("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), x.get_device(),
                       (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(),
                        self.h.data_ptr()), split_k, workspace)
 
