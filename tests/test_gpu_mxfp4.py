@@ -211,6 +211,26 @@ LARGE_BACK_SIZES = [(2323, 72, 4928), (1298, 72, 5952), (321, 75, 5408)]
 LARGE_GATED_SIZES = [(390, 11227, 96), (257, 10998, 96), (2325, 72, 4896), (1422, 75, 5408), (201, 2000, 1376)]
 
 
+# long contractions at decode rows: shares of one and two batches a wave, whole and ragged, one
+# workgroup a compute unit and more
+@pytest.mark.parametrize("M,N,K", [(1, 1500, 8192), (2, 1029, 9728), (3, 1100, 14336), (4, 500, 9728), (6, 2100, 8224),
+                                   (7, 2070, 9728), (8, 2051, 16416), (8, 2100, 32768), (16, 70, 9728), (13, 33, 16384)])
+def test_long_contractions_at_decode_rows(lib, M, N, K):
+    import torch
+    announce(f"mxfp4 long decode M={M} N={N} K={K}")
+    rng = np.random.default_rng(M + N + K + 8)
+    w, wv = weight(rng, N, K)
+    x = bf16_values(rng.standard_normal((M, K)))
+    y, untouched = guarded(M, N, offset=1)
+    lib.mxfp4_linear(bf16(x), *w, y=y)
+    check(y, O.mx_linear(x, wv))
+    xq = lib.mxfp4_quantize_rows(bf16(x))
+    z = lib.qmm_mxfp4a4(*xq, *w)
+    check(z, O.mx_linear(O.mx_decode(*(t.cpu().numpy() for t in xq)), wv))
+    assert torch.equal(z, lib.mxfp4a4_linear(bf16(x), *w)) and untouched()
+    check(lib.mxfp4_gate_up_swiglu(bf16(x), w, (w[0].flip(0), w[1].flip(0))), O.mx_gate_up(x, wv, wv[::-1]))
+
+
 @pytest.mark.parametrize("M,N,K", WIDE_SIZES)
 def test_many_columns_at_decode_rows(lib, M, N, K):
     import torch

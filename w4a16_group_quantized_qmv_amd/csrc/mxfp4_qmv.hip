@@ -359,8 +359,27 @@ bool mx_qmv_shape(MxOperands op, int sets, int M, int N, int K, int cus, bool wh
     // leaves more waves than are resident at once.  Measured, one / three units a wave, us: one row of
     // 9728 x 2560 6.0 / 5.3, of 12000 x 2592 7.2 / 6.3, of 1024 x 2560 3.3 / 3.1; 8 rows of 9728 x 2560
     // 9.2 / 7.9; 16 rows one / two / three 9.7 / 9.6 / 10.6.
-    out->share = std::max((units + kMxQmvWaves - 1) / kMxQmvWaves, std::min(units, out->rows <= 8 ? 3 : 2));
-    out->waves = (units + out->share - 1) / out->share;
+    auto waves = [&](int share) { return (units + share - 1) / share; };
+    out->share = std::max(waves(kMxQmvWaves), std::min(units, out->rows <= 8 ? 3 : 2));
+    // Long contractions: larger shares, of one or two whole batches, and with more than one workgroup a
+    // compute unit those that put as many waves on each SIMD (five or six waves put two on some): the
+    // first with at most four waves or eight, else with at most eight.  2560 columns, share 3 / as
+    // chosen, us: 4 rows of 8192 7.7 / 7.0 (share 4), of 9728 8.4 / 8.4, of the gated pair 11.8 / 11.1
+    // (6); 8 rows of 8192 10.1 / 8.8 (4), of 9728 11.4 / 10.9, of the gated pair 16.4 / 14.3 (6); 4
+    // rows of 14336 on 4096 columns 17.3 / 13.6 (8).  One workgroup a unit wants its loads spread
+    // instead (one row of 9728 on 1024 columns 4.2 with shares of 3, 4.4 of 6).  16 rows of 9728, share
+    // 5 / 8: 12.9 / 12.0, of 8192 (4 / 8) 10.4 / 10.5.
+    if (out->rows <= 8 && out->groups > cus && waves(3) > 4 && waves(3) != 8) {
+        int share = 0;
+        for (int s : {4, 6, 8})
+            if (!share && (waves(s) <= 4 || waves(s) == 8)) share = s;
+        for (int s : {4, 6, 8})
+            if (!share && waves(s) <= 8) share = s;
+        out->share = std::max(waves(kMxQmvWaves), share ? share : 8);
+    } else if (out->rows == 16 && units > 64) {
+        out->share = std::max(out->share, 8);
+    }
+    out->waves = waves(out->share);
     const int turns = (out->share + 3) / 4;
     out->batch = (out->share + turns - 1) / turns;
     const size_t x = static_cast<size_t>(out->rows) * S * 256 * out->waves;
