@@ -11,6 +11,8 @@
 // number of blocks, so the array is a flat list of blocks.  Four lanes share a block, eight values
 // each: every load is 16 bytes per lane over consecutive addresses, the maximum takes two
 // lane exchanges, and a wave's codes are 256 consecutive bytes.
+// Measured on MI355X: 4096 x 9728 bf16 17.3 us (5.8 TB/s), 9728 x 2560 fp32 16.5 us (6.8, the
+// input in the last-level cache from the call before); 33 x 2560 2.3 us, a launch and two memory latencies.
 #include "mxfp4_device.h"
 #include "mxfp4_internal.h"
 
