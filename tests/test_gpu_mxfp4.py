@@ -206,9 +206,11 @@ def test_linear_backward(lib, M, N, K, split):
 
 # many columns: the wide decode form, with ragged last blocks, and the grids of the large tiles
 WIDE_SIZES = [(1, 20500, 512), (3, 20007, 1536), (5, 12391, 1024), (16, 16384, 512), (16, 12300, 4608)]
-LARGE_SIZES = [(773, 13176, 96), (522, 13265, 96), (961, 10881, 544), (300, 17001, 160)]
-LARGE_BACK_SIZES = [(2323, 72, 4928), (1298, 72, 5952), (321, 75, 5408)]
-LARGE_GATED_SIZES = [(390, 11227, 96), (257, 10998, 96), (2325, 72, 4896), (1422, 75, 5408), (201, 2000, 1376)]
+LARGE_SIZES = [(773, 13176, 96), (522, 13265, 96), (961, 10881, 544), (300, 17001, 160),
+               (770, 5999, 4928)]
+LARGE_BACK_SIZES = [(2323, 72, 4928), (1298, 72, 5952), (321, 75, 5408), (771, 140, 4928)]
+LARGE_GATED_SIZES = [(390, 11227, 96), (257, 10998, 96), (2325, 72, 4896), (1422, 75, 5408), (201, 2000, 1376),
+                     (513, 3999, 416), (771, 75, 4928)]
 
 
 # long contractions at decode rows: shares of one and two batches a wave, whole and ragged, one
@@ -298,11 +300,11 @@ def test_large_grids_gated(lib, M, N, K):
     ("MXFP4_GATE_UP", "SIZES LARGE_GATED_SIZES"), ("MXFP4_LINEAR_BACKWARD", "BACK_SIZES LARGE_BACK_SIZES"),
     ("MXFP4_GATE_UP_BACKWARD", "BACK_SIZES LARGE_GATED_SIZES")])
 def test_sizes_reach_every_tile(lib, op, sizes):
-    """The size lists above cover the four tile shapes, split and not, of every operator's policy."""
+    """The size lists above cover the five tile shapes, split and not, of every operator's policy."""
     plans = [lib.mxfp4_plan(getattr(lib, op), *s) for name in sizes.split() for s in globals()[name]]
     tiles = {p["variant"] for p in plans if p["path"] == lib.PATH_MXFP4}
     splits = {p["split_k"] > 1 for p in plans if p["path"] == lib.PATH_MXFP4}
-    assert tiles == {0, 1, 2, 3} and splits == {False, True}, (tiles, splits)
+    assert tiles == {0, 1, 2, 3, 4} and splits == {False, True}, (tiles, splits)
 
 
 def gated(rng, M, N, K):

@@ -98,18 +98,18 @@ struct TileCost {
     double fixed, step, step_beside;
 };
 constexpr TileCost kTileCost[3][kNumMxTiles] = {
-    // 128 x 128        256 x 256      64 x 128          192 x 256
-    {{3.0, 0.67, 1.2}, {9.0, 1.20, 0}, {4.5, 0.41, 0.85}, {6.0, 1.05, 0}},    // kCodes (256 values a step)
-    {{5.0, 0.46, 1.0}, {10.0, 1.30, 0}, {5.0, 0.32, 0.54}, {8.0, 1.17, 0}},   // kRows (64)
-    {{5.0, 0.64, 0.9}, {8.0, 1.42, 0}, {5.0, 0.54, 0.9}, {6.0, 1.32, 0}},     // kColumns (64)
+    // 128 x 128        256 x 256      64 x 128          192 x 256       128 x 256
+    {{3.0, 0.67, 1.2}, {9.0, 1.20, 0}, {4.5, 0.41, 0.85}, {6.0, 1.05, 0}, {5.0, 1.05, 0}},    // kCodes (256 values a step)
+    {{5.0, 0.46, 1.0}, {10.0, 1.30, 0}, {5.0, 0.32, 0.54}, {8.0, 1.17, 0}, {6.0, 0.80, 0}},   // kRows (64)
+    {{5.0, 0.64, 0.9}, {8.0, 1.42, 0}, {5.0, 0.54, 0.9}, {6.0, 1.32, 0}, {5.0, 0.88, 0}},     // kColumns (64)
 };
 // A split's second launch, and its partials written and read per output (8 bytes at about 4 TB/s).
 constexpr double kSplitCost = 3.5, kPartialCost = 2e-6;
 constexpr int64_t kMaxSplit = 8;
 
 // The tile and the split with the lowest modelled time.  Against the best of a sweep of every tile and
-// split on 20 shapes of kRows and kColumns the choice is 1% behind on average and 10% at worst (1024 rows
-// of 9728 values on 2560 columns: 79 us unsplit against 72 in four slices).
+// split on 20 shapes of kRows and kColumns the choice is 1% behind on average and 7% at worst (2048 rows of
+// the transposed product of 4096 x 2560: 64 us unsplit against 61 in two slices of 192 x 256 tiles).
 void choose(Product& p, int32_t split_k, int64_t cus) {
     if (p.decode) return;
     const int64_t units = units_of(p);

@@ -49,7 +49,7 @@ struct MxTileArgs {
 struct MxTileShape {
     int bm, bn, waves;         // rows and weight rows of a workgroup's tile
 };
-constexpr int kNumMxTiles = 4;
+constexpr int kNumMxTiles = 5;
 extern const MxTileShape kMxTiles[kNumMxTiles];
 // Values of the contraction in one pipeline step, and in the unit that split-K distributes (a pair of
 // steps where two steps' weights or scales are loaded together).

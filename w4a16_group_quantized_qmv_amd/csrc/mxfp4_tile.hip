@@ -617,7 +617,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mx_tile_kernel(const MxTileArgs 
 
 }  // namespace
 
-const MxTileShape kMxTiles[kNumMxTiles] = {{128, 128, 4}, {256, 256, 8}, {64, 128, 4}, {192, 256, 8}};
+const MxTileShape kMxTiles[kNumMxTiles] = {{128, 128, 4}, {256, 256, 8}, {64, 128, 4}, {192, 256, 8}, {128, 256, 8}};
 
 namespace {
 
@@ -625,7 +625,8 @@ namespace {
 // stages cover a latency with three steps of loads, at the cost of a second workgroup beside: 64 x 128
 // keeps both.  192 x 256 fits four of the left operand and two of decoded weights into 160 KB (4096 x
 // 2560 with 9728 values: 198 us with two, 190 with four; kColumns 211 and 208), 256 x 256 does not;
-// 128 x 128 gained nothing from them.
+// 128 x 128 gained nothing from them.  128 x 256 has two waves a SIMD where 128 x 128 alone on its compute
+// unit has one: 1024 rows of 9728 values on 2560 columns 77 and 61 us, 2048 rows of codes 51 and 43.
 template <int BM, int BN, int WR, int WC, int STAGES, int CODE_STAGES>
 hipError_t launch_shape(MxOperands op, MxEpilogue epi, const MxTileArgs& args, hipStream_t stream) {
     const int bc = epi == MxEpilogue::kStore ? BN : BN / 2;
@@ -665,6 +666,7 @@ hipError_t launch_mx_tile(MxOperands op, MxEpilogue epi, int tile, const MxTileA
         case 1: return launch_shape<256, 256, 2, 4, 2, 2>(op, epi, args, stream);
         case 2: return launch_shape<64, 128, 2, 2, 4, 4>(op, epi, args, stream);
         case 3: return launch_shape<192, 256, 2, 4, 4, 2>(op, epi, args, stream);
+        case 4: return launch_shape<128, 256, 2, 4, 4, 2>(op, epi, args, stream);
         default: return hipErrorInvalidValue;
     }
 }
