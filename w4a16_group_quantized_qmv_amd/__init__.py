@@ -250,7 +250,7 @@ def _check(t, name, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _operands(x, wq, scales, biases, y, bits: int = 4):
+def _operands(x, wq, scales, biases, y, bits: int = 4, stream=None):
     torch = _torch()
     if x.dim() != 2 or wq.dim() != 2:
         raise ValueError("x and wq must be 2-D")
@@ -264,7 +264,7 @@ def _operands(x, wq, scales, biases, y, bits: int = 4):
     _check(biases, "biases", torch.bfloat16, (N, K // GROUP))
     devs = {t.device for t in (x, wq, scales, biases)}
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _empty_for(stream, (M, N), torch.bfloat16, x.device)
     _check(y, "y", torch.bfloat16, (M, N))
     devs.add(y.device)
     if len(devs) != 1:
@@ -284,26 +284,30 @@ def _stream(stream, device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _keep_for_stream(stream, device, *tensors):
-    """Tensors allocated here (on torch's current stream) but used by kernels on the caller's
-    ``stream``: record that stream on them, so torch's caching allocator does not hand their
-    memory to another allocation before the kernels queued there have finished with it."""
-    if stream is None:
-        return
+def _empty_for(stream, shape, dtype, device, output=True):
+    """Memory that kernels on the caller's ``stream`` (None: the current one) write.  It comes from
+    that stream's own pool of torch's allocator: a block of the current stream's pool may still be in
+    use by work queued there, which ``stream`` does not wait for.  An output is read by the caller
+    elsewhere, so the current stream is recorded on it: work that it has queued by the time the last
+    reference goes keeps the block.  A workspace is ``stream``'s alone."""
     torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream),
                                                                                       device=device)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
-def _workspace(workspace, nbytes, device):
+def _workspace(workspace, nbytes, device, stream=None):
     torch = _torch()
     if nbytes == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device)
+        workspace = _empty_for(stream, (nbytes + 3) // 4, torch.float32, device, output=False)
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
     return workspace, workspace.numel() * workspace.element_size()
@@ -311,9 +315,7 @@ def _workspace(workspace, nbytes, device):
 
 def qmv_w4a16(x, wq, scales, biases, y=None, stream=None):
     """Decode-row matvec (1 <= M <= 8); returns y."""
-    own_y = y is None
-    M, N, K, y = _operands(x, wq, scales, biases, y)
-    _keep_for_stream(stream, x.device, y if own_y else None)
+    M, N, K, y = _operands(x, wq, scales, biases, y, stream=stream)
     st = load().qmv_w4a16(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), y.data_ptr(),
                           M, N, K, GROUP, _stream(stream, x.device))
     _raise_for(st, "qmv_w4a16")
@@ -326,9 +328,7 @@ def qmv_affine(x, wq, scales, biases, bits: int, y=None, mode: int = QMV_POLICY,
     row-amortized, the per-row kernel or the burst form.  Returns y."""
     if bits not in BITS:
         raise ValueError(f"bits={bits} must be one of {BITS}")
-    own_y = y is None
-    M, N, K, y = _operands(x, wq, scales, biases, y, bits)
-    _keep_for_stream(stream, x.device, y if own_y else None)
+    M, N, K, y = _operands(x, wq, scales, biases, y, bits, stream)
     st = load().qmv_affine(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), y.data_ptr(),
                            M, N, K, GROUP, bits, mode, _stream(stream, x.device))
     _raise_for(st, "qmv_affine")
@@ -337,11 +337,9 @@ def qmv_affine(x, wq, scales, biases, bits: int, y=None, mode: int = QMV_POLICY,
 
 def qmm_w4a16(x, wq, scales, biases, y=None, split_k: int = 0, workspace=None, stream=None):
     """Tiled matrix path for any M; split_k 0 = policy, 1 = off, S > 1 forced.  Returns y."""
-    own_y, own_ws = y is None, workspace is None
-    M, N, K, y = _operands(x, wq, scales, biases, y)
+    M, N, K, y = _operands(x, wq, scales, biases, y, stream=stream)
     need = w4a16_plan(M, N, K, GROUP, PATH_QMM, split_k)["workspace_bytes"]
-    ws, ws_bytes = _workspace(workspace, need, x.device)
-    _keep_for_stream(stream, x.device, y if own_y else None, ws if own_ws else None)
+    ws, ws_bytes = _workspace(workspace, need, x.device, stream)
     st = load().qmm_w4a16(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), y.data_ptr(),
                           M, N, K, GROUP, split_k, None if ws is None else ws.data_ptr(), ws_bytes,
                           _stream(stream, x.device))
@@ -352,10 +350,8 @@ def qmm_w4a16(x, wq, scales, biases, y=None, split_k: int = 0, workspace=None, s
 def w4a16_linear(x, wq, scales, biases, y=None, workspace=None, stream=None):
     """Dispatching entry point (qmv for M <= 8, the skinny path for 8 < M <= 32, qmm beyond, each
     with the policy's split).  Returns y."""
-    own_y, own_ws = y is None, workspace is None
-    M, N, K, y = _operands(x, wq, scales, biases, y)
-    ws, ws_bytes = _workspace(workspace, w4a16_workspace_bytes(M, N, K), x.device)
-    _keep_for_stream(stream, x.device, y if own_y else None, ws if own_ws else None)
+    M, N, K, y = _operands(x, wq, scales, biases, y, stream=stream)
+    ws, ws_bytes = _workspace(workspace, w4a16_workspace_bytes(M, N, K), x.device, stream)
     st = load().w4a16_linear(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), y.data_ptr(),
                              M, N, K, GROUP, None if ws is None else ws.data_ptr(), ws_bytes,
                              _stream(stream, x.device))
@@ -383,14 +379,12 @@ def w4a16_gate_up_swiglu(x, gate, up, h=None, split_k: int = 0, workspace=None, 
     """Fused gate / up projections with SwiGLU: ``h = silu(x . Wg^T) * (x . Wu^T)`` in one tile
     kernel.  ``gate`` and ``up`` are ``(wq, scales, biases)`` triples of one shape.  Returns h."""
     (wg, sg, bg), (wu, su, bu) = gate, up
-    own_h, own_ws = h is None, workspace is None
-    M, N, K, h = _operands(x, wg, sg, bg, h)
+    M, N, K, h = _operands(x, wg, sg, bg, h, stream=stream)
     if tuple(wu.shape) != tuple(wg.shape) or tuple(su.shape) != tuple(sg.shape) or tuple(bu.shape) != tuple(bg.shape):
         raise ValueError("gate and up weights must have the same shapes")
     _operands(x, wu, su, bu, h)                      # same dtype / device / contiguity checks for up
     need = w4a16_gate_up_plan(M, N, K, GROUP, split_k)["workspace_bytes"]
-    ws, ws_bytes = _workspace(workspace, need, x.device)
-    _keep_for_stream(stream, x.device, h if own_h else None, ws if own_ws else None)
+    ws, ws_bytes = _workspace(workspace, need, x.device, stream)
     st = load().w4a16_gate_up_swiglu(x.data_ptr(), wg.data_ptr(), sg.data_ptr(), bg.data_ptr(), wu.data_ptr(),
                                      su.data_ptr(), bu.data_ptr(), h.data_ptr(), M, N, K, GROUP, split_k,
                                      None if ws is None else ws.data_ptr(), ws_bytes, _stream(stream, x.device))
@@ -410,14 +404,12 @@ def w4a8_quantize_rows(x, xq=None, sx=None, xsum=None, stream=None):
     KB = w4a8_xsum_cols(K)
     if KB == 0:
         raise ValueError(f"K={K} must be a positive multiple of {GROUP}")
-    own = [t is None for t in (xq, sx, xsum)]
-    xq = torch.empty((M, K), dtype=torch.int8, device=x.device) if xq is None else xq
-    sx = torch.empty((M,), dtype=torch.float32, device=x.device) if sx is None else sx
-    xsum = torch.empty((M, KB), dtype=torch.bfloat16, device=x.device) if xsum is None else xsum
+    xq = _empty_for(stream, (M, K), torch.int8, x.device) if xq is None else xq
+    sx = _empty_for(stream, (M,), torch.float32, x.device) if sx is None else sx
+    xsum = _empty_for(stream, (M, KB), torch.bfloat16, x.device) if xsum is None else xsum
     _check(xq, "xq", torch.int8, (M, K))
     _check(sx, "sx", torch.float32, (M,))
     _check(xsum, "xsum", torch.bfloat16, (M, KB))
-    _keep_for_stream(stream, x.device, *[t for t, o in zip((xq, sx, xsum), own) if o])
     st = load().w4a8_quantize_rows(x.data_ptr(), xq.data_ptr(), sx.data_ptr(), xsum.data_ptr(), M, K, GROUP,
                                    _stream(stream, x.device))
     _raise_for(st, "w4a8_quantize_rows")
@@ -440,13 +432,11 @@ def qmm_w4a8(xq, sx, xsum, wq, scales, biases, y=None, split_k: int = 0, workspa
     _check(wq, "wq", torch.int32, (N, K // 8))
     _check(scales, "scales", torch.bfloat16, (N, K // GROUP))
     _check(biases, "biases", torch.bfloat16, (N, K // GROUP))
-    own_y, own_ws = y is None, workspace is None
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        y = _empty_for(stream, (M, N), torch.bfloat16, xq.device)
     _check(y, "y", torch.bfloat16, (M, N))
     need = w4a8_plan(M, N, K, GROUP, split_k)["workspace_bytes"]
-    ws, ws_bytes = _workspace(workspace, need, xq.device)
-    _keep_for_stream(stream, xq.device, y if own_y else None, ws if own_ws else None)
+    ws, ws_bytes = _workspace(workspace, need, xq.device, stream)
     st = load().qmm_w4a8(xq.data_ptr(), sx.data_ptr(), xsum.data_ptr(), wq.data_ptr(), scales.data_ptr(),
                          biases.data_ptr(), y.data_ptr(), M, N, K, GROUP, split_k,
                          None if ws is None else ws.data_ptr(), ws_bytes, _stream(stream, xq.device))
@@ -457,10 +447,8 @@ def qmm_w4a8(xq, sx, xsum, wq, scales, biases, y=None, split_k: int = 0, workspa
 def w4a8_linear(x, wq, scales, biases, y=None, workspace=None, stream=None):
     """One-call W4A8 projection of bf16 ``x``: per-row int8 quantization into the workspace, then
     the int8 tile path under the policy.  Returns y."""
-    own_y, own_ws = y is None, workspace is None
-    M, N, K, y = _operands(x, wq, scales, biases, y)
-    ws, ws_bytes = _workspace(workspace, w4a8_linear_workspace_bytes(M, N, K), x.device)
-    _keep_for_stream(stream, x.device, y if own_y else None, ws if own_ws else None)
+    M, N, K, y = _operands(x, wq, scales, biases, y, stream=stream)
+    ws, ws_bytes = _workspace(workspace, w4a8_linear_workspace_bytes(M, N, K), x.device, stream)
     st = load().w4a8_linear(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), y.data_ptr(),
                             M, N, K, GROUP, None if ws is None else ws.data_ptr(), ws_bytes,
                             _stream(stream, x.device))
@@ -500,7 +488,7 @@ def w4a16_grouped_plan(N, M: int, K: int, group: int = GROUP, num_cus: int = 0) 
     return plan.as_dict()
 
 
-def _grouped_args(x, weights, ys):
+def _grouped_args(x, weights, ys, stream=None):
     if not 1 <= len(weights) <= MAX_GROUPED:
         raise ValueError(f"{len(weights)} projections: 1 .. {MAX_GROUPED} are supported")
     if ys is None:
@@ -509,7 +497,7 @@ def _grouped_args(x, weights, ys):
         raise ValueError("one output per projection")
     out, Ns = [], []
     for (wq, s, b), y in zip(weights, ys):
-        M, N, K, y = _operands(x, wq, s, b, y)
+        M, N, K, y = _operands(x, wq, s, b, y, stream=stream)
         out.append(y)
         Ns.append(N)
     vp = ctypes.c_void_p
@@ -522,11 +510,9 @@ def w4a16_linear_grouped(x, weights, ys=None, workspace=None, stream=None):
     """Projections of one input in one call: ``weights`` is a list of ``(wq, scales, biases)``
     triples (1 .. MAX_GROUPED), e.g. the query, key and value projections; returns the list of
     outputs ``y_p = x . dequant(wq_p)^T``."""
-    own_y, own_ws = ys is None, workspace is None
-    M, K, out, Ns, (wqa, sa, ba, ya) = _grouped_args(x, weights, ys)
+    M, K, out, Ns, (wqa, sa, ba, ya) = _grouped_args(x, weights, ys, stream)
     need = w4a16_grouped_plan(Ns, M, K)["workspace_bytes"]
-    ws, ws_bytes = _workspace(workspace, need, x.device)
-    _keep_for_stream(stream, x.device, *(out if own_y else []), ws if own_ws else None)
+    ws, ws_bytes = _workspace(workspace, need, x.device, stream)
     st = load().w4a16_linear_grouped(x.data_ptr(), len(weights), wqa, sa, ba, ya, (ctypes.c_int64 * len(Ns))(*Ns),
                                      M, K, GROUP, None if ws is None else ws.data_ptr(), ws_bytes,
                                      _stream(stream, x.device))

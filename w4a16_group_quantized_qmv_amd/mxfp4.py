@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import _keep_for_stream, _raise_for, _stream_handle, _torch, Plan, load
+from . import _empty_for, _raise_for, _stream_handle, _torch, Plan, load
 
 __all__ = [
     "MXFP4_BLOCK", "MXFP4_LINEAR", "MXFP4_LINEAR_BACKWARD", "MXFP4_QMM_A4", "MXFP4A4_LINEAR", "MXFP4_GATE_UP",
@@ -114,9 +114,11 @@ def _weights(codes, scales, name, index, like=None):
     return N, K
 
 
-def _output(t, name, shape, x, dtype):
-    """An output beside ``x``: allocated, or checked if it is given."""
+def _output(t, name, shape, x, dtype, stream=None):
+    """An output beside ``x``: allocated for ``stream``, or checked if it is given."""
     if t is None:
+        if stream is not None:
+            return _empty_for(stream, shape, dtype, x.device)
         return x.new_empty(shape) if x.dtype is dtype else x.new_empty(shape, dtype=dtype)
     _tensor(t, name, dtype, shape, x.get_device())
     return t
@@ -127,12 +129,12 @@ def _check_workspace(workspace, index):
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
 
 
-def _call(name, op, dims, index, stream, workspace, own, args, split_k=0):
+def _call(name, op, dims, index, stream, workspace, args, split_k=0):
     """One C-ABI call on GPU ``index``: its workspace (allocated where the caller gave none), the stream,
-    the status.  ``own``: tensors allocated for this call."""
+    the status."""
     if index != _current():
         with _torch().cuda.device(index):
-            return _call(name, op, dims, index, stream, workspace, own, args, split_k)
+            return _call(name, op, dims, index, stream, workspace, args, split_k)
     if op is None:
         args += dims
     else:
@@ -143,15 +145,15 @@ def _call(name, op, dims, index, stream, workspace, own, args, split_k=0):
             args += (*dims, split_k, None, 0)
         else:
             if workspace is None:
-                workspace = _empty(need, dtype=_U8, device=f"cuda:{index}")
-                own = (*own, workspace)
+                where = f"cuda:{index}"
+                workspace = (_empty(need, dtype=_U8, device=where) if stream is None else
+                             _empty_for(stream, need, _U8, where, output=False))
             else:
                 _check_workspace(workspace, index)
             args += (*dims, split_k, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     if stream is None:
         status = _FN[name](*args, _raw_stream(index))
     else:
-        _keep_for_stream(stream, _torch().device("cuda", index), *own)
         status = _FN[name](*args, _stream_handle(stream))
     if status:
         _raise_for(status, name)
@@ -166,11 +168,9 @@ def mxfp4_quantize_rows(x, codes=None, scales=None, stream=None):
     if K == 0 or K % MXFP4_BLOCK:
         raise ValueError(f"K={K} must be a positive multiple of {MXFP4_BLOCK}")
     _tensor(x, "x", x.dtype, (R, K))
-    given = (codes, scales)
-    codes = _output(codes, "codes", (R, K // 2), x, _U8)
-    scales = _output(scales, "scales", (R, K // MXFP4_BLOCK), x, _U8)
+    codes = _output(codes, "codes", (R, K // 2), x, _U8, stream)
+    scales = _output(scales, "scales", (R, K // MXFP4_BLOCK), x, _U8, stream)
     _call("mxfp4_quantize_rows", None, (R, K), x.get_device(), stream, None,
-          [t for t, g in zip((codes, scales), given) if g is None] if stream is not None else (),
           (x.data_ptr(), int(x.dtype is _FP32), codes.data_ptr(), scales.data_ptr()))
     return codes, scales
 
@@ -180,9 +180,8 @@ def mxfp4_dequantize_rows(codes, scales, y=None, stream=None):
     _matrix(codes, "codes")
     index = codes.get_device()
     R, K = _weights(codes, scales, "rows", index)
-    own = y is None
-    y = _output(y, "y", (R, K), codes, _BF16)
-    _call("mxfp4_dequantize_rows", None, (R, K), index, stream, None, (y,) if own else (),
+    y = _output(y, "y", (R, K), codes, _BF16, stream)
+    _call("mxfp4_dequantize_rows", None, (R, K), index, stream, None,
           (codes.data_ptr(), scales.data_ptr(), y.data_ptr()))
     return y
 
@@ -193,9 +192,8 @@ def _projection(name, op, x, codes, scales, y, split_k, workspace, stream):
     N, K = _weights(codes, scales, "weight", index)
     back = op == MXFP4_LINEAR_BACKWARD
     _tensor(x, "dy" if back else "x", _BF16, (M, N if back else K))
-    own = y is None
-    y = _output(y, "dx" if back else "y", (M, K if back else N), x, _BF16)
-    _call(name, op, (M, N, K), index, stream, workspace, (y,) if own else (),
+    y = _output(y, "dx" if back else "y", (M, K if back else N), x, _BF16, stream)
+    _call(name, op, (M, N, K), index, stream, workspace,
           (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr()), split_k)
     return y
 
@@ -223,9 +221,8 @@ def qmm_mxfp4a4(xq, xs, codes, scales, y=None, split_k: int = 0, workspace=None,
     index = xq.get_device()
     N, K = _weights(codes, scales, "weight", index)
     _weights(xq, xs, "x", index, (M, K))
-    own = y is None
-    y = _output(y, "y", (M, N), xq, _BF16)
-    _call("qmm_mxfp4a4", MXFP4_QMM_A4, (M, N, K), index, stream, workspace, (y,) if own else (),
+    y = _output(y, "y", (M, N), xq, _BF16, stream)
+    _call("qmm_mxfp4a4", MXFP4_QMM_A4, (M, N, K), index, stream, workspace,
           (xq.data_ptr(), xs.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr()), split_k)
     return y
 
@@ -238,9 +235,8 @@ def mxfp4_gate_up_swiglu(x, gate, up, h=None, split_k: int = 0, workspace=None, 
     N, K = _weights(*gate, "gate", index)
     _weights(*up, "up", index, (N, K))
     _tensor(x, "x", _BF16, (M, K))
-    own = h is None
-    h = _output(h, "h", (M, N), x, _BF16)
-    _call("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), index, stream, workspace, (h,) if own else (),
+    h = _output(h, "h", (M, N), x, _BF16, stream)
+    _call("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), index, stream, workspace,
           (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), h.data_ptr()),
           split_k)
     return h
@@ -256,12 +252,10 @@ def mxfp4_gate_up_swiglu_backward(x, gate, up, dh, dx=None, dgate=None, dup=None
     _weights(*up, "up", index, (N, K))
     _tensor(x, "x", _BF16, (M, K))
     _tensor(dh, "dh", _BF16, (M, N), index)
-    own = [t is None for t in (dx, dgate, dup)]
-    dx = _output(dx, "dx", (M, K), x, _BF16)
-    dgate = _output(dgate, "dgate", (M, N), x, _BF16)
-    dup = _output(dup, "dup", (M, N), x, _BF16)
+    dx = _output(dx, "dx", (M, K), x, _BF16, stream)
+    dgate = _output(dgate, "dgate", (M, N), x, _BF16, stream)
+    dup = _output(dup, "dup", (M, N), x, _BF16, stream)
     _call("mxfp4_gate_up_swiglu_backward", MXFP4_GATE_UP_BACKWARD, (M, N, K), index, stream, workspace,
-          tuple(t for t, o in zip((dx, dgate, dup), own) if o),
           (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), dh.data_ptr(),
            dx.data_ptr(), dgate.data_ptr(), dup.data_ptr()), split_k)
     return dx, dgate, dup
