@@ -144,7 +144,8 @@ def mx_gate_up_backward(x, wg, wu, dh):
 
 
 def mx_check(got, value, bound):
-    """None, or what is wrong: the worst element beyond its bound; NaN has to be where it is in value."""
+    """None, or what is wrong: the worst element beyond its bound.  NaN and infinities have to be where they are
+    in value (their bounds do not matter), and every finite value needs a finite bound."""
     got = np.asarray(got, dtype=np.float64)
     if got.shape != value.shape:
         return f"shape {got.shape}, not {value.shape}"
@@ -152,9 +153,17 @@ def mx_check(got, value, bound):
     if not np.array_equal(np.isnan(got), nan):
         i = np.argwhere(np.isnan(got) != nan)[0]
         return f"NaN differs at {tuple(i)}: got {got[tuple(i)]}, {value[tuple(i)]} expected"
-    off = np.where(nan, 0.0, np.abs(np.where(nan, 0.0, got) - np.where(nan, 0.0, value)) - np.where(nan, 0.0, bound))
-    if off.size and off.max() > 0:
-        i = np.unravel_index(off.argmax(), off.shape)
-        return (f"{int((off > 0).sum())} of {off.size} beyond the bound, worst at {tuple(map(int, i))}: got {got[i]}, "
+    unbounded = np.isfinite(value) & ~np.isfinite(bound)
+    if unbounded.any():
+        i = tuple(map(int, np.argwhere(unbounded)[0]))
+        return f"no finite bound at {i}: {value[i]} +- {bound[i]}"
+    # an infinity has to be met exactly; NaN elsewhere cannot arise, so a comparison decides every element
+    exact = nan | (np.isinf(value) & (got == value))
+    with np.errstate(invalid="ignore"):
+        off = np.where(exact, 0.0, np.abs(got - value) - np.where(np.isfinite(bound), bound, 0.0))
+    wrong = ~(off <= 0)
+    if wrong.any():
+        i = tuple(map(int, np.unravel_index(np.where(wrong, off, -np.inf).argmax(), off.shape)))
+        return (f"{int(wrong.sum())} of {off.size} beyond the bound, worst at {i}: got {got[i]}, "
                 f"{value[i]} +- {bound[i]} expected")
     return None

@@ -135,6 +135,29 @@ def test_check_finds_planted_mistakes():
         assert O.mx_check(wrong, y, bound) is not None
 
 
+@pytest.mark.parametrize("place", ["bound_nan", "bound_inf", "both_inf", "other_inf", "inf_expected"])
+def test_check_with_values_and_bounds_that_are_not_finite(place):
+    """One odd element neither hides the others nor passes where it is wrong itself."""
+    value, bound = np.ones((4, 3)), np.full((4, 3), 0.1)
+    got = value.copy()
+    if place.startswith("bound"):
+        bound[1, 2] = np.nan if place == "bound_nan" else np.inf
+        assert O.mx_check(got, value, bound) is not None           # no bound for a finite value
+    elif place == "both_inf":
+        got[1, 2] = value[1, 2] = -np.inf
+        bound[1, 2] = np.nan                                       # (a bound relative to an infinity)
+        assert O.mx_check(got, value, bound) is None
+    else:
+        (got if place == "other_inf" else value)[1, 2] = np.inf
+        assert O.mx_check(got, value, bound) is not None
+        value[1, 2], got[1, 2] = np.inf, -np.inf
+        assert O.mx_check(got, value, bound) is not None
+    assert O.mx_check(np.full((4, 3), 5.0), value, bound) is not None
+    wrong = got.copy()
+    wrong[3, 0] = 1.2
+    assert "(3, 0)" in O.mx_check(wrong, np.where(np.isinf(value), got, value), np.where(np.isfinite(bound), bound, 0.1))
+
+
 # ---------------------------------------------------------------------------- the policy
 
 @pytest.mark.parametrize("op", list(OPS))
