@@ -1,0 +1,187 @@
+"""MXFP4 on the GPU at the ends of its values: what decode rows quantize on the way, NaN and infinities,
+the smallest and largest scales, gates where the sigmoid vanishes, the longest contraction."""
+
+import numpy as np
+import pytest
+
+import oracle as O
+
+from gpu_helpers import announce
+from test_gpu_mxfp4 import bf16, bf16_values, check, to_gpu, values, weight
+
+pytestmark = pytest.mark.gpu
+
+DECODE_ROWS = [1, 2, 3, 4, 5, 8, 9, 16]
+
+
+def one_hot(N, K, scale):
+    """Weight rows n < K with one 1.0 (code 2) at k = n, all others zero; one scale byte."""
+    import torch
+    codes = np.zeros((N, K), np.uint8)
+    n = np.arange(min(N, K))
+    codes[n, n] = 2
+    return to_gpu(O.mx_pack(codes), torch.uint8), torch.full((N, K // 32), scale, dtype=torch.uint8, device="cuda:0")
+
+
+def special_blocks():
+    """(name, weight scale byte, float32 blocks [n, 32]): every finite bf16 value under three tops and as its
+    block's top, the borders between codes, zeros of both signs."""
+    every = (np.arange(65536, dtype=np.uint32) << 16).view(np.float32)
+    out = []
+    for name, top, scale in (("one", 1.0, 127), ("smallest", 2.0 ** -126, 187), ("large", 2.0 ** 100, 127)):
+        x = every.reshape(-1, 16).copy()
+        x[~np.isfinite(x) | (np.abs(x) >= np.float32(8 * top))] = 0
+        rows = np.zeros((x.shape[0], 32), np.float32)
+        rows[:, :16], rows[:, 31] = x, 6 * top
+        out.append((name, scale, rows))
+    finite = every[np.isfinite(every)]
+    small, rest = finite[np.abs(finite) < 1], finite[np.abs(finite) >= 1]
+    for name, tops, scale in (("small tops", small, 187), ("tops", rest, 67)):
+        rows = np.zeros((tops.size, 32), np.float32)
+        rows[np.arange(tops.size), np.arange(tops.size) % 32] = tops
+        out.append((name, scale, rows))
+    borders = np.array([0.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 6.5, 7.0, 7.5], np.float32)
+    near = np.concatenate([borders * np.float32(f) for f in (1 - 2.0 ** -7, 1.0, 1 + 2.0 ** -7)])
+    near = np.asarray(bf16_values(near[near < 8]), np.float32)
+    for name, scale, exponents in (("small borders", 187, (-127, -126, -125, -60)), ("borders", 67, (0, 60))):
+        rows = []
+        for e in exponents:
+            block = np.zeros((near.size, 32), np.float32)
+            block[:, 5], block[:, 6] = np.ldexp(near, e), -np.ldexp(near, e)
+            block[:, 31], block[:, 0] = np.ldexp(np.float32(4), e), -0.0
+            rows.append(block)
+        out.append((name, scale, np.asarray(bf16_values(np.concatenate(rows)), np.float32)))
+    return out
+
+
+def quantized_on_the_way(lib, x, N, scale, M):
+    """mxfp4a4_linear of M rows at a time against one-hot weights: the value each element was rounded to."""
+    import torch
+    K = x.shape[1]
+    w = one_hot(N, K, scale)
+    t = bf16(x)
+    assert np.array_equal(values(t), x.astype(np.float64))
+    got = torch.cat([lib.mxfp4a4_linear(t[r:r + M].contiguous(), *w)[:, :K] for r in range(0, x.shape[0], M)])
+    steps = torch.cat([lib.qmm_mxfp4a4(*lib.mxfp4_quantize_rows(t[r:r + M].contiguous()), *w)[:, :K]
+                       for r in range(0, x.shape[0], M)])
+    assert torch.equal(got.view(torch.int16), steps.view(torch.int16))
+    factor = 2.0 ** (scale - 127)
+    expected = O.mx_decode(*O.mx_encode(x)) * factor
+    wrong = np.argwhere(values(got) != expected)
+    assert not wrong.size, [(tuple(i), x[tuple(i)], values(got)[tuple(i)], expected[tuple(i)]) for i in wrong[:4]]
+
+
+@pytest.mark.parametrize("M", DECODE_ROWS)
+def test_decode_rows_quantize_every_value(lib, M):
+    """Up to 16 rows mxfp4a4_linear quantizes in the product's kernel: the same rule, value by value."""
+    K = 512 if M > 4 else 1056                         # whole windows, and a ragged last unit
+    for name, scale, blocks in special_blocks():
+        announce(f"mxfp4a4_linear quantizing M={M} {name}")
+        blocks = blocks if M in (1, 16) else blocks[::7]
+        per_row = K // 32
+        rows = -(-blocks.shape[0] // per_row)
+        x = np.zeros((rows * per_row, 32), np.float32)
+        x[:blocks.shape[0]] = blocks
+        quantized_on_the_way(lib, x.reshape(rows, K), K, scale, M)
+
+
+@pytest.mark.parametrize("M,N", [(1, 20500), (5, 12300), (16, 12300)])
+def test_wide_decode_rows_quantize_every_value(lib, M, N):
+    K = 512
+    assert lib.mxfp4_plan(lib.MXFP4A4_LINEAR, M, N, K)["variant"] == 0
+    for name, scale, blocks in special_blocks():
+        announce(f"mxfp4a4_linear wide quantizing M={M} {name}")
+        blocks = blocks[::5]
+        rows = -(-blocks.shape[0] // 16)
+        x = np.zeros((rows * 16, 32), np.float32)
+        x[:blocks.shape[0]] = blocks
+        quantized_on_the_way(lib, x.reshape(rows, K), N, scale, M)
+
+
+SHAPES = [(M, 136, 288) for M in DECODE_ROWS] + [(40, 136, 288), (1, 20500, 512), (5, 12300, 512), (16, 12300, 512)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_invalid_values_stay_in_their_rows_and_columns(lib, M, N, K, bad):
+    """Decode rows, the wide form and tiles: an invalid activation reaches its own row, a NaN scale its own
+    column, in the projections and the gated pair."""
+    import torch
+    announce(f"mxfp4 invalid values M={M} N={N} K={K} {bad}")
+    rng = np.random.default_rng(M + N)
+    (codes, scales), _ = weight(rng, N, K, 118, 124)
+    up, uv = weight(rng, N, K, 118, 124)
+    x = bf16_values(rng.standard_normal((M, K)))
+    stored = O.mx_unpack(codes.cpu().numpy())
+    stored[stored % 8 == 0] = 1                        # (an infinity times a zero weight would be NaN)
+    codes = to_gpu(O.mx_pack(stored), torch.uint8)
+    bad_scales = scales.clone()
+    bad_scales[N // 3, 2] = 255
+    wv = O.mx_decode(codes.cpu().numpy(), bad_scales.cpu().numpy())
+    row = M - 1
+    x[row, 70] = np.nan if bad == "nan" else -np.inf
+    t = bf16(np.where(np.isfinite(x), x, 0))
+    t[row, 70] = float("nan") if bad == "nan" else float("-inf")
+    with np.errstate(invalid="ignore"):
+        expected = O.mx_linear(x, wv)
+        check(lib.mxfp4_linear(t, codes, bad_scales), expected)
+        xq = lib.mxfp4_quantize_rows(t)
+        xv = O.mx_decode(*(q.cpu().numpy() for q in xq))
+        assert np.isnan(xv[row, 64:96]).all() and np.isfinite(xv).sum() == xv.size - 32
+        four = O.mx_linear(xv, wv)
+        check(lib.qmm_mxfp4a4(*xq, codes, bad_scales), four)
+        check(lib.mxfp4a4_linear(t, codes, bad_scales), four)
+        if N > 1000:
+            return
+        # the gated pair; an infinite gate or up leaves nothing finite (silu(-inf) is -inf 0)
+        h = values(lib.mxfp4_gate_up_swiglu(t, (codes, bad_scales), up))
+        dh = bf16_values(rng.standard_normal((M, N)))
+        dx, dgate, dup = (values(v) for v in lib.mxfp4_gate_up_swiglu_backward(t, (codes, bad_scales), up, bf16(dh)))
+    keep_r, keep_c = np.arange(M) != row, np.arange(N) != N // 3
+    xs, gs, us = x[keep_r], wv[keep_c], uv[keep_c]
+    if M > 1:
+        check(torch.from_numpy(h[keep_r][:, keep_c]), O.mx_gate_up(xs, gs, us))
+        (_, _), eg, eu = O.mx_gate_up_backward(xs, gs, us, dh[keep_r][:, keep_c])
+        check(torch.from_numpy(dgate[keep_r][:, keep_c]), eg)
+        check(torch.from_numpy(dup[keep_r][:, keep_c]), eu)
+        # that column's gradients are NaN, and its weights spread them over the rows' dx
+        assert np.isnan(dx[keep_r]).all()
+    for v in (h, dgate, dup):
+        assert np.isnan(v[:, N // 3]).all() and not np.isfinite(v[row]).any()
+
+
+@pytest.mark.parametrize("M", [1, 4, 16, 20, 200])
+def test_extreme_scales(lib, M):
+    """The smallest scales, alone too, and the largest that bf16 holds, in both directions of the product;
+    subnormal activations."""
+    announce(f"mxfp4 extreme scales M={M}")
+    rng = np.random.default_rng(M)
+    for low, high, size in ((0, 1, 2.0 ** 100), (0, 4, 2.0 ** 100), (248, 253, 2.0 ** -100), (220, 224, 2.0 ** -131)):
+        w, wv = weight(rng, 136, 320, low, high)
+        x = bf16_values(rng.standard_normal((M, 320)) * size)
+        dy = bf16_values(rng.standard_normal((M, 136)) * size)
+        check(lib.mxfp4_linear(bf16(x), *w), O.mx_linear(x, wv))
+        check(lib.mxfp4_linear_backward(bf16(dy), *w), O.mx_linear_backward(dy, wv))
+        xq = lib.mxfp4_quantize_rows(bf16(x))
+        check(lib.qmm_mxfp4a4(*xq, *w), O.mx_linear(O.mx_decode(*(t.cpu().numpy() for t in xq)), wv))
+        check(lib.mxfp4a4_linear(bf16(x), *w), O.mx_linear(O.mx_decode(*(t.cpu().numpy() for t in xq)), wv))
+
+
+@pytest.mark.parametrize("M,N", [(2, 37), (16, 20), (20, 70)])
+def test_the_longest_contraction(lib, M, N):
+    """2^20 values of a weight row, and 2^20 weight rows of the transposed product."""
+    import torch
+    announce(f"mxfp4 longest contraction M={M} N={N}")
+    L = 1 << 20
+    rng = np.random.default_rng(M)
+    w, wv = weight(rng, N, L, 118, 124)
+    x = bf16(rng.standard_normal((M, L)).astype(np.float32))
+    check(lib.mxfp4_linear(x, *w), O.mx_linear(values(x), wv))
+    xq = lib.mxfp4_quantize_rows(x)
+    xv = O.mx_decode(*(t.cpu().numpy() for t in xq))
+    expected = O.mx_linear(xv, wv)
+    check(lib.qmm_mxfp4a4(*xq, *w), expected)
+    check(lib.mxfp4a4_linear(x, *w), expected)
+    del wv, xv
+    wt, tv = weight(rng, L, 64, 118, 124)
+    check(lib.mxfp4_linear_backward(x, *wt), O.mx_linear_backward(values(x), tv))
