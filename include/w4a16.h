@@ -411,9 +411,11 @@ int w4a8_linear(const uint16_t* x, const uint32_t* wq, const uint16_t* scales, c
  * dup, codes and the workspace 16-byte aligned, other bf16 buffers 2-byte aligned; an output that
  * shares bytes with an input or another output returns W4A16_ERR_OVERLAP.
  *
- * A decoded weight is one of the 16 values times a power of two and is exact in bf16; scale bytes
- * 253 and 254, which no quantizer of finite values below produces, can exceed bf16's range and then
- * are not defined in the products.  All sums are fp32, rounded to bf16 once.
+ * A decoded weight is one of the 16 values times a power of two and is exact in bf16 up to 2^128.  Scale
+ * bytes 253 and 254, which the quantizer below gives no finite value, can stand for 2^128 and more:
+ * mxfp4_dequantize_rows, the weight-only and the gated products take such values as infinities of
+ * their sign; the 4-bit products never decode to bf16 and take them as they are.  All sums are fp32,
+ * rounded to bf16 once.
  */
 enum mxfp4_type { MXFP4_BF16 = 0, MXFP4_FP32 = 1 };
 
@@ -440,7 +442,8 @@ enum mxfp4_op {
 int mxfp4_quantize_rows(const void* x, int32_t x_type, uint8_t* codes, uint8_t* scales, int64_t R, int64_t K,
                         void* stream);
 
-/* The values of MXFP4 rows as bf16 [R, K] (exact); y 16-byte aligned.  One launch. */
+/* The values of MXFP4 rows as bf16 [R, K], exact below 2^128 and infinities from there on; y 16-byte
+ * aligned.  One launch. */
 int mxfp4_dequantize_rows(const uint8_t* codes, const uint8_t* scales, uint16_t* y, int64_t R, int64_t K,
                           void* stream);
 

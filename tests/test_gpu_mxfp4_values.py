@@ -167,6 +167,48 @@ def test_extreme_scales(lib, M):
         check(lib.mxfp4a4_linear(bf16(x), *w), O.mx_linear(O.mx_decode(*(t.cpu().numpy() for t in xq)), wv))
 
 
+def test_dequantize_the_two_largest_scales(lib):
+    """Scale bytes 253 and 254: 2^128 and above is past bf16 and decodes to an infinity of its sign."""
+    import torch
+    announce("mxfp4_dequantize_rows scales 253 and 254")
+    codes = np.tile(O.mx_pack(np.arange(32).reshape(1, 32) % 16), (2, 1))
+    scales = np.array([[253], [254]], np.uint8)
+    ref = O.mx_decode(codes, scales)
+    ref = np.where(np.abs(ref) >= 2.0 ** 128, np.copysign(np.inf, ref), ref)
+    assert np.isinf(ref).sum(1).tolist() == [8, 16]
+    got = values(lib.mxfp4_dequantize_rows(to_gpu(codes, torch.uint8), to_gpu(scales, torch.uint8)))
+    assert np.array_equal(got, ref) and np.array_equal(np.signbit(got), np.signbit(ref))
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_products_with_the_two_largest_scales(lib, M, N, K):
+    """Weight-only products take such weights as infinities; 4-bit products scale in the matrix core and
+    stay exact up to fp32's range."""
+    import torch
+    announce(f"mxfp4 products with scales 253 and 254 M={M} N={N} K={K}")
+    rng = np.random.default_rng(M + N + 1)
+    (codes, _), _ = weight(rng, N, K)
+    # in every third block of every third weight row, so that finite outputs are left in both directions
+    s = np.full((N, K // 32), 252, np.uint8)
+    s[::3, ::3] = rng.integers(253, 255, s[::3, ::3].shape)
+    w, wv = (codes, to_gpu(s, torch.uint8)), O.mx_decode(codes.cpu().numpy(), s)
+    x, xv = weight(rng, M, K, 60, 64)
+    check(lib.qmm_mxfp4a4(*x, *w), O.mx_linear(xv, wv))
+    check(lib.mxfp4a4_linear(lib.mxfp4_dequantize_rows(*x), *w),
+          O.mx_linear(O.mx_decode(*O.mx_encode(xv)), wv))
+
+    def activations(shape):                            # no zeros: an infinity times zero would be NaN
+        return bf16_values(np.where(rng.random(shape) < 0.5, -1, 1) * rng.uniform(1, 2, shape) * 2.0 ** -60)
+    held = np.where(np.abs(wv) >= 2.0 ** 128, np.copysign(np.inf, wv), wv)
+    assert np.isinf(held).any()
+    with np.errstate(invalid="ignore"):
+        xb = activations((M, K))
+        check(lib.mxfp4_linear(bf16(xb), *w), O.mx_linear(xb, held))
+        if N < 1000:
+            dy = activations((M, N))
+            check(lib.mxfp4_linear_backward(bf16(dy), *w), O.mx_linear_backward(dy, held))
+
+
 @pytest.mark.parametrize("M,N", [(2, 37), (16, 20), (20, 70)])
 def test_the_longest_contraction(lib, M, N):
     """2^20 values of a weight row, and 2^20 weight rows of the transposed product."""

@@ -10,8 +10,8 @@
 //   16x16x128:  lane l holds row (column) l % 16, k = 32 (l / 16) .. + 31
 // so a lane's operand is exactly one block, and byte `sel` of its scale register is that block's e.
 // The converters with a scale operand use only the exponent field of the fp32 scale, the e of the
-// format: e << 23 as a float decodes every block exactly (e = 255 to NaN; 6 * 2^126 and above to
-// infinity in bf16) and encodes with round to nearest even, saturating at 6 (all borders, both
+// format: e << 23 as a float decodes every block exactly (e = 255 to NaN; a value of 2^128 or more,
+// which e = 253 and 254 can give, to an infinity of its sign in bf16) and encodes with round to nearest even, saturating at 6 (all borders, both
 // signs and scales 0 to 254 checked on the MI355X).
 #pragma once
 

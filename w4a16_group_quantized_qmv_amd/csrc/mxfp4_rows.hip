@@ -5,7 +5,8 @@
 //   with an even mantissa bit, and values above 6 (at most 8 by the choice of e) to 6; the sign of x.
 // A block with an infinity or a NaN gets e = 255 (NaN) and codes 0, so that it cannot pass for
 // numbers.  Both directions are exact otherwise: scaling by a power of two rounds nothing that the
-// grid keeps, and every e2m1 * 2^n is a bf16 value.
+// grid keeps, and what a block of finite values is encoded to (e <= 252) is a bf16 value.  Bytes 253 and
+// 254 from elsewhere can stand for 2^128 and more, past bf16: those values become infinities.
 //
 // Bound by memory: 2 (or 4) bytes read and 0.53 written per value.  Rows are contiguous and a whole
 // number of blocks, so the array is a flat list of blocks.  Four lanes share a block, eight values

@@ -176,7 +176,8 @@ def mxfp4_quantize_rows(x, codes=None, scales=None, stream=None):
 
 
 def mxfp4_dequantize_rows(codes, scales, y=None, stream=None):
-    """The values of MXFP4 rows as bf16 ``[R, K]`` (exact); returns y."""
+    """The values of MXFP4 rows as bf16 ``[R, K]`` (exact; 2^128 and above, which only scale bytes 253 and
+    254 reach, as infinities); returns y."""
     _matrix(codes, "codes")
     index = codes.get_device()
     R, K = _weights(codes, scales, "rows", index)
