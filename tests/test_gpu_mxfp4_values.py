@@ -209,6 +209,37 @@ def test_products_with_the_two_largest_scales(lib, M, N, K):
             check(lib.mxfp4_linear_backward(bf16(dy), *w), O.mx_linear_backward(dy, held))
 
 
+@pytest.mark.parametrize("M", [1, 8, 40])
+def test_gates_where_the_sigmoid_vanishes(lib, M):
+    """Gates of +-60 .. 96, exact in fp32, beside up = 1 .. 2^40.  The sigmoid is within (4 + |g|) 2^-23 of its
+    value, or 0 where that is below 2^-126 (off by less than 2^-126 then); the products add a few steps of
+    fp32, of both terms where 1 + g (1 - s) has two, and the rounding to bf16 2^-8."""
+    import torch
+    announce(f"mxfp4 gates where the sigmoid vanishes M={M}")
+    N, K = 144, 64
+    codes = np.zeros((2, N, K), np.uint8)
+    codes[0, :, :2] = codes[1, :, 33:34] = 2           # 1.0: the gate is x[:, 0] + x[:, 1], up takes x[:, 33] = 1
+    exps = np.full((2, N, 2), 127, np.uint8)
+    exps[1, :, 1] += (np.arange(N) % 41).astype(np.uint8)
+    gate, up = ((to_gpu(O.mx_pack(codes[i]), torch.uint8), to_gpu(exps[i], torch.uint8)) for i in range(2))
+    uv = np.ldexp(1.0, np.arange(N) % 41)[None, :]
+    every = np.arange(60, 96, 0.25)
+    every = np.concatenate([-every, every])
+    for first in range(0, every.size, M):
+        x = np.zeros((M, K))
+        gv = np.resize(every[first:first + M], M)[:, None]
+        x[:, :1], x[:, 1:2], x[:, 33] = np.trunc(gv), gv - np.trunc(gv), 1
+        assert np.array_equal(bf16_values(x), x)
+        h = lib.mxfp4_gate_up_swiglu(bf16(x), gate, up)
+        _, dg, du = lib.mxfp4_gate_up_swiglu_backward(bf16(x), gate, up, bf16(np.ones((M, N))))
+        s, rest = 1 / (1 + np.exp(-gv)), 1 / (1 + np.exp(gv))
+        off = s * (4 + np.abs(gv)) * 2.0 ** -23 + np.where(s < 2.0 ** -125, 2.0 ** -126, 0)
+        for got, value, slope, terms in ((h, gv * s * uv, gv * uv, 0), (du, gv * s + 0 * uv, gv + 0 * uv, 0),
+                                         (dg, uv * s * (1 + gv * rest), uv * (1 + np.abs(gv)), uv * s * (1 + np.abs(gv)))):
+            before = np.abs(slope) * off + 2.0 ** -22 * (np.abs(value) + terms)
+            check(got, (value, before + 2.0 ** -8 * (np.abs(value) + before) + 2.0 ** -134))
+
+
 @pytest.mark.parametrize("M,N", [(2, 37), (16, 20), (20, 70)])
 def test_the_longest_contraction(lib, M, N):
     """2^20 values of a weight row, and 2^20 weight rows of the transposed product."""

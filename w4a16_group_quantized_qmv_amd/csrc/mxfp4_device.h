@@ -60,10 +60,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// 1 / (1 + 2^(-z log2 e)) from the hardware's exponential and reciprocal, each within a step of fp32;
-// the product with log2 e is off by half a step of itself, |z| 2^-24 of the result at most.  2^large
-// is infinite and its reciprocal 0, the limit; below z = -87 the hardware's reciprocal
-// flushes a result under 2^-126 to 0, an error of 2^-126 at most.
+// 1 / (1 + 2^(-z log2 e)) from the hardware's exponential and reciprocal, each within a step of fp32.
+// The exponent is off by the constant's rounding (0.23 2^-24 of it) and the product's (2^-24), which
+// makes 1.23 |z| 2^-24 of the result: (4 + |z|) 2^-23 covers all of it.  2^large is infinite and its
+// reciprocal 0, the limit; from z = -87.3 down the hardware's reciprocal flushes a result under 2^-126
+// to 0, an error below 2^-126.
 __device__ __forceinline__ float mx_sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }
