@@ -1,4 +1,4 @@
-"""Where calls with a ``stream`` argument take their memory from, without a GPU.
+"""Where calls with a ``stream`` argument take their memory from, and what they refuse, without a GPU.
 
 torch's allocator keeps one pool per stream and hands a freed block out again in that stream's order.
 A model of torch with such an allocator stands in for it here, and the library's functions are
@@ -223,3 +223,17 @@ def test_a_call_on_a_stream_takes_memory_of_that_stream(model, name, form):
     # and without the argument everything is the current stream's
     results = CALLS[name](torch, a, {})
     assert all(torch.pools.stream_of(t.data_ptr()) == CURRENT and not t.recorded for t in results)
+
+
+@pytest.mark.parametrize("name", ["mxfp4_linear", "mxfp4_linear_backward", "mxfp4a4_linear", "mxfp4_gate_up_swiglu",
+                                  "mxfp4_gate_up_swiglu_backward"])
+def test_a_gradient_is_not_dropped_in_silence(model, name):
+    torch, recorder = model
+    a = arguments(torch)
+    a["x"].requires_grad = a["dy"].requires_grad = True
+    with pytest.raises(ValueError, match="requires a gradient"):
+        CALLS[name](torch, a, {})
+    assert not recorder.calls
+    torch.is_grad_enabled = lambda: False
+    CALLS[name](torch, a, {})
+    assert len(recorder.calls) == 1

@@ -7,6 +7,10 @@ Tensor conventions (all on the GPU, contiguous):
     codes              torch.uint8    [R, K/2]    two codes per byte, the lower index in the low half
     scales             torch.uint8    [R, K/32]   the factor 2^(byte - 127) of 32 values; 255 is NaN
 A weight matrix is its ``(codes, scales)`` pair with R = N output columns; K % 32 == 0.
+
+The calls record nothing for autograd: a gradient is the matching ``..._backward`` call, as in the
+``backward`` of a ``torch.autograd.Function``.  While gradients are recorded, a tensor that requires one
+is refused rather than cut off from its history.
 """
 
 from __future__ import annotations
@@ -82,6 +86,13 @@ def _tensor(t, name, dtype, shape, index=None):
         raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, another on {where}")
 
 
+def _no_history(t, name):
+    """Refuses a tensor whose gradient this call would drop."""
+    if t.requires_grad and _torch().is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this call does not record: call it under torch.no_grad() "
+                         "(or on a detached tensor) and the matching _backward function for the gradient")
+
+
 def _matrix(t, name):
     if _T is None:
         _bind()
@@ -121,6 +132,7 @@ def _output(t, name, shape, x, dtype, stream=None):
             return _empty_for(stream, shape, dtype, x.device)
         return x.new_empty(shape) if x.dtype is dtype else x.new_empty(shape, dtype=dtype)
     _tensor(t, name, dtype, shape, x.get_device())
+    _no_history(t, name)
     return t
 
 
@@ -193,6 +205,7 @@ def _projection(name, op, x, codes, scales, y, split_k, workspace, stream):
     N, K = _weights(codes, scales, "weight", index)
     back = op == MXFP4_LINEAR_BACKWARD
     _tensor(x, "dy" if back else "x", _BF16, (M, N if back else K))
+    _no_history(x, "dy" if back else "x")
     y = _output(y, "dx" if back else "y", (M, K if back else N), x, _BF16, stream)
     _call(name, op, (M, N, K), index, stream, workspace,
           (x.data_ptr(), codes.data_ptr(), scales.data_ptr(), y.data_ptr()), split_k)
@@ -236,6 +249,7 @@ def mxfp4_gate_up_swiglu(x, gate, up, h=None, split_k: int = 0, workspace=None, 
     N, K = _weights(*gate, "gate", index)
     _weights(*up, "up", index, (N, K))
     _tensor(x, "x", _BF16, (M, K))
+    _no_history(x, "x")
     h = _output(h, "h", (M, N), x, _BF16, stream)
     _call("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), index, stream, workspace,
           (x.data_ptr(), gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), h.data_ptr()),
@@ -253,6 +267,8 @@ def mxfp4_gate_up_swiglu_backward(x, gate, up, dh, dx=None, dgate=None, dup=None
     _weights(*up, "up", index, (N, K))
     _tensor(x, "x", _BF16, (M, K))
     _tensor(dh, "dh", _BF16, (M, N), index)
+    _no_history(x, "x")
+    _no_history(dh, "dh")
     dx = _output(dx, "dx", (M, K), x, _BF16, stream)
     dgate = _output(dgate, "dgate", (M, N), x, _BF16, stream)
     dup = _output(dup, "dup", (M, N), x, _BF16, stream)
@@ -298,6 +314,7 @@ class PreparedMxfp4Linear(_Prepared):
         M, _ = _matrix(x, "x")
         N, K = _weights(codes, scales, "weight", x.get_device())
         _tensor(x, "x", _BF16, (M, K))
+        _no_history(x, "x")
         self.M, self.N, self.K, self.y = M, N, K, _output(y, "y", (M, N), x, _BF16)
         self._keep = (x, codes, scales)
         name, op = (("mxfp4a4_linear", MXFP4A4_LINEAR) if four_bit_activations else ("mxfp4_linear", MXFP4_LINEAR))
@@ -317,6 +334,7 @@ class PreparedMxfp4GateUp(_Prepared):
         N, K = _weights(*gate, "gate", x.get_device())
         _weights(*up, "up", x.get_device(), (N, K))
         _tensor(x, "x", _BF16, (M, K))
+        _no_history(x, "x")
         self.M, self.N, self.K, self.h = M, N, K, _output(h, "h", (M, N), x, _BF16)
         self._keep = (x, *gate, *up)
         self._prepare("mxfp4_gate_up_swiglu", MXFP4_GATE_UP, (M, N, K), x.get_device(),
