@@ -237,3 +237,18 @@ def test_a_gradient_is_not_dropped_in_silence(model, name):
     torch.is_grad_enabled = lambda: False
     CALLS[name](torch, a, {})
     assert len(recorder.calls) == 1
+
+
+@pytest.mark.parametrize("workspace", [4096, "room", b"0" * 4096])
+@pytest.mark.parametrize("name", ["mxfp4_linear", "mxfp4_linear_backward", "mxfp4a4_linear", "qmm_mxfp4a4",
+                                  "mxfp4_gate_up_swiglu", "mxfp4_gate_up_swiglu_backward", "qmm_w4a16",
+                                  "w4a16_gate_up_swiglu", "qmm_w4a8", "w4a8_linear"])
+def test_a_workspace_that_is_no_tensor_is_refused(model, name, workspace):
+    torch, recorder = model
+    a = arguments(torch)
+    with pytest.raises(TypeError, match="workspace must be a torch.Tensor"):
+        CALLS[name](torch, a, {"workspace": workspace})
+    if name == "mxfp4_linear":
+        with pytest.raises(TypeError, match="workspace must be a torch.Tensor"):
+            w4.PreparedMxfp4Linear(a["x"], *a["w"], split_k=2, workspace=workspace)
+    assert not recorder.calls

@@ -308,6 +308,8 @@ def _workspace(workspace, nbytes, device, stream=None):
         return None, 0
     if workspace is None:
         workspace = _empty_for(stream, (nbytes + 3) // 4, torch.float32, device, output=False)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
     return workspace, workspace.numel() * workspace.element_size()

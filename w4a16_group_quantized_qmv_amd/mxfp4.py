@@ -137,6 +137,8 @@ def _output(t, name, shape, x, dtype, stream=None):
 
 
 def _check_workspace(workspace, index):
+    if not isinstance(workspace, _T):
+        raise TypeError("workspace must be a torch.Tensor")
     if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
 
