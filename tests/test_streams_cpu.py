@@ -239,7 +239,7 @@ def test_a_gradient_is_not_dropped_in_silence(model, name):
     assert len(recorder.calls) == 1
 
 
-@pytest.mark.parametrize("workspace", [4096, "room", b"0" * 4096])
+@pytest.mark.parametrize("workspace", [4096, "room", b"room"])
 @pytest.mark.parametrize("name", ["mxfp4_linear", "mxfp4_linear_backward", "mxfp4a4_linear", "qmm_mxfp4a4",
                                   "mxfp4_gate_up_swiglu", "mxfp4_gate_up_swiglu_backward", "qmm_w4a16",
                                   "w4a16_gate_up_swiglu", "qmm_w4a8", "w4a8_linear"])
