@@ -189,6 +189,16 @@ def test_plan_split_is_clamped_to_the_steps(op):
     assert w4.mxfp4_plan(OPS[op], 200, 64, 64, 1, CUS)["split_k"] == 1
 
 
+@pytest.mark.parametrize("M,N,K", [(58, 42636, 1216), (62, 33159, 1664), (24, 109405, 1120), (39, 71025, 1088)])
+def test_code_tiles_that_fill_a_compute_unit_alone_are_counted_so(M, N, K):
+    """64 x 128 tiles of codes hold 104 KB of LDS: with more of them than compute units the rest is another
+    round, and the tiles of which two fit (128 x 128) are chosen."""
+    tiles = -(-N // 128)
+    assert tiles > CUS and w4.mxfp4_plan(w4.MXFP4_QMM_A4, M, N, K, 0, CUS)["variant"] == 0
+    # one round of them: the smaller tile
+    assert w4.mxfp4_plan(w4.MXFP4_QMM_A4, M, 9728, 2560, 0, CUS)["variant"] == 2
+
+
 @pytest.mark.parametrize("args,error", [
     ((0, 0, 64, 64), ValueError), ((0, 8, 0, 64), ValueError), ((0, 8, 64, 0), ValueError),
     ((0, 8, 64, 48), ValueError), ((0, 8, 64, (1 << 20) + 32), ValueError), ((0, (1 << 30) + 1, 64, 64), ValueError),

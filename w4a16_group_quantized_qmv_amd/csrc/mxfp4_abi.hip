@@ -93,13 +93,15 @@ int64_t units_of(const Product& p) {
 // Microseconds of one tile on a compute unit, fitted to sweeps of every tile and split on MI355X (24 to
 // 4096 rows; 2560 x 9728, 9728 x 2560, 4096 x 2560 and 1024 x 2560 weights): `fixed` for the first
 // loads and the epilogue, and `step` per pipeline step, alone on its compute unit and (for the tiles
-// of which two fit) with a second one beside it.
+// of which two fit) with a second one beside it.  64 x 128 tiles of codes take 106496 of the 163840 bytes
+// of LDS, so a second one waits (58 x 42636 x 1216 with codes: 334 of them 21.3 us, two rounds; 128 x 128
+// 15.9).
 struct TileCost {
     double fixed, step, step_beside;
 };
 constexpr TileCost kTileCost[3][kNumMxTiles] = {
     // 128 x 128        256 x 256      64 x 128          192 x 256       128 x 256
-    {{3.0, 0.67, 1.2}, {9.0, 1.20, 0}, {4.5, 0.41, 0.85}, {6.0, 1.05, 0}, {5.0, 1.05, 0}},    // kCodes (256 values a step)
+    {{3.0, 0.67, 1.2}, {9.0, 1.20, 0}, {4.5, 0.41, 0}, {6.0, 1.05, 0}, {5.0, 1.05, 0}},       // kCodes (256 values a step)
     {{5.0, 0.46, 1.0}, {10.0, 1.30, 0}, {5.0, 0.32, 0.54}, {8.0, 1.17, 0}, {6.0, 0.80, 0}},   // kRows (64)
     {{5.0, 0.64, 0.9}, {8.0, 1.42, 0}, {5.0, 0.54, 0.9}, {6.0, 1.32, 0}, {5.0, 0.88, 0}},     // kColumns (64)
 };

@@ -623,7 +623,7 @@ namespace {
 
 // Stages of the left operand; CODE_STAGES of the form that stages both operands as they come.  Four
 // stages cover a latency with three steps of loads, at the cost of a second workgroup beside: 64 x 128
-// keeps both.  192 x 256 fits four of the left operand and two of decoded weights into 160 KB (4096 x
+// with decoded weights (64 KB) keeps both, of codes (104 KB) only one fits.  192 x 256 fits four of the left operand and two of decoded weights into 160 KB (4096 x
 // 2560 with 9728 values: 198 us with two, 190 with four; kColumns 211 and 208), 256 x 256 does not;
 // 128 x 128 gained nothing from them.  128 x 256 has two waves a SIMD where 128 x 128 alone on its compute
 // unit has one: 1024 rows of 9728 values on 2560 columns 77 and 61 us, 2048 rows of codes 51 and 43.
