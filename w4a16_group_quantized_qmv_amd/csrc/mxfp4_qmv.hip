@@ -17,10 +17,11 @@
 //    bytes per lane and read back 64 bytes per lane as the blocks lie, chunk c of MFMA column r at
 //    c ^ r, so that 16 columns' reads fall into 16 bank groups.
 //  * The waves' sums and the slices' are added in order by the first threads.
-// Measured on MI355X, in a graph: one row of 9728 x 2560 (2560 values) 5.3 us (2.5 TB/s), 8 rows 7.6, 16
-// rows 9.8; the gated pair 8.4 us (3.1 TB/s); one row of 9728 x 9728 13.9 us (3.6 TB/s); five rows of
-// 151936 x 2560 in the wide form 38 to 40 us (5.2 to 5.4 TB/s).  Small matrices are a few memory
-// latencies, whatever their bytes.
+// Measured on MI355X in a graph, the same weights again (in the last-level cache where they fit) / in turn
+// with copies of 512 MB and more, us: one row of 9728 x 2560 (2560 values) 5.1 / 5.7 (2.3 TB/s), 8 rows
+// 7.9 / 8.1, 16 rows 9.5 / 10.1; the gated pair, one row 8.3 / 8.7 (3.0 TB/s); one row of 9728 x 9728
+// 12.5 / 14.0 (3.6 TB/s); five rows of 151936 x 2560 in the wide form 39 / 41 (5.0 TB/s).  Small matrices
+// are a few memory latencies, whatever their bytes.
 #include "mxfp4_device.h"
 #include "mxfp4_internal.h"
 

@@ -143,7 +143,8 @@ __global__ __launch_bounds__(kRowThreads) void mx_sum_kernel(const float* __rest
     }
 }
 
-// Workgroups: one pass over small arrays, at most eight resident per compute unit's share beyond.
+// Workgroups: one pass over small arrays; above that 8192 (32 for each of 256 compute units, four
+// times what is resident at once), which take chunk after chunk.
 int row_grid(int64_t chunks) {
     return static_cast<int>(std::min<int64_t>((chunks + kRowThreads - 1) / kRowThreads, 256 * 32));
 }

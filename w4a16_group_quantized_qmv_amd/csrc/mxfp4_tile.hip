@@ -20,11 +20,11 @@
 //  * kColumns needs, for one output column, eight consecutive contraction values in a lane, while
 //    the codes are packed along the output columns.  Decoded rows are staged as they come, from
 //    whole 128-byte lines; the operand reads are the transposing ones.  (Bytes exchanged by permutes
-//    before the write, from 2-byte loads: 4096 x 9728 x 2560 took 252 us, this 208.)
+//    before the write, from 2-byte loads: 4096 x 9728 x 2560 took 252 us, this 210 in the same tiles.)
 //  * Of the 128 bytes, MFMA step j of lane half h takes chunk 4 h + j.  For codes a chunk is one
 //    block, so the four scale bytes that a lane needs in a pipeline step are one aligned word of the
 //    row's scales.  (Steps of whole 128-byte lines: taking 64 bytes from each of two lines, which also
-//    gives such words, is twice the requests to L2; 66 us against 58 at 4096 x 9728 x 2560.)
+//    gives such words, is twice the requests to L2; 66 us against 58 at 4096 x 2560 x 9728.)
 //  * The weights are the MFMA's row operand, so a lane's results are four consecutive output
 //    columns of one row; each wave turns its block through LDS and stores whole 16-byte pieces.
 //  * With two weight sets (gate and up) the 32-column blocks of the tile alternate between them, so
@@ -32,13 +32,19 @@
 //  * Split-K: slice z takes a contiguous run of steps and writes fp32 partials; the slices are
 //    summed in order by a second launch, so results do not depend on timing.
 //
-// Bound by the matrix cores from some 500 rows on, at the clock that the card keeps under them (1.9
-// to 2.06 GHz): the 16-bit kinds keep them busy 61 to 63% of the time, kCodes 39 to 45%.  On MI355X,
-// 4096 rows, 9728 x 2560 weights: kCodes 58 us (3.5 PF), kRows 190 to 205 us (1.0 PF; contraction of
-// 9728 or 2560), kColumns 208 us (0.98 PF), kGlu 340 us for both products (1.2 PF).  The rest is the
-// L2's latency and traffic: with the left operand's loads left out kRows took 161 us and kColumns 169.
-// Below, the number of workgroups bounds it (the cost model chooses among tiles and splits): kRows of
-// 512 rows 36 us, kGlu 47 to 52 us.
+// Bound by the matrix cores from some 500 rows on, at the clock that the card keeps under them (2.0 to
+// 2.2 GHz at 4096 rows, 2.5 under light work).  Traced on MI355X, 4096 rows x weight rows x values; in
+// brackets the rate and the share of a compute unit's busy cycles in which its matrix cores are:
+//   kCodes    x 9728 x 2560   69 us (3.0 PF, 49%)     x 2560 x 9728   61 us (3.3 PF, 56%)
+//   kRows     x 9728 x 2560  190 us (1.07 PF, 70%)    x 2560 x 9728  184 us (1.11 PF, 72%)
+//   kColumns  x 9728 x 2560  201 us (1.01 PF, 61%)
+//   kGlu      x 9728 x 2560  322 us for both products (1.27 PF, 71%); kGluGrad 367 us (60%)
+// The rest is the L2's latency and traffic (the 16-bit kinds fetch some 300 MB, three to eight times
+// what they cannot do without): with the left operand's loads left out kRows took 161 us and kColumns
+// 169.  kCodes stages one step ahead in all tiles but 64 x 128, and 608 tiles on 256 compute units
+// take three rounds.  Below 500 rows the number of workgroups bounds it (the cost model chooses among
+// tiles and splits): kRows of 512 x 9728 x 2560 33 us, of 509 x 2560 x 9728 39 and 4 for the slices'
+// sum, kGlu of 512 x 9728 x 2560 54.
 #include "mxfp4_device.h"
 #include "mxfp4_internal.h"
 
