@@ -99,3 +99,24 @@ def test_a_captured_call_on_a_side_stream(lib):
         for n in calls:
             assert all(torch.equal(a, b) for a, b in zip(out[n], eager[n])), (n, turn)
             assert all(torch.equal(a, b) for a, b in zip(again[n], eager[n])), (n, turn)
+
+
+@pytest.mark.parametrize("form", ["object", "handle"])
+def test_the_default_stream_given_from_another(lib, form):
+    """The default stream, whose handle is 0, given while another one is current."""
+    import torch
+    call = _calls(lib)["mxfp4_linear"]
+    x = _random((M, K), 9)
+    alone = call(x)[0].clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    default = torch.cuda.default_stream()
+    announce(f"mxfp4_linear on the default stream from another, {form}")
+    with torch.cuda.stream(side):
+        got, = call(x, stream=default if form == "object" else 0)
+        assert _pool_of(got.data_ptr()) == default.cuda_stream == 0
+        assert torch.cuda.current_stream() == side
+        side.wait_stream(default)
+        copy = got.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(copy, alone)

@@ -90,6 +90,9 @@ class Model:
             def __init__(self, handle, device=None):
                 self.cuda_stream = int(handle)
 
+        def external(handle, device=None):
+            return Stream(handle or 0x900)             # (a null handle gives one of torch's own streams)
+
         @contextlib.contextmanager
         def stream(s):
             before, pools.current = pools.current, s.cuda_stream
@@ -106,7 +109,8 @@ class Model:
             setattr(self, name, name)
         self.is_grad_enabled = lambda: True
         self._C = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda index: pools.current, _cuda_getDevice=lambda: 0)
-        self.cuda = types.SimpleNamespace(Stream=Stream, ExternalStream=Stream, stream=stream,
+        self.cuda = types.SimpleNamespace(Stream=Stream, ExternalStream=external, stream=stream,
+                                          default_stream=lambda device=None: Stream(0),
                                           device=lambda index: contextlib.nullcontext(),
                                           current_device=lambda: 0,
                                           current_stream=lambda device=None: Stream(pools.current))
@@ -141,7 +145,7 @@ class Recorder:
                     if isinstance(v, int) and v >= 1 << 40:
                         pointers.append(v)
             stream = args[-1]
-            self.calls.append((name, pointers, getattr(stream, "value", stream)))
+            self.calls.append((name, pointers, getattr(stream, "value", stream) or 0))
             return 0
         return call
 
@@ -193,11 +197,12 @@ def arguments(t):
             "q8": (new((M, K), t.int8), new((M,), t.float32), new((M, w4.w4a8_xsum_cols(K)), t.bfloat16))}
 
 
-@pytest.mark.parametrize("form", ["object", "handle"])
+@pytest.mark.parametrize("form", ["object", "handle", "default object", "default handle"])
 @pytest.mark.parametrize("name", list(CALLS))
 def test_a_call_on_a_stream_takes_memory_of_that_stream(model, name, form):
     torch, recorder = model
-    stream = torch.cuda.Stream(SIDE) if form == "object" else SIDE
+    side = 0 if "default" in form else SIDE
+    stream = torch.cuda.Stream(side) if "object" in form else side
     a = arguments(torch)
     known = set(torch.pools.owner)
     # queued on the current stream; the workspace returns to the current stream's pool at once
@@ -207,12 +212,12 @@ def test_a_call_on_a_stream_takes_memory_of_that_stream(model, name, form):
     gc.collect()
     # the same on the side stream, which does not wait for the current one
     outputs = CALLS[name](torch, a, {"stream": stream})
-    assert [c[2] for c in recorder.calls] == [CURRENT, SIDE] and {c[0] for c in recorder.calls} == {name}
+    assert [c[2] for c in recorder.calls] == [CURRENT, side] and {c[0] for c in recorder.calls} == {name}
     mine = {p for p in recorder.calls[1][1] if p not in known}
     assert len(mine) == len(own) >= len(outputs)
     assert not mine & own, "memory of a call that is still queued on the current stream"
     for p in mine:
-        assert torch.pools.stream_of(p) == SIDE, "memory of another stream's pool"
+        assert torch.pools.stream_of(p) == side, "memory of another stream's pool"
     # outputs are read elsewhere: the current stream keeps them from the side stream's next call
     kept = {t.data_ptr() for t in outputs}
     assert all(CURRENT in t.recorded for t in outputs)

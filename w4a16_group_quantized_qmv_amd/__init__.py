@@ -293,8 +293,11 @@ def _empty_for(stream, shape, dtype, device, output=True):
     torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream),
-                                                                                      device=device)
+    if isinstance(stream, torch.cuda.Stream):
+        s = stream
+    else:                                     # (ExternalStream takes 0 for none and gives one of torch's own)
+        handle = _stream_handle(stream)
+        s = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     with torch.cuda.stream(s):
         t = torch.empty(shape, dtype=dtype, device=device)
     if output:
