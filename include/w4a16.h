@@ -84,7 +84,9 @@ enum w4a16_path {
     W4A16_PATH_PER_PROJECTION = 7, /* reported by w4a16_grouped_plan only: one w4a16_linear dispatch
                                   per projection                                                  */
     W4A16_PATH_MXFP4 = 8,      /* reported by mxfp4_plan only: MXFP4 tiles                         */
-    W4A16_PATH_MXFP4_QMV = 9   /* reported by mxfp4_plan only: the MXFP4 decode kernel             */
+    W4A16_PATH_MXFP4_QMV = 9,  /* reported by mxfp4_plan only: the MXFP4 decode kernel             */
+    W4A16_PATH_W8A8 = 10,      /* reported by w8a8_plan only: int8 tiles                           */
+    W4A16_PATH_W8A8_QMV = 11   /* reported by w8a8_plan only: the int8 decode kernel               */
 };
 
 /* Launch plan chosen by the dispatch policy (filled by w4a16_plan). */
@@ -516,6 +518,164 @@ int mxfp4_gate_up_swiglu_backward(const uint16_t* x, const uint8_t* codes_gate, 
                                   const uint8_t* codes_up, const uint8_t* scales_up, const uint16_t* dh, uint16_t* dx,
                                   uint16_t* dgate, uint16_t* dup, int64_t M, int64_t N, int64_t K, int32_t split_k,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * W8A8: int8 weights with one scale per output column, int8 activations with one scale per row (token).
+ *
+ *   codes   int8 [R, K]    16-byte aligned
+ *   scales  fp32 [R]       a row stands for scale * code
+ *
+ * A weight matrix [N, K] is such a pair with R = N; w8a8_quantize_rows makes one from a bf16 or fp32
+ * matrix, and any symmetric per-row int8 checkpoint is one already.  Activations are quantized by the same
+ * rule, in the calls that take bf16 x.  Ownership, streams, asynchrony and the status codes are those stated
+ * at the top of this file, and so is the rule that all checks come before any launch.  Limits: 1 <= rows,
+ * N <= 2^30 (activation rows below 2^24), 16 <= K <= 131056 (a sum of K products of codes fits an int32),
+ * K % 16 == 0; x, dy, codes and the workspace 16-byte aligned, other bf16 buffers 2-byte and fp32 and
+ * int32 buffers 4-byte aligned; an output that shares bytes with an input or another output returns
+ * W4A16_ERR_OVERLAP.
+ *
+ * Sums of codes are exact integers; the product with both scales is fp32, rounded to bf16 once.
+ */
+enum w8a8_type { W8A8_BF16 = 0, W8A8_FP32 = 1 };
+
+enum w8a8_op {
+    W8A8_LINEAR = 0,                    /* w8a8_linear                                            */
+    W8A8_LINEAR_BACKWARD = 1,           /* w8a8_linear_backward                                   */
+    W8A8_QMM = 2,                       /* qmm_w8a8                                               */
+    W8A8_EXPERTS_LINEAR = 3,            /* w8a8_experts_linear                                    */
+    W8A8_EXPERTS_LINEAR_BACKWARD = 4,   /* w8a8_experts_linear_backward                           */
+    W8A8_EXPERTS_GATE_UP = 5,           /* w8a8_experts_gate_up_swiglu                            */
+    W8A8_EXPERTS_GATE_UP_BACKWARD = 6   /* w8a8_experts_gate_up_swiglu_backward                   */
+};
+
+/*
+ * Quantize rows of x (bf16 or fp32, x_type), all in fp32:
+ *
+ *     a = max |x|,  scale = a / 127,  inv = 127 / a  (correctly rounded),
+ *     code = clamp(rint(x * inv), -127, 127)          (product rounded to fp32, ties to even).
+ *
+ * Rows with a < 2^-110 get scale 0 and codes 0, rows that hold an infinity or a NaN the scale NaN and codes
+ * 0, so that what is computed from them is NaN.  One launch.  Errors: W4A16_ERR_NULL, _ERR_SHAPE, _ERR_ALIGN,
+ * _ERR_OVERLAP, _ERR_UNSUPPORTED (another x_type), _ERR_LAUNCH.
+ */
+int w8a8_quantize_rows(const void* x, int32_t x_type, int8_t* codes, float* scales, int64_t R, int64_t K, void* stream);
+
+/*
+ * Launch plan of a W8A8 operator (enum w8a8_op; E matrices of N rows and K values, T activation rows, R
+ * output rows; E = 1 and T = R = M without experts; backward passes report the launch that computes dx).
+ * split_k as for qmm_w4a16 (experts: 0 or 1).  workspace_bytes is what the operator's call needs, num_cus as in
+ * w4a16_plan.  grid_y is the most that the experts' row counts can need.  Pure host arithmetic.  Returns
+ * W4A16_OK, _ERR_NULL, _ERR_SHAPE, _ERR_UNSUPPORTED (an unknown op, experts with a split) or _ERR_DEVICE.
+ */
+int w8a8_plan(int32_t op, int64_t E, int64_t T, int64_t R, int64_t N, int64_t K, int32_t split_k, int32_t num_cus,
+              w4a16_plan_t* out);
+
+/*
+ * Product of two quantized operands, y[m, n] = bf16( (sum_k xq[m, k] codes[n, k]) * scales[n] * xs[m] ): X [M, K]
+ * as xq, xs, W [N, K] as codes, scales.  With too little workspace a policy split is dropped (the unsplit
+ * plan computes the same); a forced one returns W4A16_ERR_WORKSPACE.
+ */
+int qmm_w8a8(const int8_t* xq, const float* xs, const int8_t* codes, const float* scales, uint16_t* y, int64_t M, int64_t N,
+             int64_t K, int32_t split_k, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One-call projection of bf16 x: w8a8_quantize_rows of x into the start of `workspace`, then qmm_w8a8 with
+ * the rest of it for partials (the same results).  A missing workspace, or one without room for the
+ * activations, returns W4A16_ERR_WORKSPACE; for the fewest rows one kernel quantizes on the way and no
+ * workspace is needed (w8a8_plan says so).
+ */
+int w8a8_linear(const uint16_t* x, const int8_t* codes, const float* scales, uint16_t* y, int64_t M, int64_t N, int64_t K,
+                int32_t split_k, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of w8a8_linear's input, dx = dy . W with dy [M, N], dx [M, K]; the rounding of x to codes passes
+ * gradients on as if it were not there, and the weights are frozen codes without a gradient.  A weight enters as
+ * bf16(scale * code).  N <= 2^20.  Workspace as for qmm_w8a8; where N % 8 != 0 it also holds a copy of dy with
+ * padded rows, and W4A16_ERR_WORKSPACE is returned without room for that.
+ */
+int w8a8_linear_backward(const uint16_t* dy, const int8_t* codes, const float* scales, uint16_t* dx, int64_t M, int64_t N,
+                         int64_t K, int32_t split_k, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Mixtures of experts.  A row is a pair of a token and an expert that it goes to; rows lie in the order of their
+ * experts.  `offsets` int32 [E + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1.  `tokens` int32 [R]: the
+ * rows' tokens.  `positions` int32 [T, top_k]: the rows of a token's experts, -1 for none.  They are made by
+ * experts_route, or by the caller; they are read on the device and not checked, but no call reads or writes outside
+ * its buffers, whatever they hold: offsets are taken into [0, R], positions outside [0, R) are skipped, and a row whose
+ * token is outside [0, T) has activations of zeros.  Rows that no expert has (behind offsets[E]) are left as they
+ * were in every output.
+ *
+ * Limits: 1 <= E <= 1024, 1 <= top_k <= min(E, 64), T <= 2^24, T * top_k <= 2^30.
+ */
+
+/* Workspace bytes of experts_route (0 for a few tokens and for sizes outside the limits). */
+uint64_t experts_route_workspace_bytes(int64_t T, int64_t E);
+
+/*
+ * Router: from logits [T, E] (bf16 or fp32, enum w8a8_type) the top_k largest of each token, equal ones the lowest
+ * expert first, in falling order:
+ *
+ *     experts int32 [T, top_k], weights fp32 [T, top_k]: their softmax (renormalize), or their part of the
+ *     softmax over all experts; and positions, tokens [T * top_k] and offsets as above.
+ *
+ * Logits of minus infinity, and NaN, are never chosen: a token with fewer than top_k others gets expert -1, weight 0
+ * and position -1, and the entries of tokens behind offsets[E] are -1.  A token whose logits hold a NaN gets NaN
+ * weights.  Rows of one expert are in the order of their tokens; a call repeats bit for bit.
+ */
+int experts_route(const void* logits, int32_t type, float* weights, int32_t* experts, int32_t* positions, int32_t* tokens,
+                  int32_t* offsets, int64_t T, int64_t E, int32_t top_k, int32_t renormalize, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Gradient of the logits (dlogits, the type of logits) from dweights fp32 [T, top_k]: p_e (dw_e - sum_j p_j dw_j) with
+ * the softmax p, and dw = 0 for experts that were not chosen.  One launch. */
+int experts_route_backward(const void* logits, int32_t type, const int32_t* experts, const float* dweights, void* dlogits,
+                           int64_t T, int64_t E, int32_t top_k, int32_t renormalize, void* stream);
+
+/* out[t] = sum_j weights[t, j] * y[positions[t, j]] with y [R, N], out [T, N] in bf16, the sum in fp32 and rounded
+ * once; weights NULL stands for ones (the sum of gradients of gathered rows).  One launch. */
+int experts_combine(const uint16_t* y, const int32_t* positions, const float* weights, uint16_t* out, int64_t T, int32_t top_k,
+                    int64_t R, int64_t N, void* stream);
+
+/* Its gradients from dout [T, N]: dy[positions[t, j]] = weights[t, j] * dout[t], dweights[t, j] = <dout[t],
+ * y[positions[t, j]]> (0 for no row).  Rows of dy at no position are left as they were.  One launch. */
+int experts_combine_backward(const uint16_t* dout, const uint16_t* y, const int32_t* positions, const float* weights,
+                             uint16_t* dy, float* dweights, int64_t T, int32_t top_k, int64_t R, int64_t N, void* stream);
+
+/*
+ * Projection by experts: row r of expert e is y[r] = Q(x[tokens[r]]) . W_e^T with codes int8 [E, N, K], scales
+ * [E, N], x bf16 [T, K], y [R, N], Q the quantization of w8a8_quantize_rows.  tokens NULL: x[r], T = R.
+ * T * K < 2^31 with tokens.  A workspace as w8a8_plan says.
+ */
+int w8a8_experts_linear(const uint16_t* x, const int8_t* codes, const float* scales, const int32_t* offsets,
+                        const int32_t* tokens, uint16_t* y, int64_t E, int64_t T, int64_t R, int64_t N, int64_t K,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of its rows: dx[r] = dy[r] . W_e, [R, K] (where rows were gathered, experts_combine adds those of a
+ * token up).  As w8a8_linear_backward otherwise. */
+int w8a8_experts_linear_backward(const uint16_t* dy, const int8_t* codes, const float* scales, const int32_t* offsets,
+                                 uint16_t* dx, int64_t E, int64_t R, int64_t N, int64_t K, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Gated half of the experts' feed-forward blocks, h[r] = silu(Q(x) . Wg_e^T) * (Q(x) . Wu_e^T), both projections,
+ * activation and product in one kernel. */
+int w8a8_experts_gate_up_swiglu(const uint16_t* x, const int8_t* codes_gate, const float* scales_gate,
+                                const int8_t* codes_up, const float* scales_up, const int32_t* offsets,
+                                const int32_t* tokens, uint16_t* h, int64_t E, int64_t T, int64_t R, int64_t N, int64_t K,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward pass from x and dh [R, N]; both projections are computed again.  With s = sigmoid(g):
+ *
+ *     dup = dh g s,   dgate = dh u s (1 + g (1 - s)),   dx = dgate . Wg_e + dup . Wu_e.
+ *
+ * dgate and dup [R, N] are rounded to bf16 once.  dx [R, K], a row per pair, is computed from both before that
+ * rounding, times the weights' scales and rounded to bf16 for the matrix cores.  N <= 2^20.
+ */
+int w8a8_experts_gate_up_swiglu_backward(const uint16_t* x, const int8_t* codes_gate, const float* scales_gate,
+                                         const int8_t* codes_up, const float* scales_up, const uint16_t* dh,
+                                         const int32_t* offsets, const int32_t* tokens, uint16_t* dx, uint16_t* dgate,
+                                         uint16_t* dup, int64_t E, int64_t T, int64_t R, int64_t N, int64_t K,
+                                         void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

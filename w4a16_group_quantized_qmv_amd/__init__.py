@@ -132,9 +132,25 @@ def load():
             "mxfp4a4_linear": [u16p, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
             "mxfp4_gate_up_swiglu": [u16p, vp, vp, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
             "mxfp4_gate_up_swiglu_backward": [u16p, vp, vp, vp, vp, u16p, u16p, u16p, u16p, i64, i64, i64, i32, vp,
-                                              size, vp]}.items():
+                                              size, vp],
+            "w8a8_quantize_rows": [vp, i32, vp, vp, i64, i64, vp],
+            "w8a8_plan": [i32, i64, i64, i64, i64, i64, i32, i32, ctypes.POINTER(Plan)],
+            "qmm_w8a8": [vp, vp, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
+            "w8a8_linear": [u16p, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
+            "w8a8_linear_backward": [u16p, vp, vp, u16p, i64, i64, i64, i32, vp, size, vp],
+            "w8a8_experts_linear": [u16p, vp, vp, vp, vp, u16p, i64, i64, i64, i64, i64, vp, size, vp],
+            "w8a8_experts_linear_backward": [u16p, vp, vp, vp, u16p, i64, i64, i64, i64, vp, size, vp],
+            "w8a8_experts_gate_up_swiglu": [u16p, vp, vp, vp, vp, vp, vp, u16p, i64, i64, i64, i64, i64, vp, size, vp],
+            "w8a8_experts_gate_up_swiglu_backward": [u16p, vp, vp, vp, vp, u16p, vp, vp, u16p, u16p, u16p, i64, i64, i64,
+                                                     i64, i64, vp, size, vp],
+            "experts_route": [vp, i32, vp, vp, vp, vp, vp, i64, i64, i32, i32, vp, size, vp],
+            "experts_route_backward": [vp, i32, vp, vp, vp, i64, i64, i32, i32, vp],
+            "experts_combine": [u16p, vp, vp, u16p, i64, i32, i64, i64, vp],
+            "experts_combine_backward": [u16p, u16p, vp, vp, u16p, vp, i64, i32, i64, i64, vp]}.items():
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = argtypes
+    lib.experts_route_workspace_bytes.restype = ctypes.c_uint64
+    lib.experts_route_workspace_bytes.argtypes = [i64, i64]
     lib.w4a16_time_next_launch.restype = ctypes.c_int
     lib.w4a16_time_next_launch.argtypes = [vp, vp]
     _LIB = lib
@@ -642,4 +658,7 @@ class PreparedW4A8:
 from . import mxfp4 as _mxfp4  # noqa: E402  (uses the helpers above)
 from .mxfp4 import *  # noqa: E402,F401,F403
 
-__all__ += _mxfp4.__all__
+from . import w8a8 as _w8a8  # noqa: E402
+from .w8a8 import *  # noqa: E402,F401,F403
+
+__all__ += _mxfp4.__all__ + _w8a8.__all__
