@@ -243,7 +243,8 @@ def ragged(rng, E, R, kind):
 EXPERTS = [(1, 5, 24, 48, 64, "random"), (4, 7, 14, 100, 96, "random"), (8, 200, 400, 136, 272, "random"), (3, 100, 300, 257, 400, "gaps"),
            (16, 16, 16, 64, 2560, "random"), (64, 3, 24, 1216, 256, "random"), (70, 40, 90, 50, 80, "gaps"), (5, 900, 900, 72, 528, "one"),
            (6, 1300, 2600, 300, 144, "random"), (1000, 30, 60, 24, 32, "random"), (4, 3000, 6000, 520, 64, "each"),
-           (2, 40, 40, 33, 16, "none"), (9, 2, 18, 48, 4112, "each"), (128, 60, 240, 80, 9728, "random")]
+           (2, 40, 40, 33, 16, "none"), (9, 2, 18, 48, 4112, "each"), (128, 60, 240, 80, 9728, "random"),
+           (5, 3000, 6000, 520, 1040, "random"), (3, 2100, 4200, 1000, 528, "gaps")]
 
 
 def expert_problem(E, T, R, N, K, kind, gather):
@@ -326,9 +327,9 @@ def test_experts_gate_up(lib, E, T, R, N, K, kind, gather):
 def test_the_experts_shapes_reach_every_form(lib):
     plans = {op: [lib.w8a8_plan(getattr(lib, op), T, N, K, 0, 0, E, R) for E, T, R, N, K, _ in EXPERTS] for op in (
         "W8A8_EXPERTS_LINEAR", "W8A8_EXPERTS_LINEAR_BACKWARD", "W8A8_EXPERTS_GATE_UP", "W8A8_EXPERTS_GATE_UP_BACKWARD")}
-    for op in ("W8A8_EXPERTS_LINEAR", "W8A8_EXPERTS_GATE_UP"):
-        assert {(p["path"], p["variant"]) for p in plans[op]} >= {(lib.PATH_W8A8_QMV, 0), (lib.PATH_W8A8_QMV, 1)}
-    assert all(p["path"] == lib.PATH_W8A8 for op in plans if "BACKWARD" in op for p in plans[op])
+    for op in plans:
+        assert all(p["path"] == lib.PATH_W8A8 for p in plans[op])
+        assert len({p["variant"] for p in plans[op]}) >= 2, op
 
 
 @pytest.mark.parametrize("R", [12, 600])

@@ -35,11 +35,6 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return (b >> 31) ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
-}
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
@@ -60,10 +55,119 @@ struct RouteArgs {
     bool fp32, renormalize;
 };
 
-// One token by one wave: lane j < top_k gets the j-th chosen expert (-1 for none) and its weight.  PER logits a
-// lane, expert lane + 64 i.
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
+}
+
+// Sixteen lanes are a row of the DPP: rotations by 8, 4, 2 and 1 reduce over it, and leave the result in each.
+template <int N>
+__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xF, 0xF, false));
+}
+template <typename F>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, F f) {
+    v = f(v, row_rotate<8>(v));
+    v = f(v, row_rotate<4>(v));
+    v = f(v, row_rotate<2>(v));
+    return f(v, row_rotate<1>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+    return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+__device__ __forceinline__ float row_max(float v) {
+    return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+}
+
+// The logits of a token on sixteen lanes, PER of each: WIDE (E = 16 PER) consecutive ones, loaded and stored in
+// whole pieces, else every sixteenth.
+template <int PER, bool WIDE>
+__device__ __forceinline__ int expert_of(int lane16, int i) { return WIDE ? lane16 * PER + i : lane16 + 16 * i; }
+
+template <int PER, bool WIDE, bool FP32>
+__device__ __forceinline__ void load_row(const void* logits, int64_t token, int E, int lane16, float (&v)[PER]) {
+    if constexpr (WIDE) {
+        constexpr int WORDS = PER * (FP32 ? 4 : 2) / 4;
+        const uint32_t* in = static_cast<const uint32_t*>(logits) + (token * 16 + lane16) * WORDS;
+        uint32_t w[WORDS];
+        if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const u32x4_t q = load16(in + 4 * i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[4 * i + e] = q[e];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[i] = in[i];
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            v[i] = __uint_as_float(FP32 ? w[i * WORDS / PER] : (i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = expert_of<PER, false>(lane16, i);
+            v[i] = e < E ? load_logit(logits, FP32, token * E + e) : -__builtin_inff();
+        }
+    }
+}
+
+// One token by sixteen lanes: lane j < top_k <= 16 gets the j-th chosen expert (-1 for none) and its weight.
+template <int PER, bool WIDE, bool FP32>
+__device__ __forceinline__ void select16(const RouteArgs& p, int64_t token, int lane16, int& expert, float& weight) {
+    uint32_t key[PER];
+    bool nan = false;
+    {
+        float v[PER];
+        load_row<PER, WIDE, FP32>(p.logits, token, p.E, lane16, v);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            nan |= v[i] != v[i];
+            key[i] = order_key(v[i]);
+        }
+    }
+    auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
+    expert = -1;
+    float chosen = 0.f, top = 0.f, sum = 0.f;
+    for (int j = 0; j < p.top_k; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+        best = row_reduce(best, larger);
+        // of equal ones the lowest expert
+        uint32_t at = 0xFFFFu;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i)
+            if (key[i] == best) at = expert_of<PER, WIDE>(lane16, i);
+        at = row_reduce(at, [](uint32_t a, uint32_t b) { return min(a, b); });
+        if (j == 0) {
+            top = key_value(best);
+            if (!p.renormalize) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) sum += key[i] ? expf(key_value(key[i]) - top) : 0.f;
+            }
+        }
+        if (lane16 == j && best != 0) {
+            expert = at;
+            chosen = key_value(best);
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (expert_of<PER, WIDE>(lane16, i) == static_cast<int>(at)) key[i] = 0;
+    }
+    const float mine = expert >= 0 ? expf(chosen - top) : 0.f;
+    sum = row_sum(p.renormalize ? mine : sum);
+    weight = expert >= 0 ? mine / sum : 0.f;
+    if (row_reduce(nan, [](uint32_t a, uint32_t b) { return a | b; })) weight = __builtin_nanf("");
+}
+
+// The same by a whole wave, for up to 64 chosen experts: lane j < top_k gets the j-th.  Expert lane + 64 i.
 template <int PER>
-__device__ __forceinline__ void select(const RouteArgs& p, int64_t token, int lane, int& expert, float& weight) {
+__device__ __forceinline__ void select64(const RouteArgs& p, int64_t token, int lane, int& expert, float& weight) {
     float v[PER];
     uint32_t key[PER];
     bool nan = false;
@@ -95,7 +199,7 @@ __device__ __forceinline__ void select(const RouteArgs& p, int64_t token, int la
         const uint32_t won = static_cast<uint32_t>(pair >> 32);
         if (won == 0) break;                                   // (uniform) nothing is left
         const int e = 0xFFFF - static_cast<int>(static_cast<uint32_t>(pair));
-        const float logit = __uint_as_float((won >> 31) ? won & 0x7FFFFFFFu : ~won);
+        const float logit = key_value(won);
         if (j == 0) top = logit;
         if (lane == j) {
             expert = e;
@@ -118,16 +222,25 @@ __device__ __forceinline__ void select(const RouteArgs& p, int64_t token, int la
     if (__ballot(nan)) weight = __builtin_nanf("");
 }
 
+// How a kernel chooses: by sixteen lanes (PER of 16 PER >= E), or by waves (PER of 64 PER >= E).
+template <int PER_, bool WIDE_, bool FP32_, bool WAVE_>
+struct Choice {
+    static constexpr int PER = PER_, experts = (WAVE_ ? 64 : 16) * PER_;
+    static constexpr bool WIDE = WIDE_, FP32 = FP32_, WAVE = WAVE_;
+};
+
 // The chosen experts and weights of up to 64 tokens, and their masks.
-template <int PER>
+template <typename C>
 __device__ __forceinline__ void select_block(const RouteArgs& p, unsigned long long* mask, int64_t first, int count) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) mask[e] = 0;
     __syncthreads();
-    for (int t = wave; t < count; t += kRouteWaves) {
+    constexpr int LANES = C::WAVE ? 64 : 16;
+    const int lane = threadIdx.x % LANES;
+    for (int t = threadIdx.x / LANES; t < count; t += 64 * kRouteWaves / LANES) {
         int expert;
         float weight;
-        select<PER>(p, first + t, lane, expert, weight);
+        if constexpr (C::WAVE) select64<C::PER>(p, first + t, lane, expert, weight);
+        else select16<C::PER, C::WIDE, C::FP32>(p, first + t, lane, expert, weight);
         if (lane < p.top_k) {
             const int64_t at = (first + t) * p.top_k + lane;
             p.experts[at] = expert;
@@ -178,12 +291,12 @@ __device__ __forceinline__ void place_block(const RouteArgs& p, const unsigned l
 }
 
 // All of it in one workgroup.
-template <int PER>
+template <typename C>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_small_kernel(const RouteArgs p) {
-    __shared__ unsigned long long mask[64 * PER];
-    __shared__ int start[64 * PER], scratch[kRouteWaves];
+    __shared__ unsigned long long mask[C::experts];
+    __shared__ int start[C::experts], scratch[kRouteWaves];
     const int count = static_cast<int>(p.T);
-    select_block<PER>(p, mask, 0, count);
+    select_block<C>(p, mask, 0, count);
     const int total = expert_starts(p.E, start, scratch, [&](int e) { return __popcll(mask[e]); });
     if (static_cast<int>(threadIdx.x) < p.E) p.offsets[threadIdx.x] = start[threadIdx.x];
     if (threadIdx.x == 0) p.offsets[p.E] = total;
@@ -192,12 +305,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_small_kernel(const Rou
 }
 
 // Else three launches: choice and counts of every 64 tokens, the counts' sums over the blocks, the placing.
-template <int PER>
+template <typename C>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_select_kernel(const RouteArgs p) {
-    __shared__ unsigned long long mask[64 * PER];
+    __shared__ unsigned long long mask[C::experts];
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kTokens;
     const int count = static_cast<int>(min(static_cast<int64_t>(kTokens), p.T - first));
-    select_block<PER>(p, mask, first, count);
+    select_block<C>(p, mask, first, count);
     for (int e = threadIdx.x; e < p.E; e += blockDim.x)
         p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = __popcll(mask[e]);
 }
@@ -255,69 +368,79 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_place_kernel(const Rou
         p.tokens[r] = -1;
 }
 
-// A wave per token.  The gradients of the chosen experts go to their columns through a row in LDS.
-template <int PER>
-__global__ __launch_bounds__(256) void route_backward_kernel(const void* __restrict__ logits, bool fp32,
-                                                             const int* __restrict__ experts,
+// Sixteen lanes per token; its chosen experts and their gradients are read by all of them.
+template <int PER, bool WIDE, bool FP32>
+__global__ __launch_bounds__(256) void route_backward_kernel(const void* __restrict__ logits, const int* __restrict__ experts,
                                                              const float* __restrict__ dweights, void* __restrict__ dlogits,
                                                              int64_t T, int E, int top_k, bool renormalize) {
-    __shared__ float row[4][64 * PER];
-    __shared__ uint8_t picked[4][64 * PER];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * 4 + wave;
-    if (token >= T) return;
-    float v[PER];
+    const int lane16 = threadIdx.x & 15;
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+    if (token >= T) return;                                    // (sixteen lanes together)
+    float v[PER], d[PER];
+    load_row<PER, WIDE, FP32>(logits, token, E, lane16, v);
+    uint64_t in = 0;                                           // bit i: the softmax is over this lane's i-th
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        v[i] = e < E ? load_logit(logits, fp32, token * E + e) : -__builtin_inff();
+        d[i] = 0.f;
         nan |= v[i] != v[i];
-        row[wave][e] = 0.f;
-        picked[wave][e] = 0;
+        if (!renormalize && v[i] > -__builtin_inff()) in |= 1ull << i;
     }
-    wave_lds_fence();
-    if (lane < top_k) {
-        const int e = experts[token * top_k + lane];
-        if (e >= 0 && e < E) {
-            row[wave][e] = dweights[token * top_k + lane];
-            picked[wave][e] = 1;
+    for (int j = 0; j < top_k; ++j) {
+        const int e = experts[token * top_k + j];
+        const float dw = dweights[token * top_k + j];
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (expert_of<PER, WIDE>(lane16, i) == e) {
+                d[i] = dw;
+                in |= v[i] > -__builtin_inff() ? 1ull << i : 0ull;
+            }
+    }
+    float top = -__builtin_inff(), sum = 0.f, c = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (in >> i & 1) top = fmaxf(top, v[i]);
+    top = row_max(top);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        v[i] = in >> i & 1 ? expf(v[i] - top) : 0.f;
+        sum += v[i];
+    }
+    sum = row_sum(sum);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        v[i] = in >> i & 1 ? v[i] / sum : 0.f;
+        if (in >> i & 1) c += v[i] * d[i];
+    }
+    c = row_sum(c);
+    nan = row_reduce(nan, [](uint32_t a, uint32_t b) { return a | b; }) != 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) d[i] = nan ? __builtin_nanf("") : in >> i & 1 ? v[i] * (d[i] - c) : 0.f;
+    if constexpr (WIDE) {
+        constexpr int WORDS = PER * (FP32 ? 4 : 2) / 4;
+        uint32_t* out = static_cast<uint32_t*>(dlogits) + (token * 16 + lane16) * WORDS;
+        uint32_t w[WORDS];
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            w[i] = FP32 ? __float_as_uint(d[i * PER / WORDS]) : pack_bf16(d[2 * i % PER], d[(2 * i + 1) % PER]);
+        if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < WORDS; i += 4)
+                *reinterpret_cast<u32x4_t*>(out + i) = u32x4_t{w[i], w[i + 1], w[i + 2], w[i + 3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) out[i] = w[i];
         }
-    }
-    wave_lds_fence();
-    const bool any_nan = __ballot(nan) != 0;
-    float top = -__builtin_inff();
-    bool in[PER];
+    } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        in[i] = v[i] > -__builtin_inff() && (!renormalize || picked[wave][lane + 64 * i]);
-        if (in[i]) top = fmaxf(top, v[i]);
-    }
-    top = wave_max(top);
-    float p[PER], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        p[i] = in[i] ? expf(v[i] - top) : 0.f;
-        sum += p[i];
-    }
-    sum = wave_sum(sum);
-    float c = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        p[i] = in[i] ? p[i] / sum : 0.f;
-        if (in[i]) c += p[i] * row[wave][lane + 64 * i];
-    }
-    c = wave_sum(c);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        if (e >= E) continue;
-        float d = in[i] ? p[i] * (row[wave][e] - c) : 0.f;
-        if (any_nan) d = __builtin_nanf("");
-        if (fp32)
-            static_cast<float*>(dlogits)[token * E + e] = d;
-        else
-            static_cast<uint16_t*>(dlogits)[token * E + e] = f32_to_bf16_bits(d);
+        for (int i = 0; i < PER; ++i) {
+            const int e = expert_of<PER, false>(lane16, i);
+            if (e >= E) continue;
+            if (FP32)
+                static_cast<float*>(dlogits)[token * E + e] = d[i];
+            else
+                static_cast<uint16_t*>(dlogits)[token * E + e] = f32_to_bf16_bits(d[i]);
+        }
     }
 }
 
@@ -331,22 +454,38 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
     const int n = 8 * static_cast<int>(at - token * pieces);
     if (token >= T) return;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int j = 0; j < top_k; ++j) {
-        const int64_t row = positions[token * top_k + j];
-        if (row < 0 || row >= R) continue;
-        const float w = weights ? weights[token * top_k + j] : 1.f;
-        const uint16_t* in = y + row * N + n;
-        if constexpr (WIDE) {
-            const u32x4_t v = load16(in);
+    // four rows on their way at a time
+    for (int j0 = 0; j0 < top_k; j0 += 4) {
+        int64_t row[4];
+        float w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum[2 * i] += w * __uint_as_float(v[i] << 16);
-                sum[2 * i + 1] += w * __uint_as_float(v[i] & 0xFFFF0000u);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t slot = token * top_k + min(j0 + j, top_k - 1);
+            row[j] = positions[slot];
+            w[j] = weights ? weights[slot] : 1.f;
+            if (j0 + j >= top_k || row[j] >= R) row[j] = -1;
+        }
+        if constexpr (WIDE) {
+            u32x4_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = row[j] < 0 ? u32x4_t{0, 0, 0, 0} : load16(y + row[j] * N + n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (row[j] < 0) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sum[2 * i] += w[j] * __uint_as_float(v[j][i] << 16);
+                    sum[2 * i + 1] += w[j] * __uint_as_float(v[j][i] & 0xFFFF0000u);
+                }
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (n + i < N) sum[i] += w * bf16_bits_to_f32(in[i]);
+            for (int j = 0; j < 4; ++j) {
+                if (row[j] < 0) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (n + i < N) sum[i] += w[j] * bf16_bits_to_f32(y[row[j] * N + n + i]);
+            }
         }
     }
     uint16_t* to = out + token * N + n;
@@ -403,14 +542,25 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const uint16_t* _
     if (lane == 0) dweights[slot] = dot;
 }
 
-// body(std::integral_constant<int, logits of a lane>).
+// body(a Choice by sixteen lanes) for E experts; rows of logits at `base` (and `other`).
 template <typename F>
-hipError_t for_experts(int E, F body) {
-    if (E <= 64) return body(std::integral_constant<int, 1>{});
-    if (E <= 128) return body(std::integral_constant<int, 2>{});
-    if (E <= 256) return body(std::integral_constant<int, 4>{});
-    if (E <= 512) return body(std::integral_constant<int, 8>{});
-    return body(std::integral_constant<int, 16>{});
+hipError_t for_experts(int E, bool fp32, const void* base, const void* other, F body) {
+    auto types = [&](auto per) {
+        constexpr int PER = decltype(per)::value;
+        const uintptr_t where = reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(other);
+        const bool wide = E == 16 * PER && (where & (fp32 ? (PER >= 4 ? 15 : 3) : (PER >= 8 ? 15 : 3))) == 0;
+        if (fp32) return wide ? body(Choice<PER, true, true, false>{}) : body(Choice<PER, false, true, false>{});
+        if constexpr (PER >= 2)
+            if (wide) return body(Choice<PER, true, false, false>{});
+        return body(Choice<PER, false, false, false>{});
+    };
+    if (E <= 16) return types(std::integral_constant<int, 1>{});
+    if (E <= 32) return types(std::integral_constant<int, 2>{});
+    if (E <= 64) return types(std::integral_constant<int, 4>{});
+    if (E <= 128) return types(std::integral_constant<int, 8>{});
+    if (E <= 256) return types(std::integral_constant<int, 16>{});
+    if (E <= 512) return types(std::integral_constant<int, 32>{});
+    return types(std::integral_constant<int, 64>{});
 }
 
 }  // namespace
@@ -426,13 +576,13 @@ hipError_t launch_experts_route(const void* logits, bool fp32, int top_k, bool r
     const RouteArgs args{logits, weights, experts, positions, tokens, offsets, ws, ws ? ws + static_cast<int64_t>(blocks) * E : nullptr,
                          T, E, top_k, blocks, fp32, renormalize};
     const dim3 threads(64 * kRouteWaves);
-    return for_experts(E, [&](auto per) {
-        constexpr int PER = decltype(per)::value;
+    auto run = [&](auto choice) {
+        using C = decltype(choice);
         if (T <= kTokens) {
-            hipLaunchKernelGGL(route_small_kernel<PER>, dim3(1), threads, 0, stream, args);
+            hipLaunchKernelGGL(route_small_kernel<C>, dim3(1), threads, 0, stream, args);
             return hipGetLastError();
         }
-        hipLaunchKernelGGL(route_select_kernel<PER>, dim3(blocks), threads, 0, stream, args);
+        hipLaunchKernelGGL(route_select_kernel<C>, dim3(blocks), threads, 0, stream, args);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(route_scan_kernel, dim3((E + kScanExperts - 1) / kScanExperts), dim3(kScanExperts * kScanRuns), 0,
@@ -441,15 +591,21 @@ hipError_t launch_experts_route(const void* logits, bool fp32, int top_k, bool r
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(route_place_kernel, dim3(blocks), threads, 0, stream, args);
         return hipGetLastError();
-    });
+    };
+    if (top_k > 16) {
+        if (E <= 128) return run(Choice<2, false, false, true>{});
+        return E <= 512 ? run(Choice<8, false, false, true>{}) : run(Choice<16, false, false, true>{});
+    }
+    return for_experts(E, fp32, logits, nullptr, run);
 }
 
 hipError_t launch_experts_route_backward(const void* logits, bool fp32, const int* experts, const float* dweights,
                                          void* dlogits, int64_t T, int E, int top_k, bool renormalize,
                                          hipStream_t stream) {
-    return for_experts(E, [&](auto per) {
-        hipLaunchKernelGGL(route_backward_kernel<decltype(per)::value>, dim3(static_cast<uint32_t>((T + 3) / 4)), dim3(256), 0,
-                           stream, logits, fp32, experts, dweights, dlogits, T, E, top_k, renormalize);
+    return for_experts(E, fp32, logits, dlogits, [&](auto choice) {
+        using C = decltype(choice);
+        hipLaunchKernelGGL((route_backward_kernel<C::PER, C::WIDE, C::FP32>), dim3(static_cast<uint32_t>((T + 15) / 16)), dim3(256), 0,
+                           stream, logits, experts, dweights, dlogits, T, E, top_k, renormalize);
         return hipGetLastError();
     });
 }

@@ -59,7 +59,7 @@ uint64_t gradient_bytes(int32_t op, const Sizes& d) {
 
 struct Product {
     bool decode, quantize;   // the decode kernel; activations quantized in it
-    int rows;                // decode: rows of a workgroup
+    W8QmvShape qmv;
     int tile;
     int split;
     int64_t M, N;            // output rows and columns
@@ -73,10 +73,10 @@ struct TileCost {
 };
 constexpr TileCost kTileCost[kNumW8Tiles] = {
     // 128 x 128       256 x 256      64 x 128       128 x 256      32 x 256       64 x 256
-    {3.0, 0.60, 1.0}, {8.0, 1.20, 0}, {4.5, 0.41, 0}, {5.0, 0.80, 0}, {4.5, 0.50, 0}, {5.0, 0.60, 0}};
+    {3.0, 0.60, 1.0}, {8.0, 1.20, 0}, {4.5, 0.41, 0}, {5.0, 0.80, 0}, {4.5, 0.50, 0}, {5.0, 0.60, 0}, {1000, 1000, 0}, {1000, 1000, 0}, {1000, 1000, 0}};
 constexpr TileCost kColumnCost[kNumW8ColumnTiles] = {
     // 64 x 128          128 x 256       192 x 256
-    {5.0, 0.54, 0.9}, {5.0, 0.90, 0}, {6.0, 1.35, 0}};
+    {5.0, 0.54, 0.9}, {5.0, 0.90, 0}, {6.0, 1.35, 0}, {1000,1000,0},{1000,1000,0},{1000,1000,0}};
 // A split's second launch, and its partials written and read per output (8 bytes at about 4 TB/s).
 constexpr double kSplitCost = 3.5, kPartialCost = 2e-6;
 constexpr int64_t kMaxSplit = 8;
@@ -93,7 +93,7 @@ int64_t row_blocks(const Sizes& d, bool experts, int bm) {
     return experts ? std::min(d.R, d.R / bm + d.E) : ceil_div(d.R, bm);
 }
 
-// The decode kernel serves up to 16 rows of one matrix, and experts that have few rows each.
+// The decode kernel serves up to 16 rows of one matrix.
 Product product_of(int32_t op, const Sizes& d, int32_t split_k, int64_t cus, bool last) {
     Product p{};
     const bool experts = has_experts(op), back = is_backward(op) && last;
@@ -101,14 +101,18 @@ Product product_of(int32_t op, const Sizes& d, int32_t split_k, int64_t cus, boo
     p.N = back ? d.K : d.N;
     p.split = 1;
     const int sets = is_gated(op) ? 2 : 1;
-    if (!is_backward(op) && split_k == 0 && (experts ? d.R <= 16 || d.R <= 2 * d.E : d.R <= kW8QmvRows)) {
-        W8QmvShape s;
+    if (!is_backward(op) && !experts && split_k == 0 && d.R <= kW8QmvRows) {
+        // Waves: eight short shares where few workgroups have to bring everything on its way, fewer where there are many
+        // (1 x 9728 x 2560: 8 waves 6.3 us, 4 6.3, 2 7.0; 100000 x 2560: 46, 47, 45; 2560 x 9728: 7.3, 9.7, 14.0).
+        // Rows quantized on the way: one or two short ones (1 x 9728 x 2560 7.5 us, in two launches 9.3; 2 x 2560 x 9728
+        // 10.1 and 10.4; 4 x 9728 x 2560 11.7 and 9.9).
+        const int rows = static_cast<int>(d.R), K = static_cast<int>(d.K);
+        const int64_t blocks = ceil_div(d.N, kW8QmvColumns);
+        const int waves = blocks <= 2 * cus ? 8 : blocks <= 8 * cus ? 4 : 2;
         p.decode = true;
-        p.rows = static_cast<int>(std::min<int64_t>(d.R, kW8QmvRows));
-        const bool few = op != W8A8_QMM && (experts ? d.R <= d.E : d.R <= 4);
-        if (few) p.quantize = w8_qmv_shape(sets, experts ? std::min(p.rows, 8) : p.rows, static_cast<int>(d.K), true, &s);
-        if (p.quantize && experts) p.rows = std::min(p.rows, 8);
-        p.tiles = row_blocks(d, experts, p.rows) * ceil_div(p.N, kW8QmvColumns);
+        p.quantize = op == W8A8_LINEAR && rows * d.K <= 16384 && w8_qmv_shape(rows, std::max(waves, (K + 2047) / 2048), K, true, &p.qmv);
+        if (!p.quantize) w8_qmv_shape(rows, waves, K, false, &p.qmv);
+        p.tiles = ceil_div(p.N, kW8QmvColumns);
         if (p.tiles * 64 * kW8QmvWaves < kMaxThreads) return p;
         p.decode = p.quantize = false;
     }
@@ -226,7 +230,7 @@ W8TileArgs tile_args(const Sizes& d, const Product& p, const int32_t* offsets, c
 // A forward product of codes (or, where the plan says so, of bf16 rows): the kernel and a split's sum.
 int run_forward(W8Epilogue epi, const Product& p, W8TileArgs& args, void* partials, hipStream_t stream) {
     args.ws = static_cast<int*>(partials);
-    if (p.decode) return to_status(launch_w8_qmv(epi, p.rows, args, stream));
+    if (p.decode) return to_status(launch_w8_qmv(p.qmv, args, stream));
     const hipError_t e = launch_w8_tile(epi, p.tile, args, stream);
     if (e != hipSuccess || p.split == 1) return to_status(e);
     return to_status(launch_w8_sum(args.ws, args.a_scales, args.w_scales[0], args.y[0], p.M, static_cast<int>(p.N), p.split, stream));
@@ -387,14 +391,12 @@ int w8a8_plan(int32_t op, int64_t E, int64_t T, int64_t R, int64_t N, int64_t K,
     out->k_waves = 1;
     out->variant = p.tile;
     if (p.decode) {
-        W8QmvShape q;
-        w8_qmv_shape(is_gated(op) ? 2 : 1, p.rows, static_cast<int>(K), p.quantize, &q);
         out->path = W4A16_PATH_W8A8_QMV;
-        out->tile_m = p.rows;
+        out->tile_m = p.qmv.rows;
         out->tile_n = kW8QmvColumns;
-        out->tile_k = 64;
-        out->block_threads = 64 * q.waves;
-        out->k_waves = q.waves;
+        out->tile_k = kW8Step;
+        out->block_threads = 64 * p.qmv.waves;
+        out->k_waves = p.qmv.waves;
         out->variant = p.quantize;
     }
     out->grid_x = static_cast<int32_t>(ceil_div(p.N, out->tile_n));

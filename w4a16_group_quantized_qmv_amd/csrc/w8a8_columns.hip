@@ -41,49 +41,34 @@ __device__ __forceinline__ u32x4_t decode8(uint32_t lo, uint32_t hi, float scale
     return r;
 }
 
-template <bool EXPERTS, bool SCALED, int BM, int BN, int WR, int WC, int STAGES>
-__global__ __launch_bounds__(64 * WR * WC) void w8_columns_kernel(const W8ColumnsArgs p, int tiles_m, int tiles_n) {
-    constexpr int NW = WR * WC, NT = 64 * NW;
-    constexpr int MI = BM / WR / 32, NI = BN / WC / 32;
-    static_assert(NW % 2 == 0 && BM % (8 * NW) == 0, "direct loads: whole rows, one chunk order");
+struct Place {
+    int expert, m0, m_end, c0, z;
+};
+// One object per stage, so that a direct load into one is not taken for an input of reads of the others.
+struct Stages {
+    uint8_t *a0, *a1, *a2, *a3, *b0, *b1;
+};
+
+template <bool EXPERTS, bool SCALED, int MI, int NI, int WR, int WC, int STAGES>
+__device__ __forceinline__ void w8_columns(const W8ColumnsArgs& p, const Stages& lds, const Place& place) {
+    constexpr int NW = WR * WC, NT = 64 * NW, BM = 32 * MI * WR, BN = 32 * NI * WC;
+    static_assert(NW % 2 == 0, "direct loads: one chunk order");
     static_assert(BN * 2 == NT, "32 codes per thread and step");
     static_assert(STAGES == 2 || STAGES == 4, "a round of four steps");
     constexpr bool kDeep = STAGES == 4;
-    __shared__ __attribute__((aligned(16))) uint8_t a0[BM * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t a1[BM * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t a2[kDeep ? BM * 128 : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t a3[kDeep ? BM * 128 : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t b0[BN * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t b1[BN * 128];
     auto a_stage = [&](auto ic) -> uint8_t* {
         constexpr int i = decltype(ic)::value % STAGES;
-        if constexpr (i == 0) return a0;
-        else if constexpr (i == 1) return a1;
-        else if constexpr (i == 2) return a2;
-        else return a3;
+        if constexpr (i == 0) return lds.a0;
+        else if constexpr (i == 1) return lds.a1;
+        else if constexpr (i == 2) return lds.a2;
+        else return lds.a3;
     };
-    auto b_stage = [&](auto ic) -> uint8_t* { return decltype(ic)::value % 2 ? b1 : b0; };
+    auto b_stage = [&](auto ic) -> uint8_t* { return decltype(ic)::value % 2 ? lds.b1 : lds.b0; };
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave / WC, wc = wave % WC;
-
-    int z = 0, expert = 0, first = 0, m_end = p.R, tm, tn;
-    if constexpr (EXPERTS) {
-        ExpertTile tile;
-        if (!find_expert_tile<kBandM>(p.offsets, p.E, p.R, BM, tiles_n, blockIdx.x, tile)) return;
-        expert = tile.expert;
-        first = tile.first;
-        m_end = tile.end;
-        tm = tile.tm;
-        tn = tile.tn;
-    } else {
-        const int tiles = tiles_m * tiles_n;
-        const int work = xcd_remap(blockIdx.x, tiles * p.split);
-        z = work / tiles;
-        band_order<kBandM>(work - z * tiles, tiles_m, tiles_n, tm, tn);
-    }
-    const int m0 = first + tm * BM, c0 = tn * BN;
+    const int z = place.z, expert = place.expert, m0 = place.m0, m_end = place.m_end, c0 = place.c0;
 
     const int N = p.N, K = p.K;                              // contraction, output columns
     const int set_steps = (N + 63) / 64;
@@ -92,7 +77,7 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_columns_kernel(const W8Column
     const int t_end = static_cast<int>(static_cast<int64_t>(z + 1) * steps / p.split);
 
     // ---- gradient rows
-    constexpr int A_LOADS = BM / (8 * NW);
+    constexpr int A_LOADS = (BM + 8 * NW - 1) / (8 * NW);     // (rows behind the tile's last are outside the buffer)
     const int own_chunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
     const int row_bytes = 2 * p.pitch;
     const uint32_t a_off = static_cast<uint32_t>((8 * wave + (lane >> 3)) * row_bytes) + 16u * own_chunk;
@@ -268,7 +253,7 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_columns_kernel(const W8Column
     constexpr int WCOLS = NI * 32, PITCH = WCOLS * 2 + 16, PIECES = WCOLS / 8;
     static_assert((NW / 2) * 32 * PITCH <= BN * 128, "the waves' regions fit the weight stages");
     w8_loads_done_barrier<0>();
-    uint8_t* region = ((wave & 1) ? b1 : b0) + (wave >> 1) * (32 * PITCH);
+    uint8_t* region = ((wave & 1) ? lds.b1 : lds.b0) + (wave >> 1) * (32 * PITCH);
     const bool wide = (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -299,33 +284,99 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_columns_kernel(const W8Column
     }
 }
 
+// The tile's height by the rows that are there.
+template <bool EXPERTS, bool SCALED, int MI, int NI, int WR, int WC, int STAGES>
+__device__ __forceinline__ void w8_columns_of_height(const W8ColumnsArgs& p, const Stages& lds, const Place& place) {
+    if constexpr (MI > 1) {
+        if (place.m_end - place.m0 <= 32 * (MI - 1) * WR) {
+            w8_columns_of_height<EXPERTS, SCALED, MI - 1, NI, WR, WC, STAGES>(p, lds, place);
+            return;
+        }
+    }
+    w8_columns<EXPERTS, SCALED, MI, NI, WR, WC, STAGES>(p, lds, place);
+}
+
+template <bool EXPERTS, bool SCALED, int MI, int NI, int WR, int WC, int STAGES>
+__global__ __launch_bounds__(64 * WR * WC) void w8_columns_kernel(const W8ColumnsArgs p, int height, int tiles_m, int tiles_n,
+                                                                  int whole, int cut) {
+    constexpr int BN = 32 * NI * WC;
+    constexpr int ROWS = (32 * MI * WR + 8 * WR * WC - 1) / (8 * WR * WC) * (8 * WR * WC);    // whole loads of all waves
+    __shared__ __attribute__((aligned(16))) uint8_t a0[ROWS * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t a1[ROWS * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t a2[STAGES > 2 ? ROWS * 128 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t a3[STAGES > 2 ? ROWS * 128 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t b0[BN * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t b1[BN * 128];
+    const Stages lds{a0, a1, a2, a3, b0, b1};
+    Place place{0, 0, 0, 0, 0};
+    if constexpr (EXPERTS) {
+        ExpertTile tile;
+        if (!find_expert_tile<kBandM>(p.offsets, p.E, p.R, height, tiles_n, p.cus, blockIdx.x, tile)) return;
+        place.expert = tile.expert;
+        const int rows = (height + tile.cut - 1) / tile.cut, m = tile.first + tile.tm * height;
+        place.m0 = m + tile.piece * rows;
+        place.m_end = min(min(tile.end, m + height), place.m0 + rows);
+        if (place.m0 >= place.m_end) return;
+        place.c0 = tile.tn * BN;
+    } else {
+        // the first `whole` workgroups take whole tiles, the others tiles cut into `cut` pieces of rows
+        const int tiles = tiles_m * tiles_n;
+        int work = blockIdx.x, piece = 0;
+        if (work < whole) {
+            work = xcd_remap(work, whole);
+        } else {
+            const int rest = xcd_remap(work - whole, gridDim.x - whole);
+            work = whole + rest / cut;
+            piece = rest % cut;
+        }
+        place.z = work / tiles;
+        int tm, tn;
+        band_order<kBandM>(work - place.z * tiles, tiles_m, tiles_n, tm, tn);
+        const int rows = blockIdx.x < static_cast<unsigned>(whole) ? height : (height + cut - 1) / cut;
+        place.m0 = tm * height + piece * rows;
+        place.m_end = min(min(p.R, (tm + 1) * height), place.m0 + rows);
+        place.c0 = tn * BN;
+        if (place.m0 >= place.m_end) return;
+    }
+    w8_columns_of_height<EXPERTS, SCALED, MI, NI, WR, WC, STAGES>(p, lds, place);
+}
+
 }  // namespace
 
-const W8TileShape kW8ColumnTiles[kNumW8ColumnTiles] = {{64, 128, 4}, {128, 256, 8}, {192, 256, 8}};
+const W8TileShape kW8ColumnTiles[kNumW8ColumnTiles] = {{64, 128, 4}, {128, 256, 8}, {192, 256, 8}, {256, 256, 8}, {256, 256, 8}, {128, 256, 8}};
 
 namespace {
 
-template <int BM, int BN, int WR, int WC, int STAGES>
+template <int MI, int NI, int WR, int WC, int STAGES>
 hipError_t launch_shape(const W8ColumnsArgs& args, hipStream_t stream) {
+    constexpr int BN = 32 * NI * WC;
+    const int BM = args.height > 0 ? std::min(args.height, 32 * MI * WR) : 32 * MI * WR;
     const int tiles_n = (args.K + BN - 1) / BN;
     const int tiles_m = args.offsets ? static_cast<int>(std::min<int64_t>(args.R, args.R / BM + args.E)) : (args.R + BM - 1) / BM;
-    const dim3 grid(static_cast<uint32_t>(tiles_m) * tiles_n * args.split), block(64 * WR * WC);
+    const int tiles = tiles_m * tiles_n * args.split, cut = std::max(args.cut, 1);
+    // (experts: the kernel cuts, into at most 192 pieces more than tiles)
+    const int whole = cut > 1 ? tiles / args.cus * args.cus : tiles;
+    const int more = args.offsets && args.cus > 0 ? 3 * args.cus / 4 : (tiles - whole) * (cut - 1);
+    const dim3 grid(static_cast<uint32_t>(tiles + more)), block(64 * WR * WC);
     auto run = [&](auto kernel) {
-        W4A16_LAUNCH(kernel, grid, block, 0, stream, args, tiles_m, tiles_n);
+        W4A16_LAUNCH(kernel, grid, block, 0, stream, args, BM, tiles_m, tiles_n, whole, cut);
         return hipGetLastError();
     };
-    if (!args.w_scales[0]) return run(w8_columns_kernel<true, false, BM, BN, WR, WC, STAGES>);
-    return args.offsets ? run(w8_columns_kernel<true, true, BM, BN, WR, WC, STAGES>)
-                        : run(w8_columns_kernel<false, true, BM, BN, WR, WC, STAGES>);
+    if (!args.w_scales[0]) return run(w8_columns_kernel<true, false, MI, NI, WR, WC, STAGES>);
+    return args.offsets ? run(w8_columns_kernel<true, true, MI, NI, WR, WC, STAGES>)
+                        : run(w8_columns_kernel<false, true, MI, NI, WR, WC, STAGES>);
 }
 
 }  // namespace
 
 hipError_t launch_w8_columns(int tile, const W8ColumnsArgs& args, hipStream_t stream) {
     switch (tile) {
-        case 0: return launch_shape<64, 128, 2, 2, 4>(args, stream);
-        case 1: return launch_shape<128, 256, 2, 4, 4>(args, stream);
-        case 2: return launch_shape<192, 256, 2, 4, 2>(args, stream);
+        case 0: return launch_shape<1, 2, 2, 2, 4>(args, stream);
+        case 1: return launch_shape<2, 2, 2, 4, 4>(args, stream);
+        case 2: return launch_shape<3, 2, 2, 4, 2>(args, stream);
+        case 3: return launch_shape<4, 2, 2, 4, 2>(args, stream);
+        case 4: return launch_shape<8, 1, 1, 8, 2>(args, stream);
+        case 5: return launch_shape<4, 1, 1, 8, 4>(args, stream);
         default: return hipErrorInvalidValue;
     }
 }

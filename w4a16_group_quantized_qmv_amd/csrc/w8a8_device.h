@@ -52,14 +52,16 @@ __device__ __forceinline__ uint32_t w8_code(float x, float inverse) {
 struct ExpertTile {
     int expert, first, end;     // the expert's rows
     int tm, tn;
+    int piece, cut;             // of a tile that is cut into pieces of rows
 };
 
-// Tile number `block` of the experts' tiles of BM rows x tiles_n columns of tiles, in an order that gives
-// each XCD whole experts where it can; false where there are fewer tiles.  Every wave calls it, with all
-// lanes; the result is uniform.
+// Tile number `block` of the experts' tiles of BM rows x tiles_n columns of tiles, in an order that gives each XCD
+// whole experts where it can; false where there are fewer tiles.  What is left after whole rounds over `cus`
+// compute units is cut into two or four pieces where all of them run at once (cus 0: never).  Every wave calls
+// it, with all lanes; the result is uniform.
 template <int BAND>
 __device__ __forceinline__ bool find_expert_tile(const int* __restrict__ offsets, int E, int R, int BM, int tiles_n,
-                                                 int block, ExpertTile& out) {
+                                                 int cus, int block, ExpertTile& out) {
     const int lane = threadIdx.x & 63;
     const int per = (E + 63) >> 6;
     auto rows_of = [&](int e, int& first, int& end) {
@@ -78,9 +80,28 @@ __device__ __forceinline__ bool find_expert_tile(const int* __restrict__ offsets
         const int v = __shfl_up(sum, d, 64);
         if (lane >= d) sum += v;
     }
-    const int64_t total = static_cast<int64_t>(__builtin_amdgcn_readlane(sum, 63)) * tiles_n;
-    if (block >= total) return false;
-    const int work = xcd_remap(block, static_cast<int>(min(total, static_cast<int64_t>(gridDim.x))));
+    // (offsets that fall could count rows twice: what the grid does not hold is left out)
+    const int64_t all = static_cast<int64_t>(__builtin_amdgcn_readlane(sum, 63)) * tiles_n;
+    const int total = static_cast<int>(min(all, static_cast<int64_t>(gridDim.x)));
+    int whole = total;
+    out.cut = 1;
+    if (cus > 0 && total > cus) {
+        const int rest = total % cus;
+        out.cut = 4 * rest <= cus ? 4 : 2 * rest <= cus ? 2 : 1;
+        if (out.cut > 1) whole = total - rest;
+    }
+    const int items = whole + (total - whole) * out.cut;
+    if (block >= items) return false;
+    int work;
+    if (block < whole) {
+        work = xcd_remap(block, whole);
+        out.piece = 0;
+        out.cut = 1;
+    } else {
+        const int item = xcd_remap(block - whole, items - whole);
+        work = whole + item / out.cut;
+        out.piece = item % out.cut;
+    }
     const uint64_t past = __ballot(static_cast<int64_t>(sum) * tiles_n > work);
     const int owner = __builtin_ctzll(past);
     int before = __builtin_amdgcn_readlane(sum - mine, owner);

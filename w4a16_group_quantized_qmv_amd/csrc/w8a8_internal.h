@@ -39,6 +39,9 @@ struct W8TileArgs {
     const int* tokens;
     int E, T, R, N, K;
     int split;
+    int height;                // rows of a tile, at most the shape's; 0: all of those
+    int cut, cus;              // one matrix: what is left of the tiles after whole rounds over `cus` compute units is
+                               // cut into this many pieces of rows
 };
 
 // The transposed product: dx[r, k] = sum_s sum_n g_s[r, n] w_scale_s[n] w_s[n, k]; without w_scales the rows of
@@ -52,28 +55,30 @@ struct W8ColumnsArgs {
     const int* offsets;
     int E, R, N, K;
     int pitch, sets, split;
+    int height, cut, cus;      // as above
 };
 
 struct W8TileShape {
     int bm, bn, waves;
 };
-constexpr int kNumW8Tiles = 6;
+constexpr int kNumW8Tiles = 9;
 extern const W8TileShape kW8Tiles[kNumW8Tiles];
 constexpr int kW8Step = 128;          // values of the contraction in one pipeline step
 hipError_t launch_w8_tile(W8Epilogue epi, int tile, const W8TileArgs& args, hipStream_t stream);
 
-// Decode rows: workgroups of 16 weight rows (of each set) x at most `rows` rows of one expert, whose `waves`
-// waves share the contraction.
+// Decode rows (at most 16 of one matrix): workgroups of 16 weight rows whose `waves` waves take `share` lines of 128
+// codes of the contraction each.
 constexpr int kW8QmvRows = 16, kW8QmvColumns = 16, kW8QmvWaves = 16;
+constexpr int kW8QuantizeRows = 2;      // rows that a workgroup quantizes for itself
 struct W8QmvShape {
-    int rows, waves, share, batch;   // share: units of 64 codes a wave takes, `batch` of them in flight
+    int rows, waves, share;
     size_t lds;
 };
-// quantize: activations are quantized by every workgroup for itself; false where its LDS could not hold them.
-bool w8_qmv_shape(int sets, int rows, int K, bool quantize, W8QmvShape* out);
-hipError_t launch_w8_qmv(W8Epilogue epi, int rows, const W8TileArgs& args, hipStream_t stream);
+// False where such workgroups are not possible (quantize: rows quantized by every workgroup for itself).
+bool w8_qmv_shape(int rows, int waves, int K, bool quantize, W8QmvShape* out);
+hipError_t launch_w8_qmv(const W8QmvShape& shape, const W8TileArgs& args, hipStream_t stream);
 
-constexpr int kNumW8ColumnTiles = 3;
+constexpr int kNumW8ColumnTiles = 6;
 extern const W8TileShape kW8ColumnTiles[kNumW8ColumnTiles];
 constexpr int kW8ColumnStep = 64;
 hipError_t launch_w8_columns(int tile, const W8ColumnsArgs& args, hipStream_t stream);

@@ -2,65 +2,81 @@
 #include "w8a8_device.h"
 #include "w8a8_internal.h"
 
+#include <type_traits>
+
 namespace w4a16 {
 namespace {
 
-// A workgroup of WAVES waves per row.  The row's magnitudes are reduced first, its codes made from a second
-// read, which comes from the L2 (a row is at most 512 KB).
-template <bool FP32, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void w8_quantize_kernel(const void* __restrict__ x, int8_t* __restrict__ codes,
-                                                                 float* __restrict__ scales, int K) {
-    constexpr int NT = 64 * WAVES;
-    __shared__ float red[WAVES];
-    const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x, chunks = K / 8;
+// WAVES waves per row, HELD chunks of eight values a lane: they stay in registers between the reduction of the row's
+// magnitudes and its codes (HELD 0: longer rows are read twice, the second time from the L2).  Bound by reading
+// and writing once: 4096 x 2560 bf16, 31 MB, takes QQQ us.
+template <bool FP32, int WAVES, int HELD>
+__global__ __launch_bounds__(256) void w8_quantize_kernel(const void* __restrict__ x, int8_t* __restrict__ codes,
+                                                          float* __restrict__ scales, int64_t R, int K) {
+    constexpr int NT = 64 * WAVES, ROWS = 4 / WAVES;
+    __shared__ uint32_t red[4];
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / NT;
+    const int tid = threadIdx.x % NT, chunks = K / 8;
+    if (WAVES < 4 && row >= R) return;
     const uint8_t* in = static_cast<const uint8_t*>(x) + row * K * (FP32 ? 4 : 2);
-    auto load8 = [&](int c, float (&v)[8]) {
+    struct Chunk {
+        u32x4_t a, b;
+    };
+    auto load = [&](int c) {
+        Chunk v{};
         if constexpr (FP32) {
-            const u32x4_t a = load16(in + 32 * static_cast<size_t>(c)), b = load16(in + 32 * static_cast<size_t>(c) + 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = __uint_as_float(a[i]);
-                v[4 + i] = __uint_as_float(b[i]);
-            }
+            v.a = load16(in + 32 * static_cast<size_t>(c));
+            v.b = load16(in + 32 * static_cast<size_t>(c) + 16);
         } else {
-            const u32x4_t a = load16(in + 16 * static_cast<size_t>(c));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(a[i] << 16);
-                v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-            }
+            v.a = load16(in + 16 * static_cast<size_t>(c));
         }
+        return v;
+    };
+    auto value = [](const Chunk& v, int i) {
+        if constexpr (FP32) return __uint_as_float(i < 4 ? v.a[i] : v.b[i - 4]);
+        else return __uint_as_float((i & 1) ? v.a[i / 2] & 0xFFFF0000u : v.a[i / 2] << 16);
     };
     // magnitudes as integers keep their order, and a NaN comes out above an infinity
     uint32_t top = 0;
-    for (int c = tid; c < chunks; c += NT) {
-        float v[8];
-        load8(c, v);
+    auto reduce = [&](const Chunk& v) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(value(v, i)) & 0x7FFFFFFFu);
+    };
+    Chunk held[HELD > 0 ? HELD : 1];
+    if constexpr (HELD > 0) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) held[i] = tid + i * NT < chunks ? load(tid + i * NT) : Chunk{};
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) reduce(held[i]);
+    } else {
+        for (int c = tid; c < chunks; c += NT) reduce(load(c));
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off, 64)));
     if constexpr (WAVES > 1) {
-        if ((tid & 63) == 0) red[tid >> 6] = __uint_as_float(top);
+        if ((tid & 63) == 0) red[tid >> 6] = top;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i) top = max(top, __float_as_uint(red[i]));
+        for (int i = 0; i < WAVES; ++i) top = max(top, red[i]);
     }
     float inverse, scale;
     w8_row_scale(__uint_as_float(top), inverse, scale);
     if (tid == 0) scales[row] = scale;
-    for (int c = tid; c < chunks; c += NT) {
-        float v[8];
-        load8(c, v);
+    auto store = [&](int c, const Chunk& v) {
         uint32_t lo = 0, hi = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            lo |= w8_code(v[i], inverse) << (8 * i);
-            hi |= w8_code(v[4 + i], inverse) << (8 * i);
+            lo |= w8_code(value(v, i), inverse) << (8 * i);
+            hi |= w8_code(value(v, 4 + i), inverse) << (8 * i);
         }
         *reinterpret_cast<uint2*>(codes + row * K + 8 * static_cast<int64_t>(c)) = make_uint2(lo, hi);
+    };
+    if constexpr (HELD > 0) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            if (tid + i * NT < chunks) store(tid + i * NT, held[i]);
+    } else {
+        for (int c = tid; c < chunks; c += NT) store(c, load(c));
     }
 }
 
@@ -98,12 +114,20 @@ __global__ __launch_bounds__(256) void w8_sum_kernel(const int* __restrict__ ws,
 
 hipError_t launch_w8_quantize(const void* x, bool x_fp32, int8_t* codes, float* scales, int64_t R, int K,
                               hipStream_t stream) {
-    const dim3 grid(static_cast<uint32_t>(R));
-    if (x_fp32)
-        hipLaunchKernelGGL((w8_quantize_kernel<true, 4>), grid, dim3(256), 0, stream, x, codes, scales, K);
-    else
-        hipLaunchKernelGGL((w8_quantize_kernel<false, 4>), grid, dim3(256), 0, stream, x, codes, scales, K);
-    return hipGetLastError();
+    // a wave per row up to 4096 values, a workgroup beyond
+    auto form = [&](auto tc) {
+        constexpr bool FP32 = decltype(tc)::value;
+        auto run = [&](auto kernel, int rows) {
+            hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>((R + rows - 1) / rows)), dim3(256), 0, stream, x, codes, scales, R, K);
+            return hipGetLastError();
+        };
+        if (K <= 1024) return run(w8_quantize_kernel<FP32, 1, 2>, 4);
+        if (K <= 2560) return run(w8_quantize_kernel<FP32, 1, 5>, 4);
+        if (K <= 4096) return run(w8_quantize_kernel<FP32, 1, 8>, 4);
+        if (K <= 10240) return run(w8_quantize_kernel<FP32, 4, 5>, 1);
+        return run(w8_quantize_kernel<FP32, 4, 0>, 1);
+    };
+    return x_fp32 ? form(std::true_type{}) : form(std::false_type{});
 }
 
 hipError_t launch_w8_sum(const int* ws, const float* a_scales, const float* w_scales, uint16_t* y, int64_t M, int N,

@@ -26,60 +26,43 @@
 namespace w4a16 {
 namespace {
 
-template <W8Epilogue EPI, bool EXPERTS, int BM, int BN, int WR, int WC, int STAGES>
-__global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs p, int tiles_m, int tiles_n) {
-    constexpr int NW = WR * WC;
-    constexpr int MI = BM / WR / 32, NI = BN / WC / 32;      // 32 x 32 blocks of a wave
-    constexpr bool kPair = EPI != W8Epilogue::kStore;
-    static_assert(NW % 2 == 0 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "direct loads: whole rows, one chunk order");
-    static_assert(!kPair || NI % 2 == 0, "both weight sets of an element in one wave");
-    constexpr int BC = kPair ? BN / 2 : BN;                  // output columns of the tile
+// What a workgroup works on: rows [m0, m_end) of the expert's (BM of them at most), columns from c0, slice z.
+struct Place {
+    int expert, m0, m_end, c0, z;
+};
+// Two to four stages of the left operand's and the weights' rows.  One object per stage, so that a direct load into
+// one is not taken for an input of reads of the others.
+struct Stages {
+    uint8_t *a0, *a1, *a2, *a3, *b0, *b1, *b2, *b3;
+};
 
-    // one object per stage, so that a direct load into one is not taken for an input of reads of the others
+// One tile of 32 MI WR rows and 32 NI WC rows of weights.
+template <W8Epilogue EPI, bool EXPERTS, int MI, int NI, int WR, int WC, int STAGES>
+__device__ __forceinline__ void w8_tile(const W8TileArgs& p, const Stages& lds, const Place& place) {
+    constexpr int NW = WR * WC, BM = 32 * MI * WR, BN = 32 * NI * WC;
+    constexpr bool kPair = EPI != W8Epilogue::kStore;
+    static_assert(NW % 2 == 0 && BN % (8 * NW) == 0, "direct loads: whole rows, one chunk order");
+    static_assert(!kPair || NI % 2 == 0, "both weight sets of an element in one wave");
     static_assert(STAGES >= 2 && STAGES <= 4, "stages");
-    __shared__ __attribute__((aligned(16))) uint8_t a0[BM * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t a1[BM * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t a2[STAGES > 2 ? BM * 128 : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t a3[STAGES > 3 ? BM * 128 : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t b0[BN * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t b1[BN * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t b2[STAGES > 2 ? BN * 128 : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t b3[STAGES > 3 ? BN * 128 : 16];
     auto a_stage = [&](auto ic) -> uint8_t* {
         constexpr int i = decltype(ic)::value % STAGES;
-        if constexpr (i == 0) return a0;
-        else if constexpr (i == 1) return a1;
-        else if constexpr (i == 2) return a2;
-        else return a3;
+        if constexpr (i == 0) return lds.a0;
+        else if constexpr (i == 1) return lds.a1;
+        else if constexpr (i == 2) return lds.a2;
+        else return lds.a3;
     };
     auto b_stage = [&](auto ic) -> uint8_t* {
         constexpr int i = decltype(ic)::value % STAGES;
-        if constexpr (i == 0) return b0;
-        else if constexpr (i == 1) return b1;
-        else if constexpr (i == 2) return b2;
-        else return b3;
+        if constexpr (i == 0) return lds.b0;
+        else if constexpr (i == 1) return lds.b1;
+        else if constexpr (i == 2) return lds.b2;
+        else return lds.b3;
     };
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave / WC, wc = wave % WC;
-
-    int z = 0, expert = 0, first = 0, m_end = p.R, tm, tn;
-    if constexpr (EXPERTS) {
-        ExpertTile tile;
-        if (!find_expert_tile<kBandM>(p.offsets, p.E, p.R, BM, tiles_n, blockIdx.x, tile)) return;
-        expert = tile.expert;
-        first = tile.first;
-        m_end = tile.end;
-        tm = tile.tm;
-        tn = tile.tn;
-    } else {
-        const int tiles = tiles_m * tiles_n;
-        const int work = xcd_remap(blockIdx.x, tiles * p.split);
-        z = work / tiles;
-        band_order<kBandM>(work - z * tiles, tiles_m, tiles_n, tm, tn);
-    }
-    const int m0 = first + tm * BM, c0 = tn * BC;
+    const int z = place.z, expert = place.expert, m0 = place.m0, m_end = place.m_end, c0 = place.c0;
 
     // The contraction in chunks of 16 codes, and this slice's pipeline steps.
     const int K = p.K, chunks = K / kW8Chunk;
@@ -88,7 +71,8 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs 
     const int t_end = static_cast<int>(static_cast<int64_t>(z + 1) * steps / p.split);
 
     // ---- left operand: direct load i of this wave fills rows 8 (wave + NW i) .. + 7 of a stage
-    constexpr int A_LOADS = BM / (8 * NW), B_LOADS = BN / (8 * NW);
+    // (rows behind the tile's last are read from outside the buffer)
+    constexpr int A_LOADS = (BM + 8 * NW - 1) / (8 * NW), B_LOADS = BN / (8 * NW);
     const int own_chunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
     const bool gather = EXPERTS && p.tokens != nullptr;
     auto source_row = [&](int m) {       // the row of a that output row m takes; -1 for none
@@ -243,7 +227,7 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs 
     constexpr int PITCH = WCOLS * 2 + 16;
     static_assert((NW / 2) * 32 * PITCH <= BN * 128, "the waves' regions fit the weight stages");
     w8_loads_done_barrier<0>();
-    uint8_t* region = ((wave & 1) ? b1 : b0) + (wave >> 1) * (32 * PITCH);
+    uint8_t* region = ((wave & 1) ? lds.b1 : lds.b0) + (wave >> 1) * (32 * PITCH);
     constexpr int PIECES = WCOLS / 8;                        // 16-byte pieces of a row
     auto for_pieces = [&](auto body) {
 #pragma unroll
@@ -276,14 +260,19 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs 
         wave_lds_fence();
     };
     // the scales of this lane's columns (columns past the last read 0) and rows
-    constexpr int BLOCKS = kPair ? NI / 2 : NI;
-    const int64_t s_base = static_cast<int64_t>(expert) * p.N + col0;
-    const int64_t s_bytes = 4 * (static_cast<int64_t>(p.N) - col0);
-    const __amdgpu_buffer_rsrc_t sr0 = mx_resource(p.w_scales[0] + s_base, s_bytes);
-    const __amdgpu_buffer_rsrc_t sr1 = kPair ? mx_resource(p.w_scales[1] + s_base, s_bytes) : sr0;
-    auto column_scale = [&](const __amdgpu_buffer_rsrc_t& r, int j, int q, int e) {
-        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, 4u * (32 * j + 8 * q + 4 * half + e), 0, 0));
-    };
+    constexpr int BLOCKS = kPair ? NI / 2 : NI, SETS = kPair ? 2 : 1;
+    float column_scale[SETS][BLOCKS][16];
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) {
+        const __amdgpu_buffer_rsrc_t r = mx_resource(p.w_scales[s] + static_cast<int64_t>(expert) * p.N + col0,
+                                                     4 * (static_cast<int64_t>(p.N) - col0));
+#pragma unroll
+        for (int j = 0; j < BLOCKS; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                column_scale[s][j][e] = __uint_as_float(
+                    __builtin_amdgcn_raw_buffer_load_b32(r, 4u * (32 * j + 8 * (e >> 2) + 4 * half + (e & 3)), 0, 0));
+    }
     float row_scale[MI];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -300,7 +289,7 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs 
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        v[e] = static_cast<float>(acc[i][j][4 * q + e]) * column_scale(sr0, j, q, e) * row_scale[i];
+                        v[e] = static_cast<float>(acc[i][j][4 * q + e]) * column_scale[0][j][4 * q + e] * row_scale[i];
                     put(j, q, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
                 }
             flush(p.y[0], i, p.N);
@@ -340,7 +329,7 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs 
                     float v[4], w[4], sv[4], sw[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float gs = column_scale(sr0, j, q, e), us = column_scale(sr1, j, q, e);
+                        const float gs = column_scale[0][j][4 * q + e], us = column_scale[SETS - 1][j][4 * q + e];
                         const float g = static_cast<float>(acc[i][2 * j][4 * q + e]) * gs * row_scale[i];
                         const float u = static_cast<float>(acc[i][2 * j + 1][4 * q + e]) * us * row_scale[i];
                         const float s = mx_sigmoid(g);
@@ -381,40 +370,122 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs 
     }
 }
 
+// The tile's height by the rows that are there: of a shorter one less is loaded and multiplied.
+template <W8Epilogue EPI, bool EXPERTS, int MI, int NI, int WR, int WC, int STAGES>
+__device__ __forceinline__ void w8_tile_of_height(const W8TileArgs& p, const Stages& lds, const Place& place) {
+    constexpr int LESS = MI - 1;
+    if constexpr (LESS > 0) {
+        if (place.m_end - place.m0 <= 32 * LESS * WR) {
+            w8_tile_of_height<EPI, EXPERTS, LESS, NI, WR, WC, STAGES>(p, lds, place);
+            return;
+        }
+    }
+    w8_tile<EPI, EXPERTS, MI, NI, WR, WC, STAGES>(p, lds, place);
+}
+
+template <W8Epilogue EPI, bool EXPERTS, int MI, int NI, int WR, int WC, int STAGES>
+__global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs p, int height, int tiles_m, int tiles_n,
+                                                               int whole, int cut) {
+    constexpr int BN = 32 * NI * WC, BC = EPI != W8Epilogue::kStore ? BN / 2 : BN;
+    constexpr int ROWS = (32 * MI * WR + 8 * WR * WC - 1) / (8 * WR * WC) * (8 * WR * WC);    // whole loads of all waves
+    __shared__ __attribute__((aligned(16))) uint8_t a0[ROWS * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t a1[ROWS * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t a2[STAGES > 2 ? ROWS * 128 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t a3[STAGES > 3 ? ROWS * 128 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t b0[BN * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t b1[BN * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t b2[STAGES > 2 ? BN * 128 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t b3[STAGES > 3 ? BN * 128 : 16];
+    const Stages lds{a0, a1, a2, a3, b0, b1, b2, b3};
+    Place place{0, 0, 0, 0, 0};
+    if constexpr (EXPERTS) {
+        ExpertTile tile;
+        if (!find_expert_tile<kBandM>(p.offsets, p.E, p.R, height, tiles_n, p.cus, blockIdx.x, tile)) return;
+        place.expert = tile.expert;
+        const int rows = (height + tile.cut - 1) / tile.cut, m = tile.first + tile.tm * height;
+        place.m0 = m + tile.piece * rows;
+        place.m_end = min(min(tile.end, m + height), place.m0 + rows);
+        if (place.m0 >= place.m_end) return;
+        place.c0 = tile.tn * BC;
+    } else {
+        // the first `whole` workgroups take whole tiles, the others tiles cut into `cut` pieces of rows
+        const int tiles = tiles_m * tiles_n;
+        int work = blockIdx.x, piece = 0;
+        if (work < whole) {
+            work = xcd_remap(work, whole);
+        } else {
+            const int rest = xcd_remap(work - whole, gridDim.x - whole);
+            work = whole + rest / cut;
+            piece = rest % cut;
+        }
+        place.z = work / tiles;
+        int tm, tn;
+        band_order<kBandM>(work - place.z * tiles, tiles_m, tiles_n, tm, tn);
+        const int rows = blockIdx.x < static_cast<unsigned>(whole) ? height : (height + cut - 1) / cut;
+        place.m0 = tm * height + piece * rows;
+        place.m_end = min(min(p.R, (tm + 1) * height), place.m0 + rows);
+        place.c0 = tn * BC;
+        if (place.m0 >= place.m_end) return;
+    }
+    w8_tile_of_height<EPI, EXPERTS, MI, NI, WR, WC, STAGES>(p, lds, place);
+}
+
 }  // namespace
 
-const W8TileShape kW8Tiles[kNumW8Tiles] = {{128, 128, 4}, {256, 256, 8}, {64, 128, 4}, {128, 256, 8}, {32, 256, 4}, {64, 256, 8}};
+const W8TileShape kW8Tiles[kNumW8Tiles] = {{128, 128, 4}, {256, 256, 8}, {64, 128, 4}, {128, 256, 8}, {32, 256, 4}, {64, 256, 8}, {256, 256, 8}, {32, 128, 2}, {32, 128, 2}};
 
 namespace {
 
-template <int BM, int BN, int WR, int WC, int STAGES>
+template <int MI, int NI, int WR, int WC, int STAGES>
 hipError_t launch_shape(W8Epilogue epi, const W8TileArgs& args, hipStream_t stream) {
+    constexpr int BN = 32 * NI * WC;
+    const int BM = args.height > 0 ? std::min(args.height, 32 * MI * WR) : 32 * MI * WR;
     const int bc = epi == W8Epilogue::kStore ? BN : BN / 2;
     const int tiles_n = (args.N + bc - 1) / bc;
     // with experts every one of them may end inside a tile, but none has a tile without a row
     const int tiles_m = args.offsets ? static_cast<int>(std::min<int64_t>(args.R, args.R / BM + args.E)) : (args.R + BM - 1) / BM;
-    const dim3 grid(static_cast<uint32_t>(tiles_m) * tiles_n * args.split), block(64 * WR * WC);
+    const int tiles = tiles_m * tiles_n * args.split, cut = std::max(args.cut, 1);
+    // (experts: the kernel cuts, into at most 192 pieces more than tiles)
+    const int whole = cut > 1 ? tiles / args.cus * args.cus : tiles;
+    const int more = args.offsets && args.cus > 0 ? 3 * args.cus / 4 : (tiles - whole) * (cut - 1);
+    const dim3 grid(static_cast<uint32_t>(tiles + more)), block(64 * WR * WC);
     auto run = [&](auto kernel) {
-        W4A16_LAUNCH(kernel, grid, block, 0, stream, args, tiles_m, tiles_n);
+        W4A16_LAUNCH(kernel, grid, block, 0, stream, args, BM, tiles_m, tiles_n, whole, cut);
         return hipGetLastError();
     };
     using E = W8Epilogue;
-    if (!args.offsets) return run(w8_tile_kernel<E::kStore, false, BM, BN, WR, WC, STAGES>);
-    if (epi == E::kGlu) return run(w8_tile_kernel<E::kGlu, true, BM, BN, WR, WC, STAGES>);
-    if (epi == E::kGluGrad) return run(w8_tile_kernel<E::kGluGrad, true, BM, BN, WR, WC, STAGES>);
-    return run(w8_tile_kernel<E::kStore, true, BM, BN, WR, WC, STAGES>);
+    if (!args.offsets) return run(w8_tile_kernel<E::kStore, false, MI, NI, WR, WC, STAGES>);
+    if (epi == E::kGlu) return run(w8_tile_kernel<E::kGlu, true, MI, NI, WR, WC, STAGES>);
+    if (epi == E::kGluGrad) return run(w8_tile_kernel<E::kGluGrad, true, MI, NI, WR, WC, STAGES>);
+    return run(w8_tile_kernel<E::kStore, true, MI, NI, WR, WC, STAGES>);
+}
+
+template <int MI, int NI, int WR, int WC, int STAGES>
+hipError_t launch_shape1(W8Epilogue epi, const W8TileArgs& args, hipStream_t stream) {
+    constexpr int BN = 32 * NI * WC;
+    const int BM = args.height > 0 ? std::min(args.height, 32 * MI * WR) : 32 * MI * WR;
+    const int tiles_n = (args.N + BN - 1) / BN;
+    const int tiles_m = (args.R + BM - 1) / BM;
+    const int tiles = tiles_m * tiles_n * args.split;
+    const int whole = args.cut > 1 ? tiles / args.cus * args.cus : tiles;
+    const dim3 grid(static_cast<uint32_t>(whole + (tiles - whole) * std::max(args.cut, 1))), block(64 * WR * WC);
+    W4A16_LAUNCH((w8_tile_kernel<W8Epilogue::kStore, false, MI, NI, WR, WC, STAGES>), grid, block, 0, stream, args, BM, tiles_m, tiles_n, whole, std::max(args.cut, 1));
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_w8_tile(W8Epilogue epi, int tile, const W8TileArgs& args, hipStream_t stream) {
     switch (tile) {
-        case 0: return launch_shape<128, 128, 2, 2, 2>(epi, args, stream);
-        case 1: return launch_shape<256, 256, 2, 4, 2>(epi, args, stream);
-        case 2: return launch_shape<64, 128, 2, 2, 4>(epi, args, stream);
-        case 3: return launch_shape<128, 256, 2, 4, 3>(epi, args, stream);
-        case 4: return launch_shape<32, 256, 1, 4, 4>(epi, args, stream);
-        case 5: return launch_shape<64, 256, 2, 4, 3>(epi, args, stream);
+        case 0: return launch_shape<2, 2, 2, 2, 2>(epi, args, stream);      // 128 x 128, 4 waves
+        case 1: return launch_shape<4, 2, 2, 4, 2>(epi, args, stream);      // 256 x 256, 8 waves
+        case 2: return launch_shape<1, 2, 2, 2, 4>(epi, args, stream);      // 64 x 128, 4 waves
+        case 3: return launch_shape<2, 2, 2, 4, 3>(epi, args, stream);      // 128 x 256, 8 waves
+        case 4: return launch_shape<1, 2, 1, 4, 4>(epi, args, stream);      // 32 x 256, 4 waves
+        case 5: return launch_shape<1, 2, 2, 4, 3>(epi, args, stream);      // 64 x 256, 8 waves
+        case 7: return launch_shape<1, 2, 1, 2, 4>(epi, args, stream);      // 32 x 128, 2 waves
+        case 8: return launch_shape<1, 2, 1, 2, 3>(epi, args, stream);
+        case 6: return args.offsets || epi != W8Epilogue::kStore ? hipErrorInvalidValue : launch_shape1<8, 1, 1, 8, 2>(epi, args, stream);
         default: return hipErrorInvalidValue;
     }
 }
