@@ -116,7 +116,8 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t token, int 
     }
 }
 
-// One token by sixteen lanes: lane j < top_k <= 16 gets the j-th chosen expert (-1 for none) and its weight.
+// One token by sixteen lanes: lane j < top_k <= 16 gets the j-th chosen expert (-1 for none) and its weight.  Of a bf16
+// logit the key has 16 bits, and the expert's number fits below it: one number decides, and is met once.
 template <int PER, bool WIDE, bool FP32>
 __device__ __forceinline__ void select16(const RouteArgs& p, int64_t token, int lane16, int& expert, float& weight) {
     uint32_t key[PER];
@@ -128,8 +129,11 @@ __device__ __forceinline__ void select16(const RouteArgs& p, int64_t token, int 
         for (int i = 0; i < PER; ++i) {
             nan |= v[i] != v[i];
             key[i] = order_key(v[i]);
+            if (!FP32 && key[i] != 0)      // (of the smallest keys the low bits are ones)
+                key[i] = (key[i] & 0xFFFF0000u) | (0xFFFFu - static_cast<uint32_t>(expert_of<PER, WIDE>(lane16, i)));
         }
     }
+    auto value_of = [](uint32_t k) { return FP32 ? key_value(k) : key_value((k >> 31) ? k & 0xFFFF0000u : k | 0xFFFFu); };
     auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
     expert = -1;
     float chosen = 0.f, top = 0.f, sum = 0.f;
@@ -138,26 +142,29 @@ __device__ __forceinline__ void select16(const RouteArgs& p, int64_t token, int 
 #pragma unroll
         for (int i = 0; i < PER; ++i) best = max(best, key[i]);
         best = row_reduce(best, larger);
-        // of equal ones the lowest expert
-        uint32_t at = 0xFFFFu;
+        uint32_t at = 0xFFFFu - (best & 0xFFFFu);
+        if constexpr (FP32) {
+            // of equal ones the lowest expert
+            at = 0xFFFFu;
 #pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-            if (key[i] == best) at = expert_of<PER, WIDE>(lane16, i);
-        at = row_reduce(at, [](uint32_t a, uint32_t b) { return min(a, b); });
+            for (int i = PER - 1; i >= 0; --i)
+                if (key[i] == best) at = expert_of<PER, WIDE>(lane16, i);
+            at = row_reduce(at, [](uint32_t a, uint32_t b) { return min(a, b); });
+        }
         if (j == 0) {
-            top = key_value(best);
+            top = value_of(best);
             if (!p.renormalize) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) sum += key[i] ? expf(key_value(key[i]) - top) : 0.f;
+                for (int i = 0; i < PER; ++i) sum += key[i] ? expf(value_of(key[i]) - top) : 0.f;
             }
         }
         if (lane16 == j && best != 0) {
             expert = at;
-            chosen = key_value(best);
+            chosen = value_of(best);
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (expert_of<PER, WIDE>(lane16, i) == static_cast<int>(at)) key[i] = 0;
+            if (FP32 ? expert_of<PER, WIDE>(lane16, i) == static_cast<int>(at) : key[i] == best) key[i] = 0;
     }
     const float mine = expert >= 0 ? expf(chosen - top) : 0.f;
     sum = row_sum(p.renormalize ? mine : sum);
@@ -315,32 +322,38 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_select_kernel(const Ro
         p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = __popcll(mask[e]);
 }
 
-// Sixteen experts a workgroup, 64 runs of blocks each.
+// Sixteen experts a workgroup (neighbours in a line of counts), 64 runs of blocks each; a wave sums up an expert's runs.
 constexpr int kScanExperts = 16, kScanRuns = 64;
 __global__ __launch_bounds__(kScanExperts * kScanRuns) void route_scan_kernel(const RouteArgs p) {
     __shared__ int sums[kScanRuns][kScanExperts + 1];
-    const int x = threadIdx.x % kScanExperts, run = threadIdx.x / kScanExperts;
-    const int e = blockIdx.x * kScanExperts + x;
+    const int x = threadIdx.x % kScanExperts, run = threadIdx.x / kScanExperts, e = blockIdx.x * kScanExperts + x;
     const int per = (p.blocks + kScanRuns - 1) / kScanRuns;
-    const int begin = min(run * per, p.blocks), end = min(begin + per, p.blocks);
-    int sum = 0;
-    if (e < p.E)
-        for (int b = begin; b < end; ++b) sum += p.counts[static_cast<int64_t>(b) * p.E + e];
-    sums[run][x] = sum;
+    const int begin = min(run * per, p.blocks), end = e < p.E ? min(begin + per, p.blocks) : begin;
+    int* counts = p.counts + e;
+    int mine = 0;
+#pragma unroll 8
+    for (int b = begin; b < end; ++b) mine += counts[static_cast<int64_t>(b) * p.E];
+    sums[run][x] = mine;
     __syncthreads();
-    int before = 0, total = 0;
-    for (int r = 0; r < kScanRuns; ++r) {
-        if (r < run) before += sums[r][x];
-        total += sums[r][x];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int value = sums[lane][wave];
+    int sum = value;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(sum, d, 64);
+        if (lane >= d) sum += v;
     }
-    if (e >= p.E) return;
+    sums[lane][wave] = sum - value;
+    if (lane == 63 && blockIdx.x * kScanExperts + wave < p.E) p.totals[blockIdx.x * kScanExperts + wave] = sum;
+    __syncthreads();
+    int before = sums[run][x];
+#pragma unroll 8
     for (int b = begin; b < end; ++b) {
-        int* at = p.counts + static_cast<int64_t>(b) * p.E + e;
+        int* at = counts + static_cast<int64_t>(b) * p.E;
         const int c = *at;
         *at = before;
         before += c;
     }
-    if (run == 0) p.totals[e] = total;
 }
 
 __global__ __launch_bounds__(64 * kRouteWaves) void route_place_kernel(const RouteArgs p) {
@@ -368,61 +381,75 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_place_kernel(const Rou
         p.tokens[r] = -1;
 }
 
-// Sixteen lanes per token; its chosen experts and their gradients are read by all of them.
+// Sixteen lanes per token.  What belongs to the chosen experts, slot by slot on the lanes, goes to their columns
+// through a row in LDS: the finished gradients where the softmax is over them alone, else those of the weights.
 template <int PER, bool WIDE, bool FP32>
 __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restrict__ logits, const int* __restrict__ experts,
                                                              const float* __restrict__ dweights, void* __restrict__ dlogits,
                                                              int64_t T, int E, int top_k, bool renormalize) {
+    constexpr int PITCH = 16 * PER + 4;
+    __shared__ __attribute__((aligned(16))) float rows[16 * PITCH];
     const int lane16 = threadIdx.x & 15;
     const int64_t token = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-    if (token >= T) return;                                    // (sixteen lanes together)
-    float v[PER], d[PER];
+    float* row = rows + (threadIdx.x >> 4) * PITCH;
+    if (token >= T) return;                                    // (sixteen lanes together, and no barrier follows)
+    float v[PER];
     load_row<PER, WIDE, FP32>(logits, token, E, lane16, v);
-    uint64_t in = 0;                                           // bit i: the softmax is over this lane's i-th
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        d[i] = 0.f;
         nan |= v[i] != v[i];
-        if (!renormalize && v[i] > -__builtin_inff()) in |= 1ull << i;
+        row[expert_of<PER, WIDE>(lane16, i)] = 0.f;
     }
-    for (int j = 0; j < top_k; ++j) {
-        const int e = experts[token * top_k + j];
-        const float dw = dweights[token * top_k + j];
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (expert_of<PER, WIDE>(lane16, i) == e) {
-                d[i] = dw;
-                in |= v[i] > -__builtin_inff() ? 1ull << i : 0ull;
-            }
-    }
+    const bool any_nan = row_reduce(nan, [](uint32_t a, uint32_t b) { return a | b; }) != 0;
+    // this lane's slots: their experts' logits, in rounds of sixteen
+    auto for_slots = [&](auto body) {
+        for (int j = lane16; j < top_k; j += 16) {
+            const int e = experts[token * top_k + j];
+            if (e < 0 || e >= E) continue;
+            const float l = load_logit(logits, FP32, token * E + e);
+            if (l > -__builtin_inff()) body(e, l, dweights[token * top_k + j]);
+        }
+    };
+    wave_lds_fence();
     float top = -__builtin_inff(), sum = 0.f, c = 0.f;
+    if (renormalize) {
+        for_slots([&](int, float l, float) { top = fmaxf(top, l); });
+        top = row_max(top);
+        for_slots([&](int, float l, float) { sum += expf(l - top); });
+        sum = row_sum(sum);
+        for_slots([&](int, float l, float dw) { c += expf(l - top) / sum * dw; });
+        c = row_sum(c);
+        for_slots([&](int e, float l, float dw) { row[e] = expf(l - top) / sum * (dw - c); });
+        wave_lds_fence();
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (in >> i & 1) top = fmaxf(top, v[i]);
-    top = row_max(top);
+        for (int i = 0; i < PER; ++i) v[i] = row[expert_of<PER, WIDE>(lane16, i)];
+    } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        v[i] = in >> i & 1 ? expf(v[i] - top) : 0.f;
-        sum += v[i];
+        for (int i = 0; i < PER; ++i) top = fmaxf(top, v[i]);
+        top = row_max(top);
+        for_slots([&](int e, float, float dw) { row[e] = dw; });
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            v[i] = v[i] > -__builtin_inff() ? expf(v[i] - top) : 0.f;
+            sum += v[i];
+        }
+        sum = row_sum(sum);
+        for_slots([&](int, float l, float dw) { c += expf(l - top) / sum * dw; });
+        c = row_sum(c);
+        wave_lds_fence();
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[i] = v[i] > 0.f ? v[i] / sum * (row[expert_of<PER, WIDE>(lane16, i)] - c) : v[i];
     }
-    sum = row_sum(sum);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        v[i] = in >> i & 1 ? v[i] / sum : 0.f;
-        if (in >> i & 1) c += v[i] * d[i];
-    }
-    c = row_sum(c);
-    nan = row_reduce(nan, [](uint32_t a, uint32_t b) { return a | b; }) != 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) d[i] = nan ? __builtin_nanf("") : in >> i & 1 ? v[i] * (d[i] - c) : 0.f;
+    for (int i = 0; i < PER; ++i) v[i] = any_nan ? __builtin_nanf("") : v[i];
     if constexpr (WIDE) {
         constexpr int WORDS = PER * (FP32 ? 4 : 2) / 4;
         uint32_t* out = static_cast<uint32_t*>(dlogits) + (token * 16 + lane16) * WORDS;
         uint32_t w[WORDS];
 #pragma unroll
         for (int i = 0; i < WORDS; ++i)
-            w[i] = FP32 ? __float_as_uint(d[i * PER / WORDS]) : pack_bf16(d[2 * i % PER], d[(2 * i + 1) % PER]);
+            w[i] = FP32 ? __float_as_uint(v[i * PER / WORDS]) : pack_bf16(v[2 * i % PER], v[(2 * i + 1) % PER]);
         if constexpr (WORDS % 4 == 0) {
 #pragma unroll
             for (int i = 0; i < WORDS; i += 4)
@@ -437,40 +464,41 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
             const int e = expert_of<PER, false>(lane16, i);
             if (e >= E) continue;
             if (FP32)
-                static_cast<float*>(dlogits)[token * E + e] = d[i];
+                static_cast<float*>(dlogits)[token * E + e] = v[i];
             else
-                static_cast<uint16_t*>(dlogits)[token * E + e] = f32_to_bf16_bits(d[i]);
+                static_cast<uint16_t*>(dlogits)[token * E + e] = f32_to_bf16_bits(v[i]);
         }
     }
 }
 
 // Eight columns a thread, in fp32, the experts in their order.  WIDE: rows of whole 16 bytes.
-template <bool WIDE>
+template <bool WIDE, int HELD>
 __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict__ y, const int* __restrict__ positions,
                                                       const float* __restrict__ weights, uint16_t* __restrict__ out,
                                                       int64_t T, int top_k, int64_t R, int N, int pieces) {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    // (neighbouring tokens on one XCD: their experts' rows are neighbours too)
+    const int64_t at = static_cast<int64_t>(xcd_remap(blockIdx.x, gridDim.x)) * 256 + threadIdx.x;
     const int64_t token = at / pieces;
     const int n = 8 * static_cast<int>(at - token * pieces);
     if (token >= T) return;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    // four rows on their way at a time
-    for (int j0 = 0; j0 < top_k; j0 += 4) {
-        int64_t row[4];
-        float w[4];
+    // HELD rows on their way at a time
+    for (int j0 = 0; j0 < top_k; j0 += HELD) {
+        int64_t row[HELD];
+        float w[HELD];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < HELD; ++j) {
             const int64_t slot = token * top_k + min(j0 + j, top_k - 1);
             row[j] = positions[slot];
             w[j] = weights ? weights[slot] : 1.f;
             if (j0 + j >= top_k || row[j] >= R) row[j] = -1;
         }
         if constexpr (WIDE) {
-            u32x4_t v[4];
+            u32x4_t v[HELD];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = row[j] < 0 ? u32x4_t{0, 0, 0, 0} : load16(y + row[j] * N + n);
+            for (int j = 0; j < HELD; ++j) v[j] = row[j] < 0 ? u32x4_t{0, 0, 0, 0} : load16(y + row[j] * N + n);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < HELD; ++j) {
                 if (row[j] < 0) continue;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -480,7 +508,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < HELD; ++j) {
                 if (row[j] < 0) continue;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -508,7 +536,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const uint16_t* _
                                                                float* __restrict__ dweights, int64_t slots, int top_k,
                                                                int64_t R, int N) {
     const int lane = threadIdx.x & 63;
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int64_t slot = static_cast<int64_t>(xcd_remap(blockIdx.x, gridDim.x)) * 4 + (threadIdx.x >> 6);
     if (slot >= slots) return;
     const int64_t row = positions[slot], token = slot / top_k;
     if (row < 0 || row >= R) {
@@ -615,10 +643,13 @@ hipError_t launch_experts_combine(const uint16_t* y, const int* positions, const
     const int pieces = (N + 7) / 8;
     const dim3 grid(static_cast<uint32_t>((T * pieces + 255) / 256)), threads(256);
     const bool wide = N % 8 == 0 && ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-    if (wide)
-        hipLaunchKernelGGL(combine_kernel<true>, grid, threads, 0, stream, y, positions, weights, out, T, top_k, R, N, pieces);
-    else
-        hipLaunchKernelGGL(combine_kernel<false>, grid, threads, 0, stream, y, positions, weights, out, T, top_k, R, N, pieces);
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, threads, 0, stream, y, positions, weights, out, T, top_k, R, N, pieces);
+    };
+    if (!wide) run(combine_kernel<false, 4>);
+    else if (top_k <= 2) run(combine_kernel<true, 2>);
+    else if (top_k <= 4) run(combine_kernel<true, 4>);
+    else run(combine_kernel<true, 8>);
     return hipGetLastError();
 }
 

@@ -60,46 +60,54 @@ uint64_t gradient_bytes(int32_t op, const Sizes& d) {
 struct Product {
     bool decode, quantize;   // the decode kernel; activations quantized in it
     W8QmvShape qmv;
-    int tile;
-    int split;
+    int tile, height, split, cut;
     int64_t M, N;            // output rows and columns
-    int64_t tiles;           // workgroups of the unsplit launch
+    int64_t blocks;          // workgroups of the launch, at most
+    int cus;
 };
 
-// Microseconds of one tile on a compute unit: `fixed` for the first loads and the epilogue, and `step` per
-// pipeline step, alone on its compute unit and (for the tiles of which two fit) with a second one beside it.
+// Microseconds of one tile: `fixed` for the first loads and the epilogue, and per pipeline step `base` and `grain` for
+// every grain of its rows, alone on its compute unit; `beside` times that with a second one beside it (0: only one fits).
+// Fitted to sweeps of every tile, height, split and cut on MI355X.
 struct TileCost {
-    double fixed, step, step_beside;
+    double fixed, base, grain, beside;
 };
-constexpr TileCost kTileCost[kNumW8Tiles] = {
-    // 128 x 128       256 x 256      64 x 128       128 x 256      32 x 256       64 x 256
-    {3.0, 0.60, 1.0}, {8.0, 1.20, 0}, {4.5, 0.41, 0}, {5.0, 0.80, 0}, {4.5, 0.50, 0}, {5.0, 0.60, 0}, {1000, 1000, 0}, {1000, 1000, 0}, {1000, 1000, 0}};
-constexpr TileCost kColumnCost[kNumW8ColumnTiles] = {
-    // 64 x 128          128 x 256       192 x 256
-    {5.0, 0.54, 0.9}, {5.0, 0.90, 0}, {6.0, 1.35, 0}, {1000,1000,0},{1000,1000,0},{1000,1000,0}};
-// A split's second launch, and its partials written and read per output (8 bytes at about 4 TB/s).
-constexpr double kSplitCost = 3.5, kPartialCost = 2e-6;
+constexpr TileCost kTileCost[kNumW8Tiles] = {   // steps of 128 values
+    // 128 x 128          256 x 256             64 x 128            128 x 256             64 x 256
+    {5, 0.20, 0.13, 2.2}, {10, 0.42, 0.21, 0}, {4, 0.08, 0.17, 2}, {6, 0.36, 0.20, 0}, {5, 0.24, 0.20, 0}};
+constexpr TileCost kColumnCost[kNumW8ColumnTiles] = {   // steps of 64 values
+    // 64 x 128         128 x 256             256 x 256
+    {5, 0.25, 0.2, 2}, {6, 0.80, 0.02, 0}, {7, 0.75, 0.15, 0}};
+// The gated pair's gradients: four outputs in place of one.
+constexpr double kGradCost = 12;
+// The transposed product of codes alone decodes faster.
+constexpr double kUnscaled = 0.85;
+// A split's second launch, and its partials per output.
+constexpr double kSplitCost = 3.5, kPartialCost = 1.3e-6, kColumnPartialCost = 2.0e-6;
 constexpr int64_t kMaxSplit = 8;
+constexpr double kReadRate = 5.0e6;       // bytes of weights a microsecond
 
-// Tiles of R rows in E pieces: half a tile more for each piece is what random ends leave over.
-double row_tiles(const Sizes& d, bool experts, int bm) {
-    if (!experts) return static_cast<double>(ceil_div(d.R, bm));
-    const double pieces = static_cast<double>(std::min(d.E, d.R));
-    return std::max(pieces, static_cast<double>(d.R) / bm + 0.5 * pieces);
+// Row tiles of a launch, as the launchers have it.
+int64_t row_blocks(const Sizes& d, bool experts, int height) {
+    return experts ? std::min(d.R, d.R / height + d.E) : ceil_div(d.R, height);
 }
 
-// Workgroups of rows of a launch, as the launchers have it.
-int64_t row_blocks(const Sizes& d, bool experts, int bm) {
-    return experts ? std::min(d.R, d.R / bm + d.E) : ceil_div(d.R, bm);
+// Launches that share a tile's outputs among two kinds: whole rounds over the compute units, and the rest.
+double rounds_time(double tiles, int64_t cus, const TileCost& c, double alone, double beside) {
+    if (c.beside == 0) return std::ceil(tiles / static_cast<double>(cus)) * alone;
+    const double slots = 2.0 * static_cast<double>(cus), whole = std::floor(tiles / slots), rest = tiles - whole * slots;
+    return whole * beside + (rest == 0 ? 0 : rest <= static_cast<double>(cus) ? alone : beside);
 }
 
-// The decode kernel serves up to 16 rows of one matrix.
+// The decode kernel serves up to 16 rows of one matrix; above, and for experts, the tile, its height, the split and the
+// pieces with the lowest modelled time.
 Product product_of(int32_t op, const Sizes& d, int32_t split_k, int64_t cus, bool last) {
     Product p{};
-    const bool experts = has_experts(op), back = is_backward(op) && last;
+    const bool experts = has_experts(op), back = is_backward(op) && last, grad = is_backward(op) && !last;
     p.M = d.R;
     p.N = back ? d.K : d.N;
-    p.split = 1;
+    p.split = p.cut = 1;
+    p.cus = static_cast<int>(cus);
     const int sets = is_gated(op) ? 2 : 1;
     if (!is_backward(op) && !experts && split_k == 0 && d.R <= kW8QmvRows) {
         // Waves: eight short shares where few workgroups have to bring everything on its way, fewer where there are many
@@ -112,34 +120,71 @@ Product product_of(int32_t op, const Sizes& d, int32_t split_k, int64_t cus, boo
         p.decode = true;
         p.quantize = op == W8A8_LINEAR && rows * d.K <= 16384 && w8_qmv_shape(rows, std::max(waves, (K + 2047) / 2048), K, true, &p.qmv);
         if (!p.quantize) w8_qmv_shape(rows, waves, K, false, &p.qmv);
-        p.tiles = ceil_div(p.N, kW8QmvColumns);
-        if (p.tiles * 64 * kW8QmvWaves < kMaxThreads) return p;
+        p.blocks = blocks;
+        if (p.blocks * 64 * kW8QmvWaves < kMaxThreads) return p;
         p.decode = p.quantize = false;
     }
     const int64_t steps = back ? ceil_div(d.N, kW8ColumnStep) * sets : ceil_div(d.K, kW8Step);
     const int count = back ? kNumW8ColumnTiles : kNumW8Tiles;
-    const double outputs = static_cast<double>(p.M) * p.N;
+    const double outputs = static_cast<double>(p.M) * p.N, pieces = static_cast<double>(std::min(d.E, d.R));
+    const double memory = pieces * static_cast<double>(d.N) * d.K * sets / kReadRate;
     double best = 0;
     Product chosen = p;
     for (p.tile = 0; p.tile < count; ++p.tile) {
         const TileCost& c = back ? kColumnCost[p.tile] : kTileCost[p.tile];
         const W8TileShape& s = back ? kW8ColumnTiles[p.tile] : kW8Tiles[p.tile];
         const int64_t columns = ceil_div(p.N, !back && is_gated(op) ? s.bn / 2 : s.bn);
-        p.tiles = row_blocks(d, experts, s.bm) * columns;
-        const double tiles = row_tiles(d, experts, s.bm) * static_cast<double>(columns);
-        const int64_t most = experts || !last ? 1 : std::min(kMaxSplit, steps);
-        const int64_t first = split_k > 0 && most > 1 ? std::min<int64_t>(split_k, steps) : 1;
-        for (int64_t z = first; z <= (split_k > 0 ? first : most); ++z) {
-            const bool beside = c.step_beside > 0 && tiles * z > cus;
-            const double slots = static_cast<double>(beside ? 2 * cus : cus);
-            const double rounds = std::max(1.0, experts ? tiles / slots + 0.5 : static_cast<double>(ceil_div(static_cast<int64_t>(tiles) * z, static_cast<int64_t>(slots))));
-            double t = rounds * (c.fixed + static_cast<double>(ceil_div(steps, z)) * (beside ? c.step_beside : c.step));
-            if (z > 1) t += kSplitCost + kPartialCost * outputs * static_cast<double>(z);
+        const double fixed = c.fixed + (grad ? kGradCost : 0);
+        auto step = [&](double rows) {
+            return (c.base + c.grain * std::ceil(rows / s.grain)) * (back && sets > 1 ? kUnscaled : 1);
+        };
+        auto consider = [&](double t) {
+            p.blocks = row_blocks(d, experts, p.height) * columns * p.split;
+            if (experts || p.cut > 1) p.blocks += cus;
             if (best == 0 || t < best) {
                 best = t;
                 chosen = p;
-                chosen.split = static_cast<int>(z);
             }
+        };
+        if (experts) {
+            // an expert's rows: whole tiles, and one that ends somewhere
+            p.height = s.bm;
+            p.cut = std::max(1, back ? s.bm / 128 : s.bm / 64);
+            const double mean = static_cast<double>(d.R) / pieces, n = static_cast<double>(steps);
+            const double whole = std::max(0.0, mean / s.bm - 0.5);
+            const double tile = (whole * (fixed + n * step(s.bm)) + fixed + n * step(std::min(mean, 0.5 * s.bm))) / (whole + 1);
+            // (experts differ in how many rows they get, and one round lasts as long as its longest tile)
+            const double longest = fixed + n * step(std::min(1.7 * mean, static_cast<double>(s.bm)));
+            const double tiles = (whole > 0 ? 1.12 : 1) * pieces * static_cast<double>(columns) * (whole + 1), units = static_cast<double>(cus);
+            const double rounds = tiles / (c.beside > 0 ? 2 * units : units), idle = std::ceil(rounds) - rounds;
+            const double work = tile * (c.beside > 0 ? c.beside : 1) * (rounds + (c.beside > 0 ? 0.25 : p.cut > 1 && rounds > 2 ? 0.5 : 0.75) * idle);
+            // (two workgroups a compute unit wait for the weights less; of two forms that wait the one with less work)
+            consider(std::max({tiles <= units ? longest : work, longest, memory * (c.beside > 0 ? 1 : 1.12)}) + 1e-3 * work);
+            continue;
+        }
+        for (p.height = s.bm; p.height > s.bm - 3 * s.grain && p.height > 0; p.height -= s.grain) {
+            const double tiles = static_cast<double>(ceil_div(d.R, p.height) * columns);
+            const double rows = static_cast<double>(std::min<int64_t>(p.height, d.R));
+            const int64_t most = last ? std::min(kMaxSplit, steps) : 1;
+            const int64_t first = split_k > 0 && most > 1 ? std::min<int64_t>(split_k, steps) : 1;
+            for (int64_t z = first; z <= (split_k > 0 ? first : most); ++z) {
+                const double n = static_cast<double>(ceil_div(steps, z));
+                const double alone = fixed + n * step(rows), beside = fixed + n * step(rows) * c.beside;
+                double t = rounds_time(tiles * static_cast<double>(z), cus, c, alone, beside);
+                if (z > 1) t += kSplitCost + (back ? kColumnPartialCost : kPartialCost) * outputs * static_cast<double>(z);
+                p.split = static_cast<int>(z);
+                p.cut = 1;
+                consider(std::max(t, memory));
+                // the last round's tiles in two or four pieces of rows
+                const double round = static_cast<double>(c.beside > 0 ? 2 * cus : cus);
+                const double rest = tiles - std::floor(tiles / static_cast<double>(cus)) * static_cast<double>(cus);
+                for (p.cut = 2; z == 1 && p.cut <= 4 && tiles > static_cast<double>(cus); p.cut *= 2) {
+                    if (rest == 0 || rest * p.cut > round || p.height / p.cut < s.grain) continue;
+                    const double low = fixed + n * step(std::ceil(rows / p.cut)) * (rest * p.cut > static_cast<double>(cus) ? c.beside : 1);
+                    consider(std::max(rounds_time(tiles - rest, cus, c, alone, beside) + low, memory));
+                }
+            }
+            p.split = p.cut = 1;
         }
     }
     return chosen;
@@ -164,7 +209,7 @@ int plan_call(int32_t op, const Sizes& d, int32_t split_k, int32_t num_cus, Prod
     *used_cus = cus;
     *p = product_of(op, d, split_k, cus, true);
     const W8TileShape& s = is_backward(op) ? kW8ColumnTiles[p->tile] : kW8Tiles[p->tile];
-    if (!p->decode && (p->tiles * p->split * 64 * s.waves >= kMaxThreads ||
+    if (!p->decode && (p->blocks * 64 * s.waves >= kMaxThreads ||
                        (p->split > 1 && ceil_div(p->M * p->N, 4) >= kMaxThreads)))
         return W4A16_ERR_SHAPE;
     if (d.T >= kMaxTokens) return W4A16_ERR_SHAPE;             // the quantizer's launch
@@ -223,6 +268,9 @@ W8TileArgs tile_args(const Sizes& d, const Product& p, const int32_t* offsets, c
     a.N = static_cast<int>(d.N);
     a.K = static_cast<int>(d.K);
     a.split = p.split;
+    a.height = p.height;
+    a.cut = p.cut;
+    a.cus = p.cus;
     a.y[0] = y;
     return a;
 }
@@ -264,6 +312,9 @@ int run_columns(const Product& p, W8ColumnsArgs& args, const Sizes& d, void* par
     args.K = static_cast<int>(d.K);
     args.pitch = static_cast<int>(padded(d.N));
     args.split = p.split;
+    args.height = p.height;
+    args.cut = p.cut;
+    args.cus = p.cus;
     args.ws = static_cast<float*>(partials);
     const hipError_t e = launch_w8_columns(p.tile, args, stream);
     if (e != hipSuccess || p.split == 1) return to_status(e);
@@ -384,7 +435,7 @@ int w8a8_plan(int32_t op, int64_t E, int64_t T, int64_t R, int64_t N, int64_t K,
     const bool back = is_backward(op);
     const W8TileShape& s = back ? kW8ColumnTiles[p.tile] : kW8Tiles[p.tile];
     out->path = W4A16_PATH_W8A8;
-    out->tile_m = s.bm;
+    out->tile_m = p.height;
     out->tile_n = !back && is_gated(op) ? s.bn / 2 : s.bn;
     out->tile_k = back ? kW8ColumnStep : kW8Step;
     out->block_threads = 64 * s.waves;
@@ -518,7 +569,7 @@ int w8a8_experts_gate_up_swiglu_backward(const uint16_t* x, const int8_t* codes_
     st = query_num_cus(&cus);
     if (st != W4A16_OK) return st;
     const Product again = product_of(op, d, 0, cus, false);      // both projections once more
-    if (again.tiles * 64 * kW8Tiles[again.tile].waves >= kMaxThreads) return W4A16_ERR_SHAPE;
+    if (again.blocks * 64 * kW8Tiles[again.tile].waves >= kMaxThreads) return W4A16_ERR_SHAPE;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     W8TileArgs args = tile_args(d, again, offsets, tokens, dgate);
     args.w[0] = codes_gate;

@@ -311,7 +311,7 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_columns_kernel(const W8Column
     Place place{0, 0, 0, 0, 0};
     if constexpr (EXPERTS) {
         ExpertTile tile;
-        if (!find_expert_tile<kBandM>(p.offsets, p.E, p.R, height, tiles_n, p.cus, blockIdx.x, tile)) return;
+        if (!find_expert_tile<kBandM>(p.offsets, p.E, p.R, height, tiles_n, p.cus, cut, blockIdx.x, tile)) return;
         place.expert = tile.expert;
         const int rows = (height + tile.cut - 1) / tile.cut, m = tile.first + tile.tm * height;
         place.m0 = m + tile.piece * rows;
@@ -343,7 +343,9 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_columns_kernel(const W8Column
 
 }  // namespace
 
-const W8TileShape kW8ColumnTiles[kNumW8ColumnTiles] = {{64, 128, 4}, {128, 256, 8}, {192, 256, 8}, {256, 256, 8}, {256, 256, 8}, {128, 256, 8}};
+// 64 x 128, two of four waves a compute unit; 128 x 256, whose waves have all rows of 32 columns, four stages; and 256 x
+// 256.  A step costs at least 0.8 us, so lower tiles bring nothing (2048 x 4096 x 2560 in 96 rows 60 us, in 128 61).
+const W8TileShape kW8ColumnTiles[kNumW8ColumnTiles] = {{64, 128, 4, 64}, {128, 256, 8, 32}, {256, 256, 8, 64}};
 
 namespace {
 
@@ -354,9 +356,9 @@ hipError_t launch_shape(const W8ColumnsArgs& args, hipStream_t stream) {
     const int tiles_n = (args.K + BN - 1) / BN;
     const int tiles_m = args.offsets ? static_cast<int>(std::min<int64_t>(args.R, args.R / BM + args.E)) : (args.R + BM - 1) / BM;
     const int tiles = tiles_m * tiles_n * args.split, cut = std::max(args.cut, 1);
-    // (experts: the kernel cuts, into at most 192 pieces more than tiles)
-    const int whole = cut > 1 ? tiles / args.cus * args.cus : tiles;
-    const int more = args.offsets && args.cus > 0 ? 3 * args.cus / 4 : (tiles - whole) * (cut - 1);
+    // (experts: the kernel counts the tiles and cuts, into at most cus pieces)
+    const int whole = cut > 1 && !args.offsets ? tiles / args.cus * args.cus : tiles;
+    const int more = args.offsets ? (cut > 1 ? args.cus : 0) : (tiles - whole) * (cut - 1);
     const dim3 grid(static_cast<uint32_t>(tiles + more)), block(64 * WR * WC);
     auto run = [&](auto kernel) {
         W4A16_LAUNCH(kernel, grid, block, 0, stream, args, BM, tiles_m, tiles_n, whole, cut);
@@ -372,11 +374,8 @@ hipError_t launch_shape(const W8ColumnsArgs& args, hipStream_t stream) {
 hipError_t launch_w8_columns(int tile, const W8ColumnsArgs& args, hipStream_t stream) {
     switch (tile) {
         case 0: return launch_shape<1, 2, 2, 2, 4>(args, stream);
-        case 1: return launch_shape<2, 2, 2, 4, 4>(args, stream);
-        case 2: return launch_shape<3, 2, 2, 4, 2>(args, stream);
-        case 3: return launch_shape<4, 2, 2, 4, 2>(args, stream);
-        case 4: return launch_shape<8, 1, 1, 8, 2>(args, stream);
-        case 5: return launch_shape<4, 1, 1, 8, 4>(args, stream);
+        case 1: return launch_shape<4, 1, 1, 8, 4>(args, stream);
+        case 2: return launch_shape<4, 2, 2, 4, 2>(args, stream);
         default: return hipErrorInvalidValue;
     }
 }

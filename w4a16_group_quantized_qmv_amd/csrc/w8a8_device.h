@@ -57,11 +57,11 @@ struct ExpertTile {
 
 // Tile number `block` of the experts' tiles of BM rows x tiles_n columns of tiles, in an order that gives each XCD
 // whole experts where it can; false where there are fewer tiles.  What is left after whole rounds over `cus`
-// compute units is cut into two or four pieces where all of them run at once (cus 0: never).  Every wave calls
+// compute units is cut into two or four pieces (`most` of them) where all of them run at once.  Every wave calls
 // it, with all lanes; the result is uniform.
 template <int BAND>
 __device__ __forceinline__ bool find_expert_tile(const int* __restrict__ offsets, int E, int R, int BM, int tiles_n,
-                                                 int cus, int block, ExpertTile& out) {
+                                                 int cus, int most, int block, ExpertTile& out) {
     const int lane = threadIdx.x & 63;
     const int per = (E + 63) >> 6;
     auto rows_of = [&](int e, int& first, int& end) {
@@ -85,9 +85,9 @@ __device__ __forceinline__ bool find_expert_tile(const int* __restrict__ offsets
     const int total = static_cast<int>(min(all, static_cast<int64_t>(gridDim.x)));
     int whole = total;
     out.cut = 1;
-    if (cus > 0 && total > cus) {
+    if (most > 1 && total > cus) {
         const int rest = total % cus;
-        out.cut = 4 * rest <= cus ? 4 : 2 * rest <= cus ? 2 : 1;
+        out.cut = most >= 4 && 4 * rest <= cus ? 4 : 2 * rest <= cus ? 2 : 1;
         if (out.cut > 1) whole = total - rest;
     }
     const int items = whole + (total - whole) * out.cut;

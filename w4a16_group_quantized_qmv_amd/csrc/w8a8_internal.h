@@ -40,8 +40,8 @@ struct W8TileArgs {
     int E, T, R, N, K;
     int split;
     int height;                // rows of a tile, at most the shape's; 0: all of those
-    int cut, cus;              // one matrix: what is left of the tiles after whole rounds over `cus` compute units is
-                               // cut into this many pieces of rows
+    int cut, cus;              // what is left of the tiles after whole rounds over `cus` compute units is cut into this
+                               // many pieces of rows; experts: at most, as the kernel finds
 };
 
 // The transposed product: dx[r, k] = sum_s sum_n g_s[r, n] w_scale_s[n] w_s[n, k]; without w_scales the rows of
@@ -60,8 +60,9 @@ struct W8ColumnsArgs {
 
 struct W8TileShape {
     int bm, bn, waves;
+    int grain;                 // rows of a tile count in steps of this
 };
-constexpr int kNumW8Tiles = 9;
+constexpr int kNumW8Tiles = 5;
 extern const W8TileShape kW8Tiles[kNumW8Tiles];
 constexpr int kW8Step = 128;          // values of the contraction in one pipeline step
 hipError_t launch_w8_tile(W8Epilogue epi, int tile, const W8TileArgs& args, hipStream_t stream);
@@ -78,7 +79,7 @@ struct W8QmvShape {
 bool w8_qmv_shape(int rows, int waves, int K, bool quantize, W8QmvShape* out);
 hipError_t launch_w8_qmv(const W8QmvShape& shape, const W8TileArgs& args, hipStream_t stream);
 
-constexpr int kNumW8ColumnTiles = 6;
+constexpr int kNumW8ColumnTiles = 3;
 extern const W8TileShape kW8ColumnTiles[kNumW8ColumnTiles];
 constexpr int kW8ColumnStep = 64;
 hipError_t launch_w8_columns(int tile, const W8ColumnsArgs& args, hipStream_t stream);

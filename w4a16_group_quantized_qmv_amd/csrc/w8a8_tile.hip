@@ -400,7 +400,7 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs 
     Place place{0, 0, 0, 0, 0};
     if constexpr (EXPERTS) {
         ExpertTile tile;
-        if (!find_expert_tile<kBandM>(p.offsets, p.E, p.R, height, tiles_n, p.cus, blockIdx.x, tile)) return;
+        if (!find_expert_tile<kBandM>(p.offsets, p.E, p.R, height, tiles_n, p.cus, cut, blockIdx.x, tile)) return;
         place.expert = tile.expert;
         const int rows = (height + tile.cut - 1) / tile.cut, m = tile.first + tile.tm * height;
         place.m0 = m + tile.piece * rows;
@@ -432,7 +432,14 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs 
 
 }  // namespace
 
-const W8TileShape kW8Tiles[kNumW8Tiles] = {{128, 128, 4}, {256, 256, 8}, {64, 128, 4}, {128, 256, 8}, {32, 256, 4}, {64, 256, 8}, {256, 256, 8}, {32, 128, 2}, {32, 128, 2}};
+// Where they lead (sweeps of every form; one or two workgroups fit a compute unit):
+//   128 x 128  two of four waves a compute unit: middle sizes (2048 x 4096 x 2560 25.8 us; 256 x 256 33)
+//   256 x 256  most operations a byte: large ones (4096 x 9728 x 2560 96 us; 128 x 256 104, 128 x 128 112)
+//    64 x 128  two a compute unit, three stages: few rows (gated halves of 16 tokens, 64 experts, weights from memory 70
+//              us; with four stages and one a compute unit 80, 128 x 128 79)
+//   128 x 256  three stages: between those (512 x 9728 x 2560 20.5 us)
+//    64 x 256  three stages: few rows of many experts (509 tokens' gated halves 83 us; 128 x 128 91, 64 x 128 97)
+const W8TileShape kW8Tiles[kNumW8Tiles] = {{128, 128, 4, 64}, {256, 256, 8, 64}, {64, 128, 4, 64}, {128, 256, 8, 64}, {64, 256, 8, 64}};
 
 namespace {
 
@@ -445,9 +452,9 @@ hipError_t launch_shape(W8Epilogue epi, const W8TileArgs& args, hipStream_t stre
     // with experts every one of them may end inside a tile, but none has a tile without a row
     const int tiles_m = args.offsets ? static_cast<int>(std::min<int64_t>(args.R, args.R / BM + args.E)) : (args.R + BM - 1) / BM;
     const int tiles = tiles_m * tiles_n * args.split, cut = std::max(args.cut, 1);
-    // (experts: the kernel cuts, into at most 192 pieces more than tiles)
-    const int whole = cut > 1 ? tiles / args.cus * args.cus : tiles;
-    const int more = args.offsets && args.cus > 0 ? 3 * args.cus / 4 : (tiles - whole) * (cut - 1);
+    // (experts: the kernel counts the tiles and cuts, into at most cus pieces)
+    const int whole = cut > 1 && !args.offsets ? tiles / args.cus * args.cus : tiles;
+    const int more = args.offsets ? (cut > 1 ? args.cus : 0) : (tiles - whole) * (cut - 1);
     const dim3 grid(static_cast<uint32_t>(tiles + more)), block(64 * WR * WC);
     auto run = [&](auto kernel) {
         W4A16_LAUNCH(kernel, grid, block, 0, stream, args, BM, tiles_m, tiles_n, whole, cut);
@@ -460,32 +467,15 @@ hipError_t launch_shape(W8Epilogue epi, const W8TileArgs& args, hipStream_t stre
     return run(w8_tile_kernel<E::kStore, true, MI, NI, WR, WC, STAGES>);
 }
 
-template <int MI, int NI, int WR, int WC, int STAGES>
-hipError_t launch_shape1(W8Epilogue epi, const W8TileArgs& args, hipStream_t stream) {
-    constexpr int BN = 32 * NI * WC;
-    const int BM = args.height > 0 ? std::min(args.height, 32 * MI * WR) : 32 * MI * WR;
-    const int tiles_n = (args.N + BN - 1) / BN;
-    const int tiles_m = (args.R + BM - 1) / BM;
-    const int tiles = tiles_m * tiles_n * args.split;
-    const int whole = args.cut > 1 ? tiles / args.cus * args.cus : tiles;
-    const dim3 grid(static_cast<uint32_t>(whole + (tiles - whole) * std::max(args.cut, 1))), block(64 * WR * WC);
-    W4A16_LAUNCH((w8_tile_kernel<W8Epilogue::kStore, false, MI, NI, WR, WC, STAGES>), grid, block, 0, stream, args, BM, tiles_m, tiles_n, whole, std::max(args.cut, 1));
-    return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_w8_tile(W8Epilogue epi, int tile, const W8TileArgs& args, hipStream_t stream) {
     switch (tile) {
         case 0: return launch_shape<2, 2, 2, 2, 2>(epi, args, stream);      // 128 x 128, 4 waves
         case 1: return launch_shape<4, 2, 2, 4, 2>(epi, args, stream);      // 256 x 256, 8 waves
-        case 2: return launch_shape<1, 2, 2, 2, 4>(epi, args, stream);      // 64 x 128, 4 waves
+        case 2: return launch_shape<1, 2, 2, 2, 3>(epi, args, stream);      // 64 x 128, 4 waves
         case 3: return launch_shape<2, 2, 2, 4, 3>(epi, args, stream);      // 128 x 256, 8 waves
-        case 4: return launch_shape<1, 2, 1, 4, 4>(epi, args, stream);      // 32 x 256, 4 waves
-        case 5: return launch_shape<1, 2, 2, 4, 3>(epi, args, stream);      // 64 x 256, 8 waves
-        case 7: return launch_shape<1, 2, 1, 2, 4>(epi, args, stream);      // 32 x 128, 2 waves
-        case 8: return launch_shape<1, 2, 1, 2, 3>(epi, args, stream);
-        case 6: return args.offsets || epi != W8Epilogue::kStore ? hipErrorInvalidValue : launch_shape1<8, 1, 1, 8, 2>(epi, args, stream);
+        case 4: return launch_shape<1, 2, 2, 4, 3>(epi, args, stream);      // 64 x 256, 8 waves
         default: return hipErrorInvalidValue;
     }
 }
