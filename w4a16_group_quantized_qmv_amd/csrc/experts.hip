@@ -496,7 +496,9 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
         if constexpr (WIDE) {
             u32x4_t v[HELD];
 #pragma unroll
-            for (int j = 0; j < HELD; ++j) v[j] = row[j] < 0 ? u32x4_t{0, 0, 0, 0} : load16(y + row[j] * N + n);
+            for (int j = 0; j < HELD; ++j)
+                v[j] = row[j] < 0 ? u32x4_t{0, 0, 0, 0}
+                                  : __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(y + row[j] * N + n));
 #pragma unroll
             for (int j = 0; j < HELD; ++j) {
                 if (row[j] < 0) continue;
@@ -549,7 +551,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const uint16_t* _
     float dot = 0.f;
     if constexpr (WIDE) {
         for (int n = 8 * lane; n < N; n += 512) {
-            const u32x4_t a = load16(d + n), b = load16(in + n);
+            const u32x4_t a = load16(d + n), b = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(in + n));
             u32x4_t r;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -557,7 +559,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const uint16_t* _
                 dot += a0 * __uint_as_float(b[i] << 16) + a1 * __uint_as_float(b[i] & 0xFFFF0000u);
                 r[i] = pack_bf16(w * a0, w * a1);
             }
-            *reinterpret_cast<u32x4_t*>(to + n) = r;
+            __builtin_nontemporal_store(r, reinterpret_cast<u32x4_t*>(to + n));
         }
     } else {
         for (int n = lane; n < N; n += 64) {
