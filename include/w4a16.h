@@ -564,7 +564,8 @@ int w8a8_quantize_rows(const void* x, int32_t x_type, int8_t* codes, float* scal
  * Launch plan of a W8A8 operator (enum w8a8_op; E matrices of N rows and K values, T activation rows, R
  * output rows; E = 1 and T = R = M without experts; backward passes report the launch that computes dx).
  * split_k as for qmm_w4a16 (experts: 0 or 1).  workspace_bytes is what the operator's call needs, num_cus as in
- * w4a16_plan.  grid_y is the most that the experts' row counts can need.  Pure host arithmetic.  Returns
+ * w4a16_plan.  grid_y is the most that the experts' row counts can need; variant is the tile, plus 10 where the last
+ * round's tiles are cut into pieces of rows.  Pure host arithmetic.  Returns
  * W4A16_OK, _ERR_NULL, _ERR_SHAPE, _ERR_UNSUPPORTED (an unknown op, experts with a split) or _ERR_DEVICE.
  */
 int w8a8_plan(int32_t op, int64_t E, int64_t T, int64_t R, int64_t N, int64_t K, int32_t split_k, int32_t num_cus,

@@ -102,6 +102,11 @@ def test_every_bf16_value_quantizes_as_the_format_says(lib):
 SHAPES = [(1, 8, 16), (1, 151, 2576), (2, 100, 131056), (4, 2560, 9728), (5, 96, 400), (7, 1000, 4096), (16, 4097, 2560), (17, 33, 48),
           (33, 1000, 416), (64, 128, 2560), (100, 3001, 528), (130, 260, 9728), (509, 640, 2560), (600, 2560, 512), (1100, 2400, 272),
           (2048, 4096, 256)]
+# reach the other tiles, heights, splits and pieces
+FORWARD = [(1000, 4100, 16), (8200, 1000, 16), (3000, 4100, 16), (1000, 4100, 528), (8200, 130, 2576), (8200, 130, 5008),
+           (4100, 4100, 16), (4100, 9001, 272)]
+BACKWARD = [(513, 2056, 5008), (4100, 33, 1040), (3000, 3001, 144), (8200, 33, 528), (4100, 3001, 144), (3000, 33, 2576),
+            (6000, 9001, 16), (8200, 2056, 16), (3000, 33, 5008), (6000, 33, 2576)]
 
 
 def problem(rng, M, N, K):
@@ -110,7 +115,7 @@ def problem(rng, M, N, K):
     return bf16(x), w, host
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + FORWARD)
 def test_linear(lib, M, N, K):
     import torch
     announce(f"w8a8_linear {M}x{N}x{K}")
@@ -142,7 +147,7 @@ def test_split_products_are_the_same(lib, M, N, K, split):
     assert torch.equal(lib.w8a8_linear_backward(dy, *w, split_k=split), dx)
 
 
-@pytest.mark.parametrize("M,N,K", [s for s in SHAPES if s[2] < 131056] + [(1, 1, 16), (3, 20000, 64)])
+@pytest.mark.parametrize("M,N,K", [s for s in SHAPES if s[2] < 131056] + [(1, 1, 16), (3, 20000, 64)] + BACKWARD)
 def test_linear_backward(lib, M, N, K):
     import torch
     announce(f"w8a8_linear_backward {M}x{N}x{K}")
@@ -158,11 +163,17 @@ def test_linear_backward(lib, M, N, K):
 
 
 def test_the_shapes_reach_every_form(lib):
-    forward = [lib.w8a8_plan(lib.W8A8_LINEAR, *s) for s in SHAPES]
-    assert {p["variant"] for p in forward if p["path"] == lib.PATH_W8A8_QMV} == {0, 1}
-    assert any(p["split_k"] > 1 for p in forward) and any(p["path"] == lib.PATH_W8A8 and p["split_k"] == 1 for p in forward)
-    back = [lib.w8a8_plan(lib.W8A8_LINEAR_BACKWARD, *s) for s in SHAPES]
-    assert any(p["split_k"] > 1 for p in back) and any(p["split_k"] == 1 for p in back)
+    def forms(op, shapes):
+        plans = [lib.w8a8_plan(op, *s) for s in shapes]
+        return plans, {(p["variant"], p["tile_m"]) for p in plans if p["path"] == lib.PATH_W8A8}
+
+    plans, forward = forms(lib.W8A8_LINEAR, SHAPES + FORWARD)
+    assert {p["variant"] for p in plans if p["path"] == lib.PATH_W8A8_QMV} == {0, 1}
+    assert {(0, 128), (1, 192), (1, 256), (2, 64), (3, 128), (5, 128), (10, 128), (11, 256)} <= forward
+    assert {2, 3} <= {p["variant"] for p in plans if p["split_k"] > 1 and p["path"] == lib.PATH_W8A8}
+    plans, back = forms(lib.W8A8_LINEAR_BACKWARD, SHAPES + BACKWARD)
+    assert {(0, 64), (1, 64), (1, 96), (1, 128), (2, 192), (2, 256), (12, 256)} <= back
+    assert {p["variant"] for p in plans if p["split_k"] > 1} == {0, 1, 2}
 
 
 def test_integer_cases_are_exact(lib):
@@ -244,7 +255,9 @@ EXPERTS = [(1, 5, 24, 48, 64, "random"), (4, 7, 14, 100, 96, "random"), (8, 200,
            (16, 16, 16, 64, 2560, "random"), (64, 3, 24, 1216, 256, "random"), (70, 40, 90, 50, 80, "gaps"), (5, 900, 900, 72, 528, "one"),
            (6, 1300, 2600, 300, 144, "random"), (1000, 30, 60, 24, 32, "random"), (4, 3000, 6000, 520, 64, "each"),
            (2, 40, 40, 33, 16, "none"), (9, 2, 18, 48, 4112, "each"), (128, 60, 240, 80, 9728, "random"),
-           (5, 3000, 6000, 520, 1040, "random"), (3, 2100, 4200, 1000, 528, "gaps")]
+           (5, 3000, 6000, 520, 1040, "random"), (3, 2100, 4200, 1000, 528, "gaps"), (64, 6000, 12000, 264, 144, "random"),
+           (64, 3000, 6000, 1000, 144, "gaps"), (64, 20, 40, 1000, 144, "random"), (64, 3000, 6000, 130, 80, "random"),
+           (64, 150, 300, 33, 528, "random"), (64, 3000, 6000, 33, 528, "each")]
 
 
 def expert_problem(E, T, R, N, K, kind, gather):
@@ -325,11 +338,12 @@ def test_experts_gate_up(lib, E, T, R, N, K, kind, gather):
 
 
 def test_the_experts_shapes_reach_every_form(lib):
-    plans = {op: [lib.w8a8_plan(getattr(lib, op), T, N, K, 0, 0, E, R) for E, T, R, N, K, _ in EXPERTS] for op in (
-        "W8A8_EXPERTS_LINEAR", "W8A8_EXPERTS_LINEAR_BACKWARD", "W8A8_EXPERTS_GATE_UP", "W8A8_EXPERTS_GATE_UP_BACKWARD")}
-    for op in plans:
-        assert all(p["path"] == lib.PATH_W8A8 for p in plans[op])
-        assert len({p["variant"] for p in plans[op]}) >= 2, op
+    reached = {"W8A8_EXPERTS_LINEAR": {1, 2, 3, 4, 5}, "W8A8_EXPERTS_LINEAR_BACKWARD": {0, 1, 2}, "W8A8_EXPERTS_GATE_UP": {0, 1, 2, 3, 4},
+               "W8A8_EXPERTS_GATE_UP_BACKWARD": {0, 1, 2}}
+    for op, forms in reached.items():
+        plans = [lib.w8a8_plan(getattr(lib, op), T, N, K, 0, 0, E, R) for E, T, R, N, K, _ in EXPERTS]
+        assert all(p["path"] == lib.PATH_W8A8 for p in plans)
+        assert forms <= {p["variant"] for p in plans}, op
 
 
 @pytest.mark.parametrize("R", [12, 600])

@@ -471,13 +471,14 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
     }
 }
 
-// Eight columns a thread, in fp32, the experts in their order.  WIDE: rows of whole 16 bytes.
+// Eight columns a thread, in fp32, the experts in their order.  WIDE: rows of whole 16 bytes.  Bound by memory: rows
+// are met once, so they are read streamed, four or eight on their way in a thread (8191 tokens of 2560 values, eight
+// rows each, 377 MB: 64 us, 5.9 TB/s; with ordinary loads 94).
 template <bool WIDE, int HELD>
 __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict__ y, const int* __restrict__ positions,
                                                       const float* __restrict__ weights, uint16_t* __restrict__ out,
                                                       int64_t T, int top_k, int64_t R, int N, int pieces) {
-    // (neighbouring tokens on one XCD: their experts' rows are neighbours too)
-    const int64_t at = static_cast<int64_t>(xcd_remap(blockIdx.x, gridDim.x)) * 256 + threadIdx.x;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t token = at / pieces;
     const int n = 8 * static_cast<int>(at - token * pieces);
     if (token >= T) return;
@@ -529,7 +530,9 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
     }
 }
 
-// A wave per pair of a token and an expert.
+// A wave per pair of a token and an expert, so that no sum leaves a wave and dout's row comes from the caches for all but
+// the first pair of a token.  Bound by memory: the same sizes, 713 MB, take 127 us, 5.6 TB/s (ordinary loads and
+// stores, one piece at a time, 133 to 147).
 template <bool WIDE>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const uint16_t* __restrict__ dout,
                                                                const uint16_t* __restrict__ y,
@@ -538,7 +541,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const uint16_t* _
                                                                float* __restrict__ dweights, int64_t slots, int top_k,
                                                                int64_t R, int N) {
     const int lane = threadIdx.x & 63;
-    const int64_t slot = static_cast<int64_t>(xcd_remap(blockIdx.x, gridDim.x)) * 4 + (threadIdx.x >> 6);
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
     if (slot >= slots) return;
     const int64_t row = positions[slot], token = slot / top_k;
     if (row < 0 || row >= R) {
@@ -550,16 +553,28 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const uint16_t* _
     uint16_t* to = dy + row * N;
     float dot = 0.f;
     if constexpr (WIDE) {
-        for (int n = 8 * lane; n < N; n += 512) {
-            const u32x4_t a = load16(d + n), b = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(in + n));
-            u32x4_t r;
+        // five pieces of both rows on their way at a time
+        constexpr int HELD = 5;
+        for (int n0 = 8 * lane; n0 < N; n0 += 512 * HELD) {
+            u32x4_t a[HELD], b[HELD];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a0 = __uint_as_float(a[i] << 16), a1 = __uint_as_float(a[i] & 0xFFFF0000u);
-                dot += a0 * __uint_as_float(b[i] << 16) + a1 * __uint_as_float(b[i] & 0xFFFF0000u);
-                r[i] = pack_bf16(w * a0, w * a1);
+            for (int q = 0; q < HELD; ++q) {
+                const int n = n0 + 512 * q;
+                b[q] = n < N ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(in + n)) : u32x4_t{0, 0, 0, 0};
+                a[q] = n < N ? load16(d + n) : u32x4_t{0, 0, 0, 0};
             }
-            __builtin_nontemporal_store(r, reinterpret_cast<u32x4_t*>(to + n));
+#pragma unroll
+            for (int q = 0; q < HELD; ++q) {
+                const int n = n0 + 512 * q;
+                u32x4_t r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a0 = __uint_as_float(a[q][i] << 16), a1 = __uint_as_float(a[q][i] & 0xFFFF0000u);
+                    dot += a0 * __uint_as_float(b[q][i] << 16) + a1 * __uint_as_float(b[q][i] & 0xFFFF0000u);
+                    r[i] = pack_bf16(w * a0, w * a1);
+                }
+                if (n < N) __builtin_nontemporal_store(r, reinterpret_cast<u32x4_t*>(to + n));
+            }
         }
     } else {
         for (int n = lane; n < N; n += 64) {

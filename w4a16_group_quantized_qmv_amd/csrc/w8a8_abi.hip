@@ -74,7 +74,9 @@ struct TileCost {
 };
 constexpr TileCost kTileCost[kNumW8Tiles] = {   // steps of 128 values
     // 128 x 128          256 x 256             64 x 128            128 x 256             64 x 256
-    {5, 0.20, 0.13, 2.2}, {10, 0.42, 0.21, 0}, {4, 0.08, 0.17, 2}, {6, 0.36, 0.20, 0}, {5, 0.24, 0.20, 0}};
+    {5, 0.20, 0.13, 2.2}, {10, 0.42, 0.21, 0}, {4, 0.08, 0.17, 2}, {6, 0.36, 0.20, 0}, {5, 0.26, 0.20, 0},
+    // 128 x 128, 8 waves
+    {5, 0.22, 0.115, 0}};
 constexpr TileCost kColumnCost[kNumW8ColumnTiles] = {   // steps of 64 values
     // 64 x 128         128 x 256             256 x 256
     {5, 0.25, 0.2, 2}, {6, 0.80, 0.02, 0}, {7, 0.75, 0.15, 0}};
@@ -83,7 +85,9 @@ constexpr double kGradCost = 12;
 // The transposed product of codes alone decodes faster.
 constexpr double kUnscaled = 0.85;
 // A split's second launch, and its partials per output.
-constexpr double kSplitCost = 3.5, kPartialCost = 1.3e-6, kColumnPartialCost = 2.0e-6;
+constexpr double kSplitCost = 4.5, kPartialCost = 0.8e-6, kColumnPartialCost = 2.0e-6;
+// Weights are as often in memory as in the caches that the sweeps found them in: per step, about half of what that costs.
+constexpr double kColdStep = 0.08;
 constexpr int64_t kMaxSplit = 8;
 constexpr double kReadRate = 5.0e6;       // bytes of weights a microsecond
 
@@ -125,7 +129,7 @@ Product product_of(int32_t op, const Sizes& d, int32_t split_k, int64_t cus, boo
         p.decode = p.quantize = false;
     }
     const int64_t steps = back ? ceil_div(d.N, kW8ColumnStep) * sets : ceil_div(d.K, kW8Step);
-    const int count = back ? kNumW8ColumnTiles : kNumW8Tiles;
+    const int count = back ? kNumW8ColumnTiles : is_gated(op) ? kNumW8PairTiles : kNumW8Tiles;
     const double outputs = static_cast<double>(p.M) * p.N, pieces = static_cast<double>(std::min(d.E, d.R));
     const double memory = pieces * static_cast<double>(d.N) * d.K * sets / kReadRate;
     double best = 0;
@@ -172,6 +176,7 @@ Product product_of(int32_t op, const Sizes& d, int32_t split_k, int64_t cus, boo
                 const double alone = fixed + n * step(rows), beside = fixed + n * step(rows) * c.beside;
                 double t = rounds_time(tiles * static_cast<double>(z), cus, c, alone, beside);
                 if (z > 1) t += kSplitCost + (back ? kColumnPartialCost : kPartialCost) * outputs * static_cast<double>(z);
+                t += kColdStep * n;
                 p.split = static_cast<int>(z);
                 p.cut = 1;
                 consider(std::max(t, memory));
@@ -181,7 +186,7 @@ Product product_of(int32_t op, const Sizes& d, int32_t split_k, int64_t cus, boo
                 for (p.cut = 2; z == 1 && p.cut <= 4 && tiles > static_cast<double>(cus); p.cut *= 2) {
                     if (rest == 0 || rest * p.cut > round || p.height / p.cut < s.grain) continue;
                     const double low = fixed + n * step(std::ceil(rows / p.cut)) * (rest * p.cut > static_cast<double>(cus) ? c.beside : 1);
-                    consider(std::max(rounds_time(tiles - rest, cus, c, alone, beside) + low, memory));
+                    consider(std::max(rounds_time(tiles - rest, cus, c, alone, beside) + low + kColdStep * n, memory));
                 }
             }
             p.split = p.cut = 1;
@@ -440,7 +445,7 @@ int w8a8_plan(int32_t op, int64_t E, int64_t T, int64_t R, int64_t N, int64_t K,
     out->tile_k = back ? kW8ColumnStep : kW8Step;
     out->block_threads = 64 * s.waves;
     out->k_waves = 1;
-    out->variant = p.tile;
+    out->variant = p.tile + (!has_experts(op) && p.cut > 1 ? 10 : 0);
     if (p.decode) {
         out->path = W4A16_PATH_W8A8_QMV;
         out->tile_m = p.qmv.rows;

@@ -62,7 +62,7 @@ struct W8TileShape {
     int bm, bn, waves;
     int grain;                 // rows of a tile count in steps of this
 };
-constexpr int kNumW8Tiles = 5;
+constexpr int kNumW8Tiles = 6, kNumW8PairTiles = 5;      // (the last one is not for two weight sets)
 extern const W8TileShape kW8Tiles[kNumW8Tiles];
 constexpr int kW8Step = 128;          // values of the contraction in one pipeline step
 hipError_t launch_w8_tile(W8Epilogue epi, int tile, const W8TileArgs& args, hipStream_t stream);

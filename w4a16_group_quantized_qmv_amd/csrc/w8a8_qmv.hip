@@ -7,7 +7,7 @@
 //  * A workgroup has 16 weight rows; its waves take consecutive shares of the contraction.  A wave moves its share
 //    to LDS of its own, eight rows by one line of 128 bytes an instruction, up to five lines of every row at once,
 //    and waits only for itself.  (Loads to registers in the operand's layout, 64 bytes of 16 rows, took 9.2 us for
-//    one row of 9728 x 2560 where this takes KKK.)
+//    one row of 9728 x 2560 where this takes 6.4 us: 3.9 TB/s, a launch included.)
 //  * 16-byte chunk c of row r lies at c ^ ((r / 2) % 8), as in the tiles.  The 16x16x64 MFMA takes the weight rows
 //    as its rows and the activation rows as its columns.
 //  * The activations come as codes, or as bf16 and are quantized by every workgroup for itself: a launch less, for

@@ -9,7 +9,7 @@ namespace {
 
 // WAVES waves per row, HELD chunks of eight values a lane: they stay in registers between the reduction of the row's
 // magnitudes and its codes (HELD 0: longer rows are read twice, the second time from the L2).  Bound by reading
-// and writing once: 4096 x 2560 bf16, 31 MB, takes QQQ us.
+// and writing once: 4096 x 2560 bf16, 31 MB, takes 8.6 us, 3.7 TB/s.
 template <bool FP32, int WAVES, int HELD>
 __global__ __launch_bounds__(256) void w8_quantize_kernel(const void* __restrict__ x, int8_t* __restrict__ codes,
                                                           float* __restrict__ scales, int64_t R, int K) {
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void w8_quantize_kernel(const void* __restrict
     }
 }
 
-// Slices are int32, so their sum is exact in any order.
+// Slices are int32, so their sum is exact in any order.  Bound by reading them (three of 509 x 2560: 5.2 us).
 __global__ __launch_bounds__(256) void w8_sum_kernel(const int* __restrict__ ws, const float* __restrict__ a_scales,
                                                      const float* __restrict__ w_scales, uint16_t* __restrict__ y,
                                                      int64_t M, int N, int split) {

@@ -459,7 +459,9 @@ __global__ __launch_bounds__(64 * WR * WC) void w8_tile_kernel(const W8TileArgs 
 //              us; with four stages and one a compute unit 80, 128 x 128 79)
 //   128 x 256  three stages: between those (512 x 9728 x 2560 20.5 us)
 //    64 x 256  three stages: few rows of many experts (509 tokens' gated halves 83 us; 128 x 128 91, 64 x 128 97)
-const W8TileShape kW8Tiles[kNumW8Tiles] = {{128, 128, 4, 64}, {256, 256, 8, 64}, {64, 128, 4, 64}, {128, 256, 8, 64}, {64, 256, 8, 64}};
+//   128 x 128  of eight waves, four stages, one a compute unit: slices of a long contraction with weights from memory
+//              (509 x 2560 x 9728 in three slices 23 us, 64 x 128 in one 37; again from the caches 21 and 26); not paired
+const W8TileShape kW8Tiles[kNumW8Tiles] = {{128, 128, 4, 64}, {256, 256, 8, 64}, {64, 128, 4, 64}, {128, 256, 8, 64}, {64, 256, 8, 64}, {128, 128, 8, 64}};
 
 namespace {
 
@@ -482,8 +484,11 @@ hipError_t launch_shape(W8Epilogue epi, const W8TileArgs& args, hipStream_t stre
     };
     using E = W8Epilogue;
     if (!args.offsets) return run(w8_tile_kernel<E::kStore, false, MI, NI, WR, WC, STAGES>);
-    if (epi == E::kGlu) return run(w8_tile_kernel<E::kGlu, true, MI, NI, WR, WC, STAGES>);
-    if (epi == E::kGluGrad) return run(w8_tile_kernel<E::kGluGrad, true, MI, NI, WR, WC, STAGES>);
+    if (epi != E::kStore && NI % 2 != 0) return hipErrorInvalidValue;
+    if constexpr (NI % 2 == 0) {
+        if (epi == E::kGlu) return run(w8_tile_kernel<E::kGlu, true, MI, NI, WR, WC, STAGES>);
+        if (epi == E::kGluGrad) return run(w8_tile_kernel<E::kGluGrad, true, MI, NI, WR, WC, STAGES>);
+    }
     return run(w8_tile_kernel<E::kStore, true, MI, NI, WR, WC, STAGES>);
 }
 
@@ -496,6 +501,7 @@ hipError_t launch_w8_tile(W8Epilogue epi, int tile, const W8TileArgs& args, hipS
         case 2: return launch_shape<1, 2, 2, 2, 3>(epi, args, stream);      // 64 x 128, 4 waves
         case 3: return launch_shape<2, 2, 2, 4, 3>(epi, args, stream);      // 128 x 256, 8 waves
         case 4: return launch_shape<1, 2, 2, 4, 3>(epi, args, stream);      // 64 x 256, 8 waves
+        case 5: return launch_shape<2, 1, 2, 4, 4>(epi, args, stream);      // 128 x 128, 8 waves
         default: return hipErrorInvalidValue;
     }
 }
