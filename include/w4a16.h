@@ -638,7 +638,8 @@ int experts_combine(const uint16_t* y, const int32_t* positions, const float* we
                     int64_t R, int64_t N, void* stream);
 
 /* Its gradients from dout [T, N]: dy[positions[t, j]] = weights[t, j] * dout[t], dweights[t, j] = <dout[t],
- * y[positions[t, j]]> (0 for no row).  Rows of dy at no position are left as they were.  One launch. */
+ * y[positions[t, j]]> (0 for no row).  No row may be at two positions (experts_route's never are): dy would get one of
+ * the two.  Rows of dy at no position are left as they were.  One launch. */
 int experts_combine_backward(const uint16_t* dout, const uint16_t* y, const int32_t* positions, const float* weights,
                              uint16_t* dy, float* dweights, int64_t T, int32_t top_k, int64_t R, int64_t N, void* stream);
 

@@ -211,6 +211,56 @@ def test_a_block_forward_and_backward(lib, E, T, F, K, top):
     check(r["dx"], O.combine_reference(v["rows"], positions))
 
 
+@pytest.mark.parametrize("T", [6, 200])
+def test_a_padded_batch(lib, T):
+    """Tokens of padding, all logits minus infinity and x and dout NaN, reach no expert: the others' results are those of a
+    batch without them, theirs zeros."""
+    import torch
+    announce(f"experts block, padded, T={T}")
+    _, x, logits, ((gate, _), (up, _), (down, _)), dout = block_problem(8, T, 48, 96, 3 * T)
+    real = np.flatnonzero(np.arange(T) % 3 != 1)
+    padding = np.setdiff1d(np.arange(T), real)
+    alone = block(lib, bf16(x[real]), to_gpu(logits[real]), gate, up, down, 2, bf16(dout[real]))
+    x[padding] = dout[padding] = np.nan
+    logits[padding] = -np.inf
+    r = block(lib, bf16(x), to_gpu(logits), gate, up, down, 2, bf16(dout))
+    rows = len(real) * 2
+    assert int(r["offsets"][-1]) == rows and (host(r["experts"])[padding] == -1).all()
+    for n in ("h", "y", "dy", "dh", "rows", "dgate", "dup"):
+        assert torch.equal(r[n][:rows], alone[n]), n
+    for n in ("out", "dx", "weights", "dlogits", "dweights"):
+        assert torch.equal(r[n][to_gpu(real)], alone[n]), n
+        assert bool((r[n][to_gpu(padding)] == 0).all()), n
+
+
+@pytest.mark.parametrize("kind", ["plain", "bf16"])
+@pytest.mark.parametrize("E", [16, 64, 256])
+def test_logits_at_any_alignment(lib, E, kind):
+    """Logits and their gradient one value behind a whole 16 bytes, against the same at the start of an allocation."""
+    import torch
+    announce(f"experts_route alignment E={E} {kind}")
+    T, top = 100, 5
+    values = torch.from_numpy(np.random.default_rng(E).standard_normal(T * E + 1).astype(np.float32)).cuda()
+    values = values.to(torch.bfloat16) if kind == "bf16" else values
+    shifted, whole = values[1:].view(T, E), values[1:].clone().view(T, E)
+    for renormalize in (True, False):
+        want = lib.experts_route(whole, top, renormalize)
+        for got, ref in zip(lib.experts_route(shifted, top, renormalize), want):
+            if ref.dtype is torch.float32:
+                # (the sums of the softmax in another order: 256 terms)
+                assert torch.allclose(got, ref, rtol=260 * 2.0 ** -24, atol=0)
+            else:
+                assert torch.equal(got, ref)
+        dw = torch.rand(T, top, device="cuda")
+        out = torch.full((T * E + 9,), -77.0, dtype=values.dtype, device="cuda")
+        lib.experts_route_backward(shifted, want[1], dw, renormalize, dlogits=out[1:1 + T * E].view(T, E))
+        assert bool((out[:1] == -77).all()) and bool((out[1 + T * E:] == -77).all())
+        reference, bound = O.route_backward_reference(whole.double().cpu().numpy(), host(want[1]), dw.double().cpu().numpy(), renormalize)
+        if kind == "bf16":
+            bound = bound + (np.abs(reference) + bound) * 2.0 ** -8
+        compare(out[1:1 + T * E].view(T, E).float(), reference, bound)
+
+
 def test_a_block_in_an_autograd_function(lib):
     """The block as a torch.autograd.Function: its gradients are the calls', eager and captured, forward and backward."""
     import torch

@@ -368,6 +368,22 @@ def test_offsets_that_make_no_sense_stay_inside_the_buffers(lib, R):
     check(y, O.w8_linear(xq, xs, codes[3], scales[3]), slice(R // 2, R))
 
 
+def test_offsets_whose_tiles_pass_31_bits(lib):
+    """Falling offsets give 512 experts 2^28 rows each, 2^31 tiles of 64 rows: only as many as the grid holds are taken."""
+    import torch
+    announce("w8a8 experts, tiles past 31 bits")
+    E, R, K = 1024, 1 << 28, 16
+    w, _ = weight(np.random.default_rng(8), 1, K)
+    x = bf16(np.random.default_rng(9).standard_normal((1, K)))
+    tokens = torch.zeros(R, dtype=torch.int32, device="cuda")
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[1::2] = R
+    y, untouched = guarded(R, 1)
+    lib.w8a8_experts_linear(x, w[0].expand(E, 1, K).contiguous(), w[1].expand(E, 1).contiguous(), offsets, tokens, y=y)
+    torch.cuda.synchronize()
+    assert bool((y == lib.w8a8_linear(x, *w)).all()) and untouched()
+
+
 def test_weights_past_four_gigabytes(lib):
     """The last of 130 experts starts beyond 2^32 bytes."""
     import torch

@@ -495,3 +495,11 @@ def test_shapes_that_do_not_fit_are_refused(model, name, change):
     with pytest.raises(ValueError):
         PYTHON[name](a, {})
     assert not recorder.calls
+
+
+@pytest.mark.parametrize("top_k", [-1, 0, E + 1, 65])
+def test_more_experts_than_there_are_cannot_be_chosen(model, top_k):
+    torch, recorder = model
+    with pytest.raises(ValueError, match="top_k"):
+        w4.experts_route(arguments(torch)["logits"], top_k)
+    assert not recorder.calls

@@ -69,10 +69,12 @@ __device__ __forceinline__ bool find_expert_tile(const int* __restrict__ offsets
         end = max(min(max(offsets[e + 1], 0), R), first);
         return (end - first + BM - 1) / BM;
     };
+    // (offsets that fall could count rows twice, and past 31 bits: what the grid does not hold is left out)
+    const int room = static_cast<int>(gridDim.x);
     int mine = 0, first, end;
     for (int i = 0; i < per; ++i) {
         const int e = lane * per + i;
-        if (e < E) mine += rows_of(e, first, end);
+        if (e < E) mine = min(mine + rows_of(e, first, end), room);
     }
     int sum = mine;
 #pragma unroll
@@ -80,9 +82,8 @@ __device__ __forceinline__ bool find_expert_tile(const int* __restrict__ offsets
         const int v = __shfl_up(sum, d, 64);
         if (lane >= d) sum += v;
     }
-    // (offsets that fall could count rows twice: what the grid does not hold is left out)
     const int64_t all = static_cast<int64_t>(__builtin_amdgcn_readlane(sum, 63)) * tiles_n;
-    const int total = static_cast<int>(min(all, static_cast<int64_t>(gridDim.x)));
+    const int total = static_cast<int>(min(all, static_cast<int64_t>(room)));
     int whole = total;
     out.cut = 1;
     if (most > 1 && total > cus) {

@@ -39,7 +39,7 @@ from . import mxfp4 as _mx
 from .mxfp4 import _check_workspace, _matrix, _no_history, _output, _tensor
 
 __all__ = [
-    "W8A8_CHUNK", "W8A8_LINEAR", "W8A8_LINEAR_BACKWARD", "W8A8_QMM", "W8A8_EXPERTS_LINEAR",
+    "W8A8_CHUNK", "EXPERTS_MAX_TOP_K", "W8A8_LINEAR", "W8A8_LINEAR_BACKWARD", "W8A8_QMM", "W8A8_EXPERTS_LINEAR",
     "W8A8_EXPERTS_LINEAR_BACKWARD", "W8A8_EXPERTS_GATE_UP", "W8A8_EXPERTS_GATE_UP_BACKWARD", "PATH_W8A8",
     "PATH_W8A8_QMV", "w8a8_plan", "w8a8_quantize_rows", "qmm_w8a8", "w8a8_linear", "w8a8_linear_backward",
     "w8a8_experts_linear", "w8a8_experts_linear_backward", "w8a8_experts_gate_up_swiglu",
@@ -48,6 +48,7 @@ __all__ = [
 ]
 
 W8A8_CHUNK = 16
+EXPERTS_MAX_TOP_K = 64
 (W8A8_LINEAR, W8A8_LINEAR_BACKWARD, W8A8_QMM, W8A8_EXPERTS_LINEAR, W8A8_EXPERTS_LINEAR_BACKWARD, W8A8_EXPERTS_GATE_UP,
  W8A8_EXPERTS_GATE_UP_BACKWARD) = range(7)
 PATH_W8A8, PATH_W8A8_QMV = 10, 11
@@ -310,6 +311,8 @@ def experts_route(logits, top_k: int, renormalize: bool = True, weights=None, ex
     ``renormalize=False`` their part of the softmax over all of them.  Logits of minus infinity are never chosen: expert
     and position are -1 there and the weight 0."""
     T, E, index = _logits(logits)
+    if not 1 <= top_k <= min(E, EXPERTS_MAX_TOP_K):
+        raise ValueError(f"top_k={top_k} must be 1 .. {min(E, EXPERTS_MAX_TOP_K)} for {E} experts")
     weights = _output(weights, "weights", (T, top_k), logits, _FP32, stream)
     experts = _output(experts, "experts", (T, top_k), logits, _I32, stream)
     positions = _output(positions, "positions", (T, top_k), logits, _I32, stream)
@@ -361,8 +364,8 @@ def experts_combine(y, positions, weights=None, out=None, stream=None):
 
 
 def experts_combine_backward(dout, y, positions, weights, dy=None, dweights=None, stream=None):
-    """Gradients of ``experts_combine``; returns ``(dy, dweights)``.  Rows of ``dy`` at no position are left as they
-    were (a new ``dy`` holds no values there)."""
+    """Gradients of ``experts_combine``; returns ``(dy, dweights)``.  A row is at one position at most.  Rows of ``dy`` at
+    no position are left as they were (a new ``dy`` holds no values there)."""
     if weights is None:
         raise TypeError("weights must be a torch.Tensor")
     T, top_k, R, N, index = _pairs(y, positions, weights)
