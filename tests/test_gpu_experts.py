@@ -29,6 +29,9 @@ def make_logits(rng, T, E, kind):
         logits[T // 2] = -np.inf
     elif kind == "wide":
         logits *= 60
+    elif kind == "close":                                     # apart in the lowest bits alone, some rows only at the border
+        logits[::2] = 1 + rng.integers(0, 300, logits[::2].shape) * np.float32(2.0 ** -23)
+        logits[1::2] = np.float32(-3) - np.argsort(rng.random(logits[1::2].shape), 1) * np.float32(2.0 ** -16)
     elif kind == "bf16":
         logits = bf16_values(logits).astype(np.float32)
     return logits
@@ -41,7 +44,8 @@ def compare(got, want, bound):
 
 ROUTES = [(1, 1, 1, "plain"), (1, 60, 4, "plain"), (5, 60, 4, "bf16"), (3, 8, 8, "masked"), (64, 64, 6, "ties"), (65, 64, 2, "masked"),
           (63, 65, 8, "bf16"), (130, 128, 1, "plain"), (300, 256, 8, "ties"), (1000, 5, 3, "masked"), (257, 512, 10, "wide"),
-          (100, 1000, 8, "bf16"), (70, 1024, 64, "plain"), (2100, 3, 2, "ties"), (4161, 40, 8, "bf16")]
+          (100, 1000, 8, "bf16"), (70, 1024, 64, "plain"), (2100, 3, 2, "ties"), (4161, 40, 8, "bf16"),
+          (90, 256, 8, "close"), (20, 16, 16, "close"), (70, 1024, 9, "close"), (33, 100, 3, "close")]
 
 
 @pytest.mark.parametrize("renormalize", [True, False])

@@ -10,7 +10,9 @@
 // bits is the expert's count, and the bits below a token's are the rank of its pair.  The masks are built with
 // LDS atomics whose order does not matter, so a call repeats bit for bit.
 //
-// Bound by latency up to some hundred tokens (one launch of one workgroup), by reading and writing once above.
+// Bound by latency up to some thousand tokens, the router up to 64 in one launch of one workgroup (5 x 60: 3.4 us).  32767 x
+// 256 fp32, eight of them: choice 13.9 us (34 MB; a chain of one load, nine rounds and a barrier, two workgroups a compute
+// unit), scan 4.1, placing 6.1, backward 9.5 (69 MB: 7.3 TB/s, partly from the caches).
 #include "device_common.h"
 #include "mxfp4_device.h"
 #include "w8a8_internal.h"
@@ -82,27 +84,30 @@ __device__ __forceinline__ float row_max(float v) {
     }));
 }
 
-// The logits of a token on sixteen lanes, PER of each: WIDE (E = 16 PER) consecutive ones, loaded and stored in
-// whole pieces, else every sixteenth.
-template <int PER, bool WIDE>
-__device__ __forceinline__ int expert_of(int lane16, int i) { return WIDE ? lane16 * PER + i : lane16 + 16 * i; }
+// The logits of a token on sixteen lanes, PER of each: WIDE (E = 16 PER) in pieces of 16 bytes (or all PER, where those are
+// fewer), neighbours on neighbouring lanes, else one by one.
+template <int PER, bool WIDE, bool FP32>
+__device__ __forceinline__ int expert_of(int lane16, int i) {
+    constexpr int PIECE = !WIDE ? 1 : PER < (FP32 ? 4 : 8) ? PER : FP32 ? 4 : 8;
+    return (lane16 + 16 * (i / PIECE)) * PIECE + i % PIECE;
+}
 
 template <int PER, bool WIDE, bool FP32>
 __device__ __forceinline__ void load_row(const void* logits, int64_t token, int E, int lane16, float (&v)[PER]) {
     if constexpr (WIDE) {
         constexpr int WORDS = PER * (FP32 ? 4 : 2) / 4;
-        const uint32_t* in = static_cast<const uint32_t*>(logits) + (token * 16 + lane16) * WORDS;
+        const uint32_t* in = static_cast<const uint32_t*>(logits) + token * 16 * WORDS;
         uint32_t w[WORDS];
         if constexpr (WORDS % 4 == 0) {
 #pragma unroll
             for (int i = 0; i < WORDS / 4; ++i) {
-                const u32x4_t q = load16(in + 4 * i);
+                const u32x4_t q = load16(in + 4 * (lane16 + 16 * i));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[4 * i + e] = q[e];
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < WORDS; ++i) w[i] = in[i];
+            for (int i = 0; i < WORDS; ++i) w[i] = in[lane16 * WORDS + i];
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i)
@@ -110,16 +115,51 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t token, int 
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = expert_of<PER, false>(lane16, i);
+            const int e = expert_of<PER, false, FP32>(lane16, i);
             v[i] = e < E ? load_logit(logits, FP32, token * E + e) : -__builtin_inff();
         }
     }
 }
 
-// One token by sixteen lanes: lane j < top_k <= 16 gets the j-th chosen expert (-1 for none) and its weight.  Of a bf16
-// logit the key has 16 bits, and the expert's number fits below it: one number decides, and is met once.
+// The same numbers by rounds over whole keys: of equal ones the lowest expert.  Lane j gets the j-th expert.
+template <int PER, bool WIDE>
+__device__ __forceinline__ int choose_exactly(const RouteArgs& p, int64_t token, int lane16) {
+    uint32_t key[PER];
+    {
+        float v[PER];
+        load_row<PER, WIDE, true>(p.logits, token, p.E, lane16, v);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = order_key(v[i]);
+    }
+    int expert = -1;
+    for (int j = 0; j < p.top_k; ++j) {
+        uint32_t best = 0, at = 0xFFFFu;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+        best = row_reduce(best, [](uint32_t a, uint32_t b) { return max(a, b); });
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i)
+            if (key[i] == best) at = expert_of<PER, WIDE, true>(lane16, i);
+        at = row_reduce(at, [](uint32_t a, uint32_t b) { return min(a, b); });
+        if (lane16 == j && best != 0) expert = at;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (expert_of<PER, WIDE, true>(lane16, i) == static_cast<int>(at)) key[i] = 0;
+    }
+    return expert;
+}
+
+// One token by sixteen lanes: lane j < top_k <= 16 gets the j-th chosen expert (-1 for none) and its weight.
+//
+// The expert's number, from the largest down, takes the low bits of a logit's key: one number decides, and is met once.
+// With keys k_i and the last one chosen c, k_i - c modulo 2^32 is largest for the largest key below c, so a round is a
+// subtraction and a maximum for each, and nothing is struck out.  The low 16 bits of a bf16 logit are free.  Of an fp32
+// logit the lowest bits are lost; where two keys in a row differ in nothing else, the token is chosen exactly instead.
+// (32767 x 256 fp32, eight of them: 13.9 us; rounds that strike out, over whole keys, 15.3.)
 template <int PER, bool WIDE, bool FP32>
 __device__ __forceinline__ void select16(const RouteArgs& p, int64_t token, int lane16, int& expert, float& weight) {
+    constexpr uint32_t LOW = FP32 ? 16 * PER - 1 : 0xFFFFu;
+    static_assert((PER & (PER - 1)) == 0 && 16 * PER <= 65536, "the low bits hold an expert's number");
     uint32_t key[PER];
     bool nan = false;
     {
@@ -128,46 +168,38 @@ __device__ __forceinline__ void select16(const RouteArgs& p, int64_t token, int 
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             nan |= v[i] != v[i];
-            key[i] = order_key(v[i]);
-            if (!FP32 && key[i] != 0)      // (of the smallest keys the low bits are ones)
-                key[i] = (key[i] & 0xFFFF0000u) | (0xFFFFu - static_cast<uint32_t>(expert_of<PER, WIDE>(lane16, i)));
+            const uint32_t k = order_key(v[i]);
+            key[i] = k == 0 ? 0 : (k & ~LOW) | (LOW - static_cast<uint32_t>(expert_of<PER, WIDE, FP32>(lane16, i)));
         }
     }
-    auto value_of = [](uint32_t k) { return FP32 ? key_value(k) : key_value((k >> 31) ? k & 0xFFFF0000u : k | 0xFFFFu); };
-    auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
     expert = -1;
-    float chosen = 0.f, top = 0.f, sum = 0.f;
-    for (int j = 0; j < p.top_k; ++j) {
-        uint32_t best = 0;
+    uint32_t last = 0;                     // (2^32: above all keys)
+    bool unsure = false;
+    const int rounds = FP32 ? min(p.top_k + 1, p.E) : p.top_k;
+    for (int j = 0; j < rounds; ++j) {
+        uint32_t below = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) best = max(best, key[i]);
-        best = row_reduce(best, larger);
-        uint32_t at = 0xFFFFu - (best & 0xFFFFu);
-        if constexpr (FP32) {
-            // of equal ones the lowest expert
-            at = 0xFFFFu;
-#pragma unroll
-            for (int i = PER - 1; i >= 0; --i)
-                if (key[i] == best) at = expert_of<PER, WIDE>(lane16, i);
-            at = row_reduce(at, [](uint32_t a, uint32_t b) { return min(a, b); });
-        }
-        if (j == 0) {
-            top = value_of(best);
-            if (!p.renormalize) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) sum += key[i] ? expf(value_of(key[i]) - top) : 0.f;
-            }
-        }
-        if (lane16 == j && best != 0) {
-            expert = at;
-            chosen = value_of(best);
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (FP32 ? expert_of<PER, WIDE>(lane16, i) == static_cast<int>(at) : key[i] == best) key[i] = 0;
+        for (int i = 0; i < PER; ++i) below = max(below, key[i] - last);
+        below = row_reduce(below, [](uint32_t a, uint32_t b) { return max(a, b); });
+        const uint32_t best = below + last;
+        if (best == 0) break;              // (the same on the sixteen lanes) nothing is left
+        if (FP32) unsure |= j > 0 && (best ^ last) <= LOW;
+        if (lane16 == j && j < p.top_k) expert = LOW - (best & LOW);
+        last = best;
     }
+    if (FP32 && unsure) expert = choose_exactly<PER, WIDE>(p, token, lane16);
+    const float chosen = expert >= 0 ? load_logit(p.logits, FP32, token * p.E + expert) : -__builtin_inff();
+    const float top = row_max(chosen);
     const float mine = expert >= 0 ? expf(chosen - top) : 0.f;
-    sum = row_sum(p.renormalize ? mine : sum);
+    float sum = mine;
+    if (!p.renormalize) {
+        float v[PER];
+        load_row<PER, WIDE, FP32>(p.logits, token, p.E, lane16, v);
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sum += v[i] > -__builtin_inff() ? expf(v[i] - top) : 0.f;
+    }
+    sum = row_sum(sum);
     weight = expert >= 0 ? mine / sum : 0.f;
     if (row_reduce(nan, [](uint32_t a, uint32_t b) { return a | b; })) weight = __builtin_nanf("");
 }
@@ -399,7 +431,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         nan |= v[i] != v[i];
-        row[expert_of<PER, WIDE>(lane16, i)] = 0.f;
+        row[expert_of<PER, WIDE, FP32>(lane16, i)] = 0.f;
     }
     const bool any_nan = row_reduce(nan, [](uint32_t a, uint32_t b) { return a | b; }) != 0;
     // this lane's slots: their experts' logits, in rounds of sixteen
@@ -423,7 +455,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
         for_slots([&](int e, float l, float dw) { row[e] = expf(l - top) / sum * (dw - c); });
         wave_lds_fence();
 #pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = row[expert_of<PER, WIDE>(lane16, i)];
+        for (int i = 0; i < PER; ++i) v[i] = row[expert_of<PER, WIDE, FP32>(lane16, i)];
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) top = fmaxf(top, v[i]);
@@ -439,13 +471,13 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
         c = row_sum(c);
         wave_lds_fence();
 #pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = v[i] > 0.f ? v[i] / sum * (row[expert_of<PER, WIDE>(lane16, i)] - c) : v[i];
+        for (int i = 0; i < PER; ++i) v[i] = v[i] > 0.f ? v[i] / sum * (row[expert_of<PER, WIDE, FP32>(lane16, i)] - c) : v[i];
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] = any_nan ? __builtin_nanf("") : v[i];
     if constexpr (WIDE) {
         constexpr int WORDS = PER * (FP32 ? 4 : 2) / 4;
-        uint32_t* out = static_cast<uint32_t*>(dlogits) + (token * 16 + lane16) * WORDS;
+        uint32_t* out = static_cast<uint32_t*>(dlogits) + token * 16 * WORDS;
         uint32_t w[WORDS];
 #pragma unroll
         for (int i = 0; i < WORDS; ++i)
@@ -453,15 +485,15 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
         if constexpr (WORDS % 4 == 0) {
 #pragma unroll
             for (int i = 0; i < WORDS; i += 4)
-                *reinterpret_cast<u32x4_t*>(out + i) = u32x4_t{w[i], w[i + 1], w[i + 2], w[i + 3]};
+                *reinterpret_cast<u32x4_t*>(out + 4 * lane16 + 16 * i) = u32x4_t{w[i], w[i + 1], w[i + 2], w[i + 3]};
         } else {
 #pragma unroll
-            for (int i = 0; i < WORDS; ++i) out[i] = w[i];
+            for (int i = 0; i < WORDS; ++i) out[lane16 * WORDS + i] = w[i];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = expert_of<PER, false>(lane16, i);
+            const int e = expert_of<PER, false, FP32>(lane16, i);
             if (e >= E) continue;
             if (FP32)
                 static_cast<float*>(dlogits)[token * E + e] = v[i];
