@@ -45,6 +45,7 @@ def compare(got, want, bound):
 ROUTES = [(1, 1, 1, "plain"), (1, 60, 4, "plain"), (5, 60, 4, "bf16"), (3, 8, 8, "masked"), (64, 64, 6, "ties"), (65, 64, 2, "masked"),
           (63, 65, 8, "bf16"), (130, 128, 1, "plain"), (300, 256, 8, "ties"), (1000, 5, 3, "masked"), (257, 512, 10, "wide"),
           (100, 1000, 8, "bf16"), (70, 1024, 64, "plain"), (2100, 3, 2, "ties"), (4161, 40, 8, "bf16"),
+          (75, 1024, 10, "bf16"), (9, 1000, 5, "ties"), (80, 600, 16, "masked"), (66, 200, 40, "close"), (66, 700, 33, "bf16"),
           (90, 256, 8, "close"), (20, 16, 16, "close"), (70, 1024, 9, "close"), (33, 100, 3, "close")]
 
 

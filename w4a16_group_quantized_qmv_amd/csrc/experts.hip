@@ -57,10 +57,6 @@ struct RouteArgs {
     bool fp32, renormalize;
 };
 
-__device__ __forceinline__ float key_value(uint32_t key) {
-    return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
-}
-
 // Sixteen lanes are a row of the DPP: rotations by 8, 4, 2 and 1 reduce over it, and leave the result in each.
 template <int N>
 __device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
@@ -73,27 +69,41 @@ __device__ __forceinline__ uint32_t row_reduce(uint32_t v, F f) {
     v = f(v, row_rotate<2>(v));
     return f(v, row_rotate<1>(v));
 }
-__device__ __forceinline__ float row_sum(float v) {
-    return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+
+// The same over the LANES of a token, 16 or all 64.
+template <int LANES, typename F>
+__device__ __forceinline__ uint32_t lanes_reduce(uint32_t v, F f) {
+    v = row_reduce(v, f);
+    if constexpr (LANES == 64) {
+        auto row = [&](int l) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l)); };
+        v = f(f(row(0), row(16)), f(row(32), row(48)));
+    }
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    return __uint_as_float(lanes_reduce<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
 }
-__device__ __forceinline__ float row_max(float v) {
-    return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+    return __uint_as_float(lanes_reduce<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
         return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
     }));
 }
 
-// The logits of a token on sixteen lanes, PER of each: WIDE (E = 16 PER) in pieces of 16 bytes (or all PER, where those are
-// fewer), neighbours on neighbouring lanes, else one by one.
-template <int PER, bool WIDE, bool FP32>
-__device__ __forceinline__ int expert_of(int lane16, int i) {
+// The logits of a token on its lanes, PER of each: WIDE (E = 16 PER, sixteen lanes) in pieces of 16 bytes (or all PER,
+// where those are fewer), neighbours on neighbouring lanes, else one by one.
+template <int PER, bool WIDE, bool FP32, int LANES = 16>
+__device__ __forceinline__ int expert_of(int lane, int i) {
     constexpr int PIECE = !WIDE ? 1 : PER < (FP32 ? 4 : 8) ? PER : FP32 ? 4 : 8;
-    return (lane16 + 16 * (i / PIECE)) * PIECE + i % PIECE;
+    return (lane + LANES * (i / PIECE)) * PIECE + i % PIECE;
 }
 
-template <int PER, bool WIDE, bool FP32>
-__device__ __forceinline__ void load_row(const void* logits, int64_t token, int E, int lane16, float (&v)[PER]) {
+template <int PER, bool WIDE, bool FP32, int LANES = 16>
+__device__ __forceinline__ void load_row(const void* logits, int64_t token, int E, int lane, float (&v)[PER]) {
+    static_assert(!WIDE || LANES == 16, "pieces are for sixteen lanes");
     if constexpr (WIDE) {
         constexpr int WORDS = PER * (FP32 ? 4 : 2) / 4;
         const uint32_t* in = static_cast<const uint32_t*>(logits) + token * 16 * WORDS;
@@ -101,13 +111,13 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t token, int 
         if constexpr (WORDS % 4 == 0) {
 #pragma unroll
             for (int i = 0; i < WORDS / 4; ++i) {
-                const u32x4_t q = load16(in + 4 * (lane16 + 16 * i));
+                const u32x4_t q = load16(in + 4 * (lane + 16 * i));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[4 * i + e] = q[e];
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < WORDS; ++i) w[i] = in[lane16 * WORDS + i];
+            for (int i = 0; i < WORDS; ++i) w[i] = in[lane * WORDS + i];
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i)
@@ -115,19 +125,19 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t token, int 
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = expert_of<PER, false, FP32>(lane16, i);
+            const int e = expert_of<PER, false, FP32, LANES>(lane, i);
             v[i] = e < E ? load_logit(logits, FP32, token * E + e) : -__builtin_inff();
         }
     }
 }
 
-// The same numbers by rounds over whole keys: of equal ones the lowest expert.  Lane j gets the j-th expert.
-template <int PER, bool WIDE>
-__device__ __forceinline__ int choose_exactly(const RouteArgs& p, int64_t token, int lane16) {
+// The chosen experts by rounds over whole keys: of equal ones the lowest.  Lane j gets the j-th.
+template <int PER, bool WIDE, int LANES>
+__device__ __forceinline__ int choose_exactly(const RouteArgs& p, int64_t token, int lane) {
     uint32_t key[PER];
     {
         float v[PER];
-        load_row<PER, WIDE, true>(p.logits, token, p.E, lane16, v);
+        load_row<PER, WIDE, true, LANES>(p.logits, token, p.E, lane, v);
 #pragma unroll
         for (int i = 0; i < PER; ++i) key[i] = order_key(v[i]);
     }
@@ -136,40 +146,40 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& p, int64_t token,
         uint32_t best = 0, at = 0xFFFFu;
 #pragma unroll
         for (int i = 0; i < PER; ++i) best = max(best, key[i]);
-        best = row_reduce(best, [](uint32_t a, uint32_t b) { return max(a, b); });
+        best = lanes_reduce<LANES>(best, [](uint32_t a, uint32_t b) { return max(a, b); });
 #pragma unroll
         for (int i = PER - 1; i >= 0; --i)
-            if (key[i] == best) at = expert_of<PER, WIDE, true>(lane16, i);
-        at = row_reduce(at, [](uint32_t a, uint32_t b) { return min(a, b); });
-        if (lane16 == j && best != 0) expert = at;
+            if (key[i] == best) at = expert_of<PER, WIDE, true, LANES>(lane, i);
+        at = lanes_reduce<LANES>(at, [](uint32_t a, uint32_t b) { return min(a, b); });
+        if (lane == j && best != 0) expert = at;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (expert_of<PER, WIDE, true>(lane16, i) == static_cast<int>(at)) key[i] = 0;
+            if (expert_of<PER, WIDE, true, LANES>(lane, i) == static_cast<int>(at)) key[i] = 0;
     }
     return expert;
 }
 
-// One token by sixteen lanes: lane j < top_k <= 16 gets the j-th chosen expert (-1 for none) and its weight.
+// One token by LANES lanes: lane j < top_k gets the j-th chosen expert (-1 for none) and its weight.
 //
 // The expert's number, from the largest down, takes the low bits of a logit's key: one number decides, and is met once.
 // With keys k_i and the last one chosen c, k_i - c modulo 2^32 is largest for the largest key below c, so a round is a
 // subtraction and a maximum for each, and nothing is struck out.  The low 16 bits of a bf16 logit are free.  Of an fp32
 // logit the lowest bits are lost; where two keys in a row differ in nothing else, the token is chosen exactly instead.
 // (32767 x 256 fp32, eight of them: 13.9 us; rounds that strike out, over whole keys, 15.3.)
-template <int PER, bool WIDE, bool FP32>
-__device__ __forceinline__ void select16(const RouteArgs& p, int64_t token, int lane16, int& expert, float& weight) {
-    constexpr uint32_t LOW = FP32 ? 16 * PER - 1 : 0xFFFFu;
-    static_assert((PER & (PER - 1)) == 0 && 16 * PER <= 65536, "the low bits hold an expert's number");
+template <int PER, bool WIDE, bool FP32, int LANES>
+__device__ __forceinline__ void select(const RouteArgs& p, int64_t token, int lane, int& expert, float& weight) {
+    constexpr uint32_t LOW = FP32 ? LANES * PER - 1 : 0xFFFFu;
+    static_assert((PER & (PER - 1)) == 0 && LANES * PER <= 65536, "the low bits hold an expert's number");
     uint32_t key[PER];
     bool nan = false;
     {
         float v[PER];
-        load_row<PER, WIDE, FP32>(p.logits, token, p.E, lane16, v);
+        load_row<PER, WIDE, FP32, LANES>(p.logits, token, p.E, lane, v);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             nan |= v[i] != v[i];
             const uint32_t k = order_key(v[i]);
-            key[i] = k == 0 ? 0 : (k & ~LOW) | (LOW - static_cast<uint32_t>(expert_of<PER, WIDE, FP32>(lane16, i)));
+            key[i] = k == 0 ? 0 : (k & ~LOW) | (LOW - static_cast<uint32_t>(expert_of<PER, WIDE, FP32, LANES>(lane, i)));
         }
     }
     expert = -1;
@@ -180,85 +190,28 @@ __device__ __forceinline__ void select16(const RouteArgs& p, int64_t token, int 
         uint32_t below = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) below = max(below, key[i] - last);
-        below = row_reduce(below, [](uint32_t a, uint32_t b) { return max(a, b); });
+        below = lanes_reduce<LANES>(below, [](uint32_t a, uint32_t b) { return max(a, b); });
         const uint32_t best = below + last;
-        if (best == 0) break;              // (the same on the sixteen lanes) nothing is left
+        if (best == 0) break;              // (the same on all the token's lanes) nothing is left
         if (FP32) unsure |= j > 0 && (best ^ last) <= LOW;
-        if (lane16 == j && j < p.top_k) expert = LOW - (best & LOW);
+        if (lane == j && j < p.top_k) expert = LOW - (best & LOW);
         last = best;
     }
-    if (FP32 && unsure) expert = choose_exactly<PER, WIDE>(p, token, lane16);
+    if (FP32 && unsure) expert = choose_exactly<PER, WIDE, LANES>(p, token, lane);
     const float chosen = expert >= 0 ? load_logit(p.logits, FP32, token * p.E + expert) : -__builtin_inff();
-    const float top = row_max(chosen);
+    const float top = lanes_max<LANES>(chosen);
     const float mine = expert >= 0 ? expf(chosen - top) : 0.f;
     float sum = mine;
     if (!p.renormalize) {
         float v[PER];
-        load_row<PER, WIDE, FP32>(p.logits, token, p.E, lane16, v);
+        load_row<PER, WIDE, FP32, LANES>(p.logits, token, p.E, lane, v);
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) sum += v[i] > -__builtin_inff() ? expf(v[i] - top) : 0.f;
     }
-    sum = row_sum(sum);
+    sum = lanes_sum<LANES>(sum);
     weight = expert >= 0 ? mine / sum : 0.f;
-    if (row_reduce(nan, [](uint32_t a, uint32_t b) { return a | b; })) weight = __builtin_nanf("");
-}
-
-// The same by a whole wave, for up to 64 chosen experts: lane j < top_k gets the j-th.  Expert lane + 64 i.
-template <int PER>
-__device__ __forceinline__ void select64(const RouteArgs& p, int64_t token, int lane, int& expert, float& weight) {
-    float v[PER];
-    uint32_t key[PER];
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        v[i] = e < p.E ? load_logit(p.logits, p.fp32, token * p.E + e) : -__builtin_inff();
-        nan |= v[i] != v[i];
-        key[i] = order_key(v[i]);
-    }
-    expert = -1;
-    float chosen = 0.f, top = 0.f;
-    for (int j = 0; j < p.top_k; ++j) {
-        uint32_t best = 0;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-        // the larger key wins, of equal ones the lower expert
-        uint64_t pair = (static_cast<uint64_t>(best) << 32) | static_cast<uint32_t>(0xFFFF - (lane + 64 * at));
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) {
-            const uint64_t other = __shfl_xor(pair, d, 64);
-            pair = other > pair ? other : pair;
-        }
-        const uint32_t won = static_cast<uint32_t>(pair >> 32);
-        if (won == 0) break;                                   // (uniform) nothing is left
-        const int e = 0xFFFF - static_cast<int>(static_cast<uint32_t>(pair));
-        const float logit = key_value(won);
-        if (j == 0) top = logit;
-        if (lane == j) {
-            expert = e;
-            chosen = logit;
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (lane + 64 * i == e) key[i] = 0;
-    }
-    const float mine = expert >= 0 ? expf(chosen - top) : 0.f;
-    float sum = 0.f;
-    if (p.renormalize) {
-        sum = wave_sum(mine);
-    } else {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) sum += v[i] > -__builtin_inff() ? expf(v[i] - top) : 0.f;
-        sum = wave_sum(sum);
-    }
-    weight = expert >= 0 ? mine / sum : 0.f;
-    if (__ballot(nan)) weight = __builtin_nanf("");
+    if (lanes_reduce<LANES>(nan, [](uint32_t a, uint32_t b) { return a | b; })) weight = __builtin_nanf("");
 }
 
 // How a kernel chooses: by sixteen lanes (PER of 16 PER >= E), or by waves (PER of 64 PER >= E).
@@ -278,8 +231,7 @@ __device__ __forceinline__ void select_block(const RouteArgs& p, unsigned long l
     for (int t = threadIdx.x / LANES; t < count; t += 64 * kRouteWaves / LANES) {
         int expert;
         float weight;
-        if constexpr (C::WAVE) select64<C::PER>(p, first + t, lane, expert, weight);
-        else select16<C::PER, C::WIDE, C::FP32>(p, first + t, lane, expert, weight);
+        select<C::PER, C::WIDE, C::FP32, LANES>(p, first + t, lane, expert, weight);
         if (lane < p.top_k) {
             const int64_t at = (first + t) * p.top_k + lane;
             p.experts[at] = expert;
@@ -447,11 +399,11 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
     float top = -__builtin_inff(), sum = 0.f, c = 0.f;
     if (renormalize) {
         for_slots([&](int, float l, float) { top = fmaxf(top, l); });
-        top = row_max(top);
+        top = lanes_max<16>(top);
         for_slots([&](int, float l, float) { sum += expf(l - top); });
-        sum = row_sum(sum);
+        sum = lanes_sum<16>(sum);
         for_slots([&](int, float l, float dw) { c += expf(l - top) / sum * dw; });
-        c = row_sum(c);
+        c = lanes_sum<16>(c);
         for_slots([&](int e, float l, float dw) { row[e] = expf(l - top) / sum * (dw - c); });
         wave_lds_fence();
 #pragma unroll
@@ -459,16 +411,16 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) top = fmaxf(top, v[i]);
-        top = row_max(top);
+        top = lanes_max<16>(top);
         for_slots([&](int e, float, float dw) { row[e] = dw; });
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             v[i] = v[i] > -__builtin_inff() ? expf(v[i] - top) : 0.f;
             sum += v[i];
         }
-        sum = row_sum(sum);
+        sum = lanes_sum<16>(sum);
         for_slots([&](int, float l, float dw) { c += expf(l - top) / sum * dw; });
-        c = row_sum(c);
+        c = lanes_sum<16>(c);
         wave_lds_fence();
 #pragma unroll
         for (int i = 0; i < PER; ++i) v[i] = v[i] > 0.f ? v[i] / sum * (row[expert_of<PER, WIDE, FP32>(lane16, i)] - c) : v[i];
@@ -669,11 +621,19 @@ hipError_t launch_experts_route(const void* logits, bool fp32, int top_k, bool r
         hipLaunchKernelGGL(route_place_kernel, dim3(blocks), threads, 0, stream, args);
         return hipGetLastError();
     };
-    if (top_k > 16) {
-        if (E <= 128) return run(Choice<2, false, false, true>{});
-        return E <= 512 ? run(Choice<8, false, false, true>{}) : run(Choice<16, false, false, true>{});
-    }
-    return for_experts(E, fp32, logits, nullptr, run);
+    // A wave a token for more than sixteen chosen experts, and where sixteen lanes would have 64 logits each, unless they
+    // are whole rows of bf16 (32768 x 1024, eight chosen: fp32 70 us, by sixteen lanes 128; bf16 80 and 52; x 1000 79 and 93).
+    auto by_waves = [&](auto types) {
+        constexpr bool F = decltype(types)::value;
+        if (E <= 128) return run(Choice<2, false, F, true>{});
+        return E <= 512 ? run(Choice<8, false, F, true>{}) : run(Choice<16, false, F, true>{});
+    };
+    if (top_k > 16) return fp32 ? by_waves(std::true_type{}) : by_waves(std::false_type{});
+    return for_experts(E, fp32, logits, nullptr, [&](auto choice) {
+        using C = decltype(choice);
+        if constexpr (C::PER == 64 && (C::FP32 || !C::WIDE)) return run(Choice<16, false, C::FP32, true>{});
+        else return run(choice);
+    });
 }
 
 hipError_t launch_experts_route_backward(const void* logits, bool fp32, const int* experts, const float* dweights,
