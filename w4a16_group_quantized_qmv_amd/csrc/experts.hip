@@ -10,9 +10,9 @@
 // bits is the expert's count, and the bits below a token's are the rank of its pair.  The masks are built with
 // LDS atomics whose order does not matter, so a call repeats bit for bit.
 //
-// Bound by latency up to some thousand tokens, the router up to 64 in one launch of one workgroup (5 x 60: 3.4 us).  32767 x
-// 256 fp32, eight of them: choice 13.9 us (34 MB; a chain of one load, nine rounds and a barrier, two workgroups a compute
-// unit), scan 4.1, placing 6.1, backward 9.5 (69 MB: 7.3 TB/s, partly from the caches).
+// Bound by latency up to some thousand tokens, the router up to 64 in one launch of one workgroup (5 x 60: 3.2 us).  32767 x
+// 256 bf16, eight of them: choice 14 us (17 MB; a chain of one load, eight rounds and a barrier, two workgroups a compute
+// unit), scan 4.1, placing 6.1, backward 9.5 (36 MB, 3.8 TB/s).
 #include "device_common.h"
 #include "mxfp4_device.h"
 #include "w8a8_internal.h"
@@ -133,13 +133,16 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t token, int 
 
 // The chosen experts by rounds over whole keys: of equal ones the lowest.  Lane j gets the j-th.
 template <int PER, bool WIDE, int LANES>
-__device__ __forceinline__ int choose_exactly(const RouteArgs& p, int64_t token, int lane) {
+__device__ __forceinline__ int choose_exactly(const RouteArgs& p, int64_t token, int lane, bool& nan) {
     uint32_t key[PER];
     {
         float v[PER];
         load_row<PER, WIDE, true, LANES>(p.logits, token, p.E, lane, v);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) key[i] = order_key(v[i]);
+        for (int i = 0; i < PER; ++i) {
+            nan |= v[i] != v[i];
+            key[i] = order_key(v[i]);
+        }
     }
     int expert = -1;
     for (int j = 0; j < p.top_k; ++j) {
@@ -159,19 +162,15 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& p, int64_t token,
     return expert;
 }
 
-// One token by LANES lanes: lane j < top_k gets the j-th chosen expert (-1 for none) and its weight.
-//
-// The expert's number, from the largest down, takes the low bits of a logit's key: one number decides, and is met once.
-// With keys k_i and the last one chosen c, k_i - c modulo 2^32 is largest for the largest key below c, so a round is a
-// subtraction and a maximum for each, and nothing is struck out.  The low 16 bits of a bf16 logit are free.  Of an fp32
-// logit the lowest bits are lost; where two keys in a row differ in nothing else, the token is chosen exactly instead.
-// (32767 x 256 fp32, eight of them: 13.9 us; rounds that strike out, over whole keys, 15.3.)
+// The same by keys with a number: the expert's, from the largest down, takes the low bits of a logit's key, so that one
+// number decides.  With keys k_i and the last one chosen c, k_i - c modulo 2^32 is largest for the largest key below c: a
+// round is a subtraction and a maximum for each, and nothing is struck out.  The low 16 bits of a bf16 logit are free.  Of
+// an fp32 logit the lowest bits are lost; where two keys in a row differ in nothing else, the token is chosen exactly.
 template <int PER, bool WIDE, bool FP32, int LANES>
-__device__ __forceinline__ void select(const RouteArgs& p, int64_t token, int lane, int& expert, float& weight) {
+__device__ __forceinline__ int choose(const RouteArgs& p, int64_t token, int lane, bool& nan) {
     constexpr uint32_t LOW = FP32 ? LANES * PER - 1 : 0xFFFFu;
     static_assert((PER & (PER - 1)) == 0 && LANES * PER <= 65536, "the low bits hold an expert's number");
     uint32_t key[PER];
-    bool nan = false;
     {
         float v[PER];
         load_row<PER, WIDE, FP32, LANES>(p.logits, token, p.E, lane, v);
@@ -182,7 +181,7 @@ __device__ __forceinline__ void select(const RouteArgs& p, int64_t token, int la
             key[i] = k == 0 ? 0 : (k & ~LOW) | (LOW - static_cast<uint32_t>(expert_of<PER, WIDE, FP32, LANES>(lane, i)));
         }
     }
-    expert = -1;
+    int expert = -1;
     uint32_t last = 0;                     // (2^32: above all keys)
     bool unsure = false;
     const int rounds = FP32 ? min(p.top_k + 1, p.E) : p.top_k;
@@ -197,7 +196,17 @@ __device__ __forceinline__ void select(const RouteArgs& p, int64_t token, int la
         if (lane == j && j < p.top_k) expert = LOW - (best & LOW);
         last = best;
     }
-    if (FP32 && unsure) expert = choose_exactly<PER, WIDE, LANES>(p, token, lane);
+    if (FP32 && unsure) expert = choose_exactly<PER, WIDE, LANES>(p, token, lane, nan);
+    return expert;
+}
+
+// One token by LANES lanes: lane j < top_k gets the j-th chosen expert (-1 for none) and its weight.
+template <int PER, bool WIDE, bool FP32, int LANES>
+__device__ __forceinline__ void select(const RouteArgs& p, int64_t token, int lane, int& expert, float& weight) {
+    bool nan = false;
+    // (of up to 256 fp32 logits exactly at once: 32768 x 128 19.3 us, by numbers 20.7; bf16 17.4 and 17.1, x 256 23.0 and 21.9)
+    if constexpr (FP32 && LANES == 16 && PER <= 16) expert = choose_exactly<PER, WIDE, LANES>(p, token, lane, nan);
+    else expert = choose<PER, WIDE, FP32, LANES>(p, token, lane, nan);
     const float chosen = expert >= 0 ? load_logit(p.logits, FP32, token * p.E + expert) : -__builtin_inff();
     const float top = lanes_max<LANES>(chosen);
     const float mine = expert >= 0 ? expf(chosen - top) : 0.f;
