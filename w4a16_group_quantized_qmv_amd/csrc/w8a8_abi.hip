@@ -68,7 +68,8 @@ struct Product {
 
 // Microseconds of one tile: `fixed` for the first loads and the epilogue, and per pipeline step `base` and `grain` for
 // every grain of its rows, alone on its compute unit; `beside` times that with a second one beside it (0: only one fits).
-// Fitted to sweeps of every tile, height, split and cut on MI355X.
+// Fitted to sweeps of every tile, height, split and cut on MI355X.  Behind the best of such sweeps, on average: one matrix
+// (23 shapes) 3 to 6% from run to run, weights from the caches or from memory; experts (62 of shape and operator) 4%.
 struct TileCost {
     double fixed, base, grain, beside;
 };
