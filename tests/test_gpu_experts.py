@@ -293,6 +293,34 @@ def test_a_block_in_an_autograd_function(lib):
         assert torch.equal(a.grad, want["dx"]) and torch.equal(b.grad, want["dlogits"])
     with pytest.raises(ValueError, match="requires a gradient"):
         lib.experts_route(logits.clone().requires_grad_(), 2)
+    del a, b, out
+
+    # captured: leaves of its own, that no eager graph holds
+    leaves = [t.clone().requires_grad_() for t in (x, logits)]
+
+    def step():
+        result = Block.apply(*leaves)
+        return (result.detach(), *torch.autograd.grad(result, leaves, dout))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    for _ in range(3):
+        with torch.no_grad():
+            for t in leaves:
+                t.copy_(torch.randn(t.shape, device="cuda", generator=g))
+        graph.replay()
+        want = block(lib, *(t.detach() for t in leaves), gate, up, down, 2, dout)
+        torch.cuda.synchronize()
+        for got, n in zip(captured, ("out", "dx", "dlogits")):
+            assert torch.equal(got, want[n]), n
 
 
 def test_a_block_captured_and_replayed_with_new_inputs(lib):

@@ -449,7 +449,7 @@ def test_gradients_against_differences(lib):
 
 
 def _calls(lib):
-    """Every product with its inputs, as functions of ``kw``."""
+    """Every call with its inputs, as functions of ``kw``."""
     rng = np.random.default_rng(20)
     E, T, R, N, K = 6, 150, 300, 200, 528
     _, offsets, tokens, x, _, _ = expert_problem(E, T, R, N, K, "random", True)
@@ -457,7 +457,14 @@ def _calls(lib):
     gate, up, one = weight(rng, E, N, K)[0], weight(rng, E, N, K)[0], weight(rng, N, K)[0]
     dh, dy = bf16(rng.standard_normal((R, N))), bf16(rng.standard_normal((T, N)))
     few = x[:3].contiguous()
+    logits = bf16(rng.standard_normal((T, 40)))
+    chosen = lib.experts_route(logits, 3)
+    rows = bf16(rng.standard_normal((3 * T, N)))
     return {
+        "route": lambda **kw: lib.experts_route(logits, 3, **kw),
+        "route backward": lambda **kw: (lib.experts_route_backward(logits, chosen[1], chosen[0], **kw),),
+        "combine": lambda **kw: (lib.experts_combine(rows, chosen[2], chosen[0], **kw),),
+        "combine backward": lambda **kw: lib.experts_combine_backward(dy, rows, chosen[2], chosen[0], **kw),
         "quantize": lambda **kw: lib.w8a8_quantize_rows(x, **kw),
         "linear": lambda **kw: (lib.w8a8_linear(x, *one, **kw),),
         "linear few": lambda **kw: (lib.w8a8_linear(few, *one, **kw),),
