@@ -74,18 +74,19 @@ def _workspace_bytes(op, M, N, K, split_k, experts, rows, device):
     return int(w8a8_plan(op, M, N, K, split_k, 0, experts, rows)["workspace_bytes"])
 
 
-# The library's functions and torch's types, looked up once.
+# The library's functions and torch's types, looked up once.  The table is what a call looks at, so it comes last
+# and whole: another thread in its first call finds all of it or looks everything up for itself.
 _FN = {}
 _BF16 = _FP32 = _I8 = _I32 = None
 
 
 def _bind():
-    global _BF16, _FP32, _I8, _I32
+    global _FN, _BF16, _FP32, _I8, _I32
     if _mx._T is None:
         _mx._bind()
     torch, lib = _torch(), load()
-    _FN.update((n, getattr(lib, n)) for n in __all__ if hasattr(lib, n))
     _BF16, _FP32, _I8, _I32 = torch.bfloat16, torch.float32, torch.int8, torch.int32
+    _FN = {n: getattr(lib, n) for n in __all__ if hasattr(lib, n)}
 
 
 def _rows(t, name):
