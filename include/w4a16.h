@@ -600,14 +600,17 @@ int w8a8_linear_backward(const uint16_t* dy, const int8_t* codes, const float* s
 /*
  * Mixtures of experts.  A row is a pair of a token and an expert that it goes to; rows lie in the order of their
  * experts.  `offsets` int32 [E + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1.  `tokens` int32 [R]: the
- * rows' tokens.  `positions` int32 [T, top_k]: the rows of a token's experts, -1 for none.  They are made by
- * experts_route, or by the caller; they are read on the device and not checked, but no call reads or writes outside
- * its buffers, whatever they hold: offsets are taken into [0, R], positions outside [0, R) are skipped, and a row whose
- * token is outside [0, T) has activations of zeros.  Rows that no expert has (behind offsets[E]) are left as they
- * were in every output.
+ * rows' tokens.  `positions` int32 [T, top_k]: the rows of a token's experts, -1 for none, EXPERTS_NAN_ROW for none of
+ * a token whose logits hold a NaN.  They are made by experts_route, or by the caller; they are read on the device and
+ * not checked, but no call reads or writes outside its buffers, whatever they hold: offsets are taken into [0, R],
+ * positions outside [0, R) stand for no row and are skipped (EXPERTS_NAN_ROW makes the token's sums NaN), and a row
+ * whose token is outside [0, T) has activations of zeros.  Rows that no expert has (behind offsets[E]) are left as
+ * they were in every output.
  *
  * Limits: 1 <= E <= 1024, 1 <= top_k <= min(E, 64), T <= 2^24, T * top_k <= 2^30.
  */
+
+#define EXPERTS_NAN_ROW INT32_MIN
 
 /* Workspace bytes of experts_route (0 for a few tokens and for sizes outside the limits). */
 uint64_t experts_route_workspace_bytes(int64_t T, int64_t E);
@@ -621,7 +624,7 @@ uint64_t experts_route_workspace_bytes(int64_t T, int64_t E);
  *
  * Logits of minus infinity, and NaN, are never chosen: a token with fewer than top_k others gets expert -1, weight 0
  * and position -1, and the entries of tokens behind offsets[E] are -1.  A token whose logits hold a NaN gets NaN
- * weights.  Rows of one expert are in the order of their tokens; a call repeats bit for bit.
+ * weights, and the position EXPERTS_NAN_ROW where it has no expert, so that what is made of it is NaN.  Rows of one expert are in the order of their tokens; a call repeats bit for bit.
  */
 int experts_route(const void* logits, int32_t type, float* weights, int32_t* experts, int32_t* positions, int32_t* tokens,
                   int32_t* offsets, int64_t T, int64_t E, int32_t top_k, int32_t renormalize, void* workspace,
@@ -633,12 +636,13 @@ int experts_route_backward(const void* logits, int32_t type, const int32_t* expe
                            int64_t T, int64_t E, int32_t top_k, int32_t renormalize, void* stream);
 
 /* out[t] = sum_j weights[t, j] * y[positions[t, j]] with y [R, N], out [T, N] in bf16, the sum in fp32 and rounded
- * once; weights NULL stands for ones (the sum of gradients of gathered rows).  One launch. */
+ * once; weights NULL stands for ones (the sum of gradients of gathered rows).  NaN for a token with a position
+ * EXPERTS_NAN_ROW.  One launch. */
 int experts_combine(const uint16_t* y, const int32_t* positions, const float* weights, uint16_t* out, int64_t T, int32_t top_k,
                     int64_t R, int64_t N, void* stream);
 
 /* Its gradients from dout [T, N]: dy[positions[t, j]] = weights[t, j] * dout[t], dweights[t, j] = <dout[t],
- * y[positions[t, j]]> (0 for no row).  No row may be at two positions (experts_route's never are): dy would get one of
+ * y[positions[t, j]]> (0 for no row, NaN at EXPERTS_NAN_ROW).  No row may be at two positions (experts_route's never are): dy would get one of
  * the two.  Rows of dy at no position are left as they were.  One launch. */
 int experts_combine_backward(const uint16_t* dout, const uint16_t* y, const int32_t* positions, const float* weights,
                              uint16_t* dy, float* dweights, int64_t T, int32_t top_k, int64_t R, int64_t N, void* stream);

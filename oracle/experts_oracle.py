@@ -19,6 +19,8 @@ __all__ = ["w8_quantize", "w8_product", "w8_linear", "w8_linear_backward", "w8_g
 
 H, F, TINY = 2.0 ** -8, 2.0 ** -24, 2.0 ** -126
 
+NAN_ROW = -2 ** 31       # the position of a slot without an expert whose token's logits hold a NaN
+
 
 def w8_quantize(x):
     """Codes (int8) and scales (float32) of rows of float values: every step in fp32, as the format is defined."""
@@ -106,18 +108,19 @@ def route_reference(logits, top_k, renormalize=True):
     """(weights, bound), experts, positions, tokens, offsets by sorting each token's experts in Python."""
     T, E = logits.shape
     weights, experts = np.zeros((T, top_k)), np.full((T, top_k), -1, np.int32)
+    positions = np.full((T, top_k), -1, np.int32)
     for t in range(T):
         row = [float(v) for v in logits[t]]
         chosen = sorted((e for e in range(E) if row[e] > -np.inf), key=lambda e: (-row[e], e))[:top_k]
         experts[t, :len(chosen)] = chosen
         if any(v != v for v in row):
-            weights[t] = np.nan
+            weights[t], positions[t] = np.nan, NAN_ROW
         elif chosen:
             over = chosen if renormalize else [e for e in range(E) if row[e] > -np.inf]
             with np.errstate(invalid="ignore"):
                 p = {e: np.exp(np.float64(row[e]) - row[chosen[0]]) for e in over}
             weights[t, :len(chosen)] = [p[e] / sum(p.values()) for e in chosen]
-    positions, tokens, offsets = np.full((T, top_k), -1, np.int32), np.full(T * top_k, -1, np.int32), [0]
+    tokens, offsets = np.full(T * top_k, -1, np.int32), [0]
     row = 0
     for e in range(E):
         for t in range(T):
@@ -169,6 +172,8 @@ def combine_reference(y, positions, weights=None):
                 term = (1.0 if weights is None else float(weights[t, j])) * y[positions[t, j]]
                 out[t] += term
                 mass[t] += np.abs(term)
+            elif positions[t, j] == NAN_ROW:
+                out[t] = np.nan
     return _rounded(out, mass * (top_k + 1) * F + TINY)
 
 
@@ -183,6 +188,8 @@ def combine_backward_reference(dout, y, positions, weights):
                 dy[r] = float(weights[t, j]) * dout[t]
                 dw[t, j] = (dout[t] * y[r]).sum()
                 mass[t, j] = np.abs(dout[t] * y[r]).sum()
+            elif r == NAN_ROW:
+                dw[t, j] = np.nan
     return _rounded(dy, np.abs(dy) * F), (dw, mass * (y.shape[1] + 1) * F + TINY)
 
 

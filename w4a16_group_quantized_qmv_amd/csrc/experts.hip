@@ -15,6 +15,7 @@
 // unit), scan 4.1, placing 6.1, backward 9.5 (36 MB, 3.8 TB/s).
 #include "device_common.h"
 #include "mxfp4_device.h"
+#include "w4a16.h"
 #include "w8a8_internal.h"
 
 #include <type_traits>
@@ -275,7 +276,8 @@ __device__ __forceinline__ int expert_starts(int E, int* start, int* scratch, F 
     return total;
 }
 
-// The pairs of up to 64 tokens at their rows: start[e] + rank.
+// The pairs of up to 64 tokens at their rows: start[e] + rank.  Without an expert no row, and a mark that the combination
+// passes on where the token's weights are NaN: logits that are all NaN would else look like padding there.
 __device__ __forceinline__ void place_block(const RouteArgs& p, const unsigned long long* mask, const int* start,
                                             int64_t first, int count) {
     for (int s = threadIdx.x; s < count * p.top_k; s += blockDim.x) {
@@ -285,6 +287,8 @@ __device__ __forceinline__ void place_block(const RouteArgs& p, const unsigned l
         if (e >= 0) {
             row = start[e] + __popcll(mask[e] & ((1ull << t) - 1));
             p.tokens[row] = static_cast<int>(first) + t;
+        } else if (p.weights[at] != p.weights[at]) {
+            row = EXPERTS_NAN_ROW;
         }
         p.positions[at] = row;
     }
@@ -476,6 +480,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
     const int n = 8 * static_cast<int>(at - token * pieces);
     if (token >= T) return;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    float lost = 0.f;                      // (a sum is never -0: adding this one leaves its bits)
     // HELD rows on their way at a time
     for (int j0 = 0; j0 < top_k; j0 += HELD) {
         int64_t row[HELD];
@@ -485,6 +490,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
             const int64_t slot = token * top_k + min(j0 + j, top_k - 1);
             row[j] = positions[slot];
             w[j] = weights ? weights[slot] : 1.f;
+            if (row[j] == EXPERTS_NAN_ROW) lost = __builtin_nanf("");
             if (j0 + j >= top_k || row[j] >= R) row[j] = -1;
         }
         if constexpr (WIDE) {
@@ -512,6 +518,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
             }
         }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += lost;
     uint16_t* to = out + token * N + n;
     if constexpr (WIDE) {
         *reinterpret_cast<u32x4_t*>(to) = u32x4_t{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]),
@@ -538,7 +546,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const uint16_t* _
     if (slot >= slots) return;
     const int64_t row = positions[slot], token = slot / top_k;
     if (row < 0 || row >= R) {
-        if (lane == 0) dweights[slot] = 0.f;
+        if (lane == 0) dweights[slot] = row == EXPERTS_NAN_ROW ? __builtin_nanf("") : 0.f;
         return;
     }
     const float w = weights[slot];

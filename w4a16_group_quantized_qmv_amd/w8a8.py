@@ -9,7 +9,8 @@ Tensor conventions (all on the GPU, contiguous):
     scales             torch.float32  [N], for experts [E, N]: a row stands for scale * code
     offsets            torch.int32    [E + 1]      expert e has rows offsets[e] .. offsets[e + 1] - 1
     tokens             torch.int32    [R]          the rows' tokens
-    positions          torch.int32    [T, top_k]   the rows of a token's experts, -1 for none
+    positions          torch.int32    [T, top_k]   the rows of a token's experts, -1 for none; EXPERTS_NAN_ROW for none
+                                                   of a token whose logits hold a NaN, which makes its sums NaN
 A weight matrix is its ``(codes, scales)`` pair.  Rows behind ``offsets[E]`` are left as they were in every output.
 
 A block of a mixture of experts, forward and backward with frozen weights:
@@ -39,8 +40,8 @@ from . import mxfp4 as _mx
 from .mxfp4 import _check_workspace, _matrix, _no_history, _output, _tensor
 
 __all__ = [
-    "W8A8_CHUNK", "EXPERTS_MAX_TOP_K", "W8A8_LINEAR", "W8A8_LINEAR_BACKWARD", "W8A8_QMM", "W8A8_EXPERTS_LINEAR",
-    "W8A8_EXPERTS_LINEAR_BACKWARD", "W8A8_EXPERTS_GATE_UP", "W8A8_EXPERTS_GATE_UP_BACKWARD", "PATH_W8A8",
+    "W8A8_CHUNK", "EXPERTS_MAX_TOP_K", "EXPERTS_NAN_ROW", "W8A8_LINEAR", "W8A8_LINEAR_BACKWARD", "W8A8_QMM",
+    "W8A8_EXPERTS_LINEAR", "W8A8_EXPERTS_LINEAR_BACKWARD", "W8A8_EXPERTS_GATE_UP", "W8A8_EXPERTS_GATE_UP_BACKWARD", "PATH_W8A8",
     "PATH_W8A8_QMV", "w8a8_plan", "w8a8_quantize_rows", "qmm_w8a8", "w8a8_linear", "w8a8_linear_backward",
     "w8a8_experts_linear", "w8a8_experts_linear_backward", "w8a8_experts_gate_up_swiglu",
     "w8a8_experts_gate_up_swiglu_backward", "experts_route_workspace_bytes", "experts_route",
@@ -49,6 +50,7 @@ __all__ = [
 
 W8A8_CHUNK = 16
 EXPERTS_MAX_TOP_K = 64
+EXPERTS_NAN_ROW = -2 ** 31
 (W8A8_LINEAR, W8A8_LINEAR_BACKWARD, W8A8_QMM, W8A8_EXPERTS_LINEAR, W8A8_EXPERTS_LINEAR_BACKWARD, W8A8_EXPERTS_GATE_UP,
  W8A8_EXPERTS_GATE_UP_BACKWARD) = range(7)
 PATH_W8A8, PATH_W8A8_QMV = 10, 11
@@ -310,7 +312,8 @@ def experts_route(logits, top_k: int, renormalize: bool = True, weights=None, ex
     """The ``top_k`` experts of each token by ``logits`` (bf16 or fp32 ``[T, E]``) and the rows' order; returns
     ``(weights, experts, positions, tokens, offsets)``.  The weights are the softmax over the chosen experts, or with
     ``renormalize=False`` their part of the softmax over all of them.  Logits of minus infinity are never chosen: expert
-    and position are -1 there and the weight 0."""
+    and position are -1 there and the weight 0.  Logits that hold a NaN give NaN weights, and the position
+    ``EXPERTS_NAN_ROW`` where no expert is chosen, so that the token's results are NaN."""
     T, E, index = _logits(logits)
     if not 1 <= top_k <= min(E, EXPERTS_MAX_TOP_K):
         raise ValueError(f"top_k={top_k} must be 1 .. {min(E, EXPERTS_MAX_TOP_K)} for {E} experts")
