@@ -74,3 +74,29 @@ def test_the_mark_of_nan_logits_reaches_the_combination(lib, top, N):
     assert (values(dy)[~reached] == -77).all() and untouched()
     assert (np.isnan(want_dw) == (positions == lib.EXPERTS_NAN_ROW)).all()
     compare(dw, want_dw, bound_dw)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("E", [16, 20, 64, 300, 1000])
+def test_the_gradient_of_infinite_logits(lib, E, kind):
+    """Beside an infinite logit the softmax over all experts is NaN for each of them, and so are their gradients; masked
+    ones (minus infinity) and other tokens are as without it."""
+    announce(f"experts_route_backward, infinite logits, E={E} {kind}")
+    rng = np.random.default_rng(E)
+    T, top = 21, 3
+    logits = bf16_values(rng.standard_normal((T, E))).astype(np.float32)
+    logits[rng.random((T, E)) < 0.2] = -np.inf
+    logits[3, E // 2], logits[T - 1, [0, E - 1]] = np.inf, np.inf
+    logits[5] = -np.inf
+    t = bf16(logits) if kind == "bf16" else to_gpu(logits)
+    dw = rng.standard_normal((T, top)).astype(np.float32)
+    for renormalize in (True, False):
+        experts = lib.experts_route(t, top, renormalize)[1]
+        d = lib.experts_route_backward(t, experts, to_gpu(dw), renormalize)
+        with np.errstate(invalid="ignore"):
+            want, bound = O.route_backward_reference(logits.astype(np.float64), host(experts), dw.astype(np.float64), renormalize)
+        if not renormalize:
+            assert (np.isnan(want[[3, T - 1]]) == (logits[[3, T - 1]] > -np.inf)).all()
+        if kind == "bf16":
+            bound = bound + (np.abs(want) + bound) * 2.0 ** -8
+        compare(d.float(), want, bound)

@@ -426,17 +426,20 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
         for (int i = 0; i < PER; ++i) top = fmaxf(top, v[i]);
         top = lanes_max<16>(top);
         for_slots([&](int e, float, float dw) { row[e] = dw; });
+        // (masked experts, marked by -1, take no part; beside an infinite logit the sum is NaN, for all others)
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            v[i] = v[i] > -__builtin_inff() ? expf(v[i] - top) : 0.f;
-            sum += v[i];
+            const bool in = v[i] > -__builtin_inff();
+            const float e = in ? expf(v[i] - top) : 0.f;
+            sum += e;
+            v[i] = in ? e : -1.f;
         }
         sum = lanes_sum<16>(sum);
         for_slots([&](int, float l, float dw) { c += expf(l - top) / sum * dw; });
         c = lanes_sum<16>(c);
         wave_lds_fence();
 #pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = v[i] > 0.f ? v[i] / sum * (row[expert_of<PER, WIDE, FP32>(lane16, i)] - c) : v[i];
+        for (int i = 0; i < PER; ++i) v[i] = v[i] == -1.f ? 0.f : v[i] / sum * (row[expert_of<PER, WIDE, FP32>(lane16, i)] - c);
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] = any_nan ? __builtin_nanf("") : v[i];
