@@ -106,7 +106,9 @@ __device__ __forceinline__ void w8_columns(const W8ColumnsArgs& p, const Stages&
         constexpr int at = decltype(slot)::value % DEPTH;
         const int set = p.sets > 1 && t >= set_steps ? 1 : 0;
         const int64_t n = 64 * static_cast<int64_t>(t - set * set_steps), row = static_cast<int64_t>(expert) * N + n;
-        const __amdgpu_buffer_rsrc_t cr = mx_resource(p.w[set] + row * K + c0, (N - n) * K - c0);
+        // (steps past a slice's end take no weights of the next one: zeros times an infinite one would be NaN)
+        const int64_t rows = EXPERTS || t < t_end ? N - n : 0;
+        const __amdgpu_buffer_rsrc_t cr = mx_resource(p.w[set] + row * K + c0, rows * K - c0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int column = 32 * unit_block + 16 * i;
@@ -114,7 +116,7 @@ __device__ __forceinline__ void w8_columns(const W8ColumnsArgs& p, const Stages&
             codes[at][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(cr, o, 0, 0));
         }
         if constexpr (SCALED) {
-            const __amdgpu_buffer_rsrc_t sr = mx_resource(p.w_scales[set] + row, 4 * (N - n));
+            const __amdgpu_buffer_rsrc_t sr = mx_resource(p.w_scales[set] + row, 4 * rows);
             scale[at] = __builtin_amdgcn_raw_buffer_load_b32(sr, 4 * unit_row, 0, 0);
         }
     };
