@@ -196,6 +196,9 @@ Product product_of(int32_t op, const Sizes& d, int32_t split_k, int64_t cus, boo
     return chosen;
 }
 
+// The gated backward's first launch: both projections once more, with another tile and grid than dx has.
+Product both_again(const Sizes& d, int64_t cus) { return product_of(W8A8_EXPERTS_GATE_UP_BACKWARD, d, 0, cus, false); }
+
 uint64_t partial_bytes(const Product& p) { return p.split == 1 ? 0 : static_cast<uint64_t>(p.split) * p.M * p.N * 4; }
 
 // Workspace that an operator cannot do without (the rest is for partials).
@@ -218,6 +221,10 @@ int plan_call(int32_t op, const Sizes& d, int32_t split_k, int32_t num_cus, Prod
     if (!p->decode && (p->blocks * 64 * s.waves >= kMaxThreads ||
                        (p->split > 1 && ceil_div(p->M * p->N, 4) >= kMaxThreads)))
         return W4A16_ERR_SHAPE;
+    if (op == W8A8_EXPERTS_GATE_UP_BACKWARD) {
+        const Product again = both_again(d, cus);
+        if (again.blocks * 64 * kW8Tiles[again.tile].waves >= kMaxThreads) return W4A16_ERR_SHAPE;
+    }
     if (d.T >= kMaxTokens) return W4A16_ERR_SHAPE;             // the quantizer's launch
     return W4A16_OK;
 }
@@ -574,8 +581,7 @@ int w8a8_experts_gate_up_swiglu_backward(const uint16_t* x, const int8_t* codes_
     int32_t cus;
     st = query_num_cus(&cus);
     if (st != W4A16_OK) return st;
-    const Product again = product_of(op, d, 0, cus, false);      // both projections once more
-    if (again.blocks * 64 * kW8Tiles[again.tile].waves >= kMaxThreads) return W4A16_ERR_SHAPE;
+    const Product again = both_again(d, cus);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     W8TileArgs args = tile_args(d, again, offsets, tokens, dgate);
     args.w[0] = codes_gate;
