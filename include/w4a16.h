@@ -529,8 +529,9 @@ int mxfp4_gate_up_swiglu_backward(const uint16_t* x, const uint8_t* codes_gate, 
  * matrix, and any symmetric per-row int8 checkpoint is one already.  Activations are quantized by the same
  * rule, in the calls that take bf16 x.  Ownership, streams, asynchrony and the status codes are those stated
  * at the top of this file, and so is the rule that all checks come before any launch.  Limits: 1 <= rows,
- * N <= 2^30 (activation rows below 2^24), 16 <= K <= 131056 (a sum of K products of codes fits an int32),
- * K % 16 == 0; x, dy, codes and the workspace 16-byte aligned, other bf16 buffers 2-byte and fp32 and
+ * N <= 2^30 (w8a8_linear: rows below 2^24), 16 <= K <= 131056 (a sum of K products of codes fits an int32),
+ * K % 16 == 0; sizes whose tiles would take 2^32 threads or more in one launch return W4A16_ERR_SHAPE, from the plan
+ * as well; x, dy, codes and the workspace 16-byte aligned, other bf16 buffers 2-byte and fp32 and
  * int32 buffers 4-byte aligned; an output that shares bytes with an input or another output returns
  * W4A16_ERR_OVERLAP.
  *
@@ -555,7 +556,7 @@ enum w8a8_op {
  *     code = clamp(rint(x * inv), -127, 127)          (product rounded to fp32, ties to even).
  *
  * Rows with a < 2^-110 get scale 0 and codes 0, rows that hold an infinity or a NaN the scale NaN and codes
- * 0, so that what is computed from them is NaN.  One launch.  Errors: W4A16_ERR_NULL, _ERR_SHAPE, _ERR_ALIGN,
+ * 0, so that what is computed from them is NaN.  One launch for every 2^23 rows.  Errors: W4A16_ERR_NULL, _ERR_SHAPE, _ERR_ALIGN,
  * _ERR_OVERLAP, _ERR_UNSUPPORTED (another x_type), _ERR_LAUNCH.
  */
 int w8a8_quantize_rows(const void* x, int32_t x_type, int8_t* codes, float* scales, int64_t R, int64_t K, void* stream);

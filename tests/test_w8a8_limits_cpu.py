@@ -4,6 +4,8 @@ import pytest
 
 import w4a16_group_quantized_qmv_amd as w4
 
+from test_w8a8_cpu import GOOD, NULL, SHAPE, call
+
 CUS = 256
 
 
@@ -16,3 +18,24 @@ def test_the_plan_of_the_gated_backward_knows_both_launches():
     with pytest.raises(ValueError):
         w4.w8a8_plan(w4.W8A8_EXPERTS_GATE_UP_BACKWARD, *sizes)
     assert w4.w8a8_plan(w4.W8A8_EXPERTS_GATE_UP_BACKWARD, 1000, 1 << 19, 16, 0, CUS, 1000, 1000)["path"] == w4.PATH_W8A8
+
+
+ROWS = (1 << 24) + 40
+
+
+@pytest.mark.parametrize("op,experts", [(w4.W8A8_QMM, 1), (w4.W8A8_LINEAR_BACKWARD, 1), (w4.W8A8_EXPERTS_LINEAR, 8),
+                                        (w4.W8A8_EXPERTS_LINEAR_BACKWARD, 8), (w4.W8A8_EXPERTS_GATE_UP, 8),
+                                        (w4.W8A8_EXPERTS_GATE_UP_BACKWARD, 8)])
+def test_rows_past_two_to_the_24_are_planned(op, experts):
+    """As many rows as the router makes of 2^24 tokens and fewer, where no call quantizes them in one launch."""
+    for rows in (1 << 24, ROWS):
+        assert w4.w8a8_plan(op, rows, 64, 64, 0, CUS, experts)["path"] == w4.PATH_W8A8
+    if experts > 1:
+        assert w4.w8a8_plan(op, 1 << 24, 64, 64, 0, CUS, experts, 1 << 25)["path"] == w4.PATH_W8A8
+
+
+def test_quantized_rows_past_two_to_the_24():
+    """The sizes pass: what is refused is the pointer that is missing."""
+    assert call("w8a8_quantize_rows", {**GOOD, "codes": None}, M=ROWS, K=16) == NULL
+    assert call("w8a8_quantize_rows", {**GOOD, "codes": None}, M=1 << 30, K=16) == NULL
+    assert call("w8a8_quantize_rows", {**GOOD, "codes": None}, M=(1 << 30) + 1, K=16) == SHAPE

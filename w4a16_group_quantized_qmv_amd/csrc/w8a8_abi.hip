@@ -17,7 +17,7 @@ using namespace w4a16;
 
 constexpr int64_t kMaxRows = int64_t{1} << 30;      // rows and columns: tile and row numbers stay inside 31 bits
 constexpr int64_t kMaxThreads = int64_t{1} << 32;   // threads of one launch stay below
-constexpr int64_t kMaxTokens = int64_t{1} << 24;    // a wave or four per token stay within that
+constexpr int64_t kMaxTokens = int64_t{1} << 24;    // the router's and the combination's tokens
 
 uint64_t round256(uint64_t v) { return (v + 255) / 256 * 256; }
 int64_t padded(int64_t N) { return ceil_div(N, 8) * 8; }
@@ -44,6 +44,7 @@ int check_sizes(int32_t op, const Sizes& d, int32_t split_k) {
     // the backward products contract over N
     if (is_backward(op) && d.N > kMaxK) return W4A16_ERR_SHAPE;
     if (has_experts(op)) return split_k > 1 ? W4A16_ERR_UNSUPPORTED : W4A16_OK;
+    if (op == W8A8_LINEAR && d.T >= kMaxTokens) return W4A16_ERR_SHAPE;
     return d.E != 1 || d.T != d.R ? W4A16_ERR_SHAPE : W4A16_OK;
 }
 
@@ -225,7 +226,6 @@ int plan_call(int32_t op, const Sizes& d, int32_t split_k, int32_t num_cus, Prod
         const Product again = both_again(d, cus);
         if (again.blocks * 64 * kW8Tiles[again.tile].waves >= kMaxThreads) return W4A16_ERR_SHAPE;
     }
-    if (d.T >= kMaxTokens) return W4A16_ERR_SHAPE;             // the quantizer's launch
     return W4A16_OK;
 }
 
@@ -427,7 +427,6 @@ extern "C" {
 int w8a8_quantize_rows(const void* x, int32_t x_type, int8_t* codes, float* scales, int64_t R, int64_t K, void* stream) {
     const int st = check_matrix(R, K);
     if (st != W4A16_OK) return st;
-    if (R >= kMaxTokens) return W4A16_ERR_SHAPE;               // four waves a row
     if (x_type != W8A8_BF16 && x_type != W8A8_FP32) return W4A16_ERR_UNSUPPORTED;
     if (!x || !codes || !scales) return W4A16_ERR_NULL;
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return W4A16_ERR_ALIGN;

@@ -128,7 +128,16 @@ __global__ __launch_bounds__(256) void w8_sum_kernel(const int* __restrict__ ws,
 
 hipError_t launch_w8_quantize(const void* x, bool x_fp32, int8_t* codes, float* scales, int64_t R, int K,
                               hipStream_t stream) {
-    // a wave per row up to 4096 values, a workgroup beyond
+    // a wave per row up to 4096 values, a workgroup beyond; 2^23 rows a launch, whose threads stay below 2^32
+    constexpr int64_t kRows = int64_t{1} << 23;
+    if (R > kRows) {
+        for (int64_t r = 0; r < R; r += kRows) {
+            const hipError_t e = launch_w8_quantize(static_cast<const uint8_t*>(x) + r * K * (x_fp32 ? 4 : 2), x_fp32, codes + r * K,
+                                                    scales + r, R - r < kRows ? R - r : kRows, K, stream);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
     auto form = [&](auto tc) {
         constexpr bool FP32 = decltype(tc)::value;
         auto run = [&](auto kernel, int rows) {
