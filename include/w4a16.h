@@ -608,7 +608,8 @@ int w8a8_linear_backward(const uint16_t* dy, const int8_t* codes, const float* s
  * whose token is outside [0, T) has activations of zeros.  Rows that no expert has (behind offsets[E]) are left as
  * they were in every output.
  *
- * Limits: 1 <= E <= 1024, 1 <= top_k <= min(E, 64), T <= 2^24, T * top_k <= 2^30.
+ * Limits: 1 <= E <= 1024, 1 <= top_k <= min(E, 64), T * top_k <= 2^30, 1 <= R <= 2^30; router and combination
+ * 1 <= T <= 2^24, the combination T * ceil(N / 8) <= 2^32 - 256, its gradients T * top_k <= 2^26 - 4.
  */
 
 #define EXPERTS_NAN_ROW INT32_MIN

@@ -55,3 +55,26 @@ def test_products_of_rows_past_two_to_the_24(lib):
     for got, want in zip(lib.w8a8_experts_gate_up_swiglu_backward(many, two, two, many_dy, offsets),
                          lib.w8a8_experts_gate_up_swiglu_backward(x, two, two, dy, alone)):
         assert same(got, want)
+
+
+def test_a_combination_of_two_to_the_26_pairs(lib):
+    announce("experts_combine, 2^26 pairs")
+    rng = np.random.default_rng(3)
+    T, top = (1 << 23) + 11, 8
+    for N in (8, 3):
+        y = bf16(rng.standard_normal((500, N)))
+        positions, weights = to_gpu(rng.integers(-1, 500, (1000, top)).astype(np.int32)), to_gpu(rng.random((1000, top)).astype(np.float32))
+        out = lib.experts_combine(y, repeated(positions, T), repeated(weights, T))
+        assert same(out, lib.experts_combine(y, positions, weights))
+
+
+def test_the_largest_gradient_of_a_combination(lib):
+    import torch
+    announce("experts_combine_backward, 2^26 - 8 pairs")
+    rng = np.random.default_rng(4)
+    T, top, N = (1 << 23) - 1, 8, 8
+    y, dout, weights = bf16(rng.standard_normal((8000, N))), bf16(rng.standard_normal((1000, N))), to_gpu(rng.random((1000, top)).astype(np.float32))
+    positions = torch.arange(T * top, dtype=torch.int32, device="cuda").view(T, top)
+    dy, dweights = lib.experts_combine_backward(repeated(dout, T), repeated(y, T * top), positions, repeated(weights, T))
+    want_dy, want_dweights = lib.experts_combine_backward(dout, y, positions[:1000], weights)
+    assert same(dy, want_dy) and same(dweights, want_dweights)

@@ -39,3 +39,16 @@ def test_quantized_rows_past_two_to_the_24():
     assert call("w8a8_quantize_rows", {**GOOD, "codes": None}, M=ROWS, K=16) == NULL
     assert call("w8a8_quantize_rows", {**GOOD, "codes": None}, M=1 << 30, K=16) == NULL
     assert call("w8a8_quantize_rows", {**GOOD, "codes": None}, M=(1 << 30) + 1, K=16) == SHAPE
+
+
+def test_limits_of_the_combination():
+    """Forward a thread for eight columns, backward a wave for a pair; where the sizes pass, the missing pointer is refused."""
+    def forward(T, top, N):
+        return call("experts_combine", {**GOOD, "y": None}, M=T, top=top, N=N)
+
+    def backward(T, top, N):
+        return call("experts_combine_backward", {**GOOD, "dw": None}, M=T, top=top, N=N)
+    assert forward(1 << 24, 8, 8) == forward(1 << 24, 64, 2040) == forward(1 << 21, 8, 16376) == forward((1 << 24) - 1, 8, 2048) == NULL
+    assert forward((1 << 24) + 1, 1, 8) == forward(1 << 24, 1, 2041) == forward(1 << 21, 8, 16384) == SHAPE
+    assert backward((1 << 23) - 1, 8, 16384) == backward((1 << 20) - 1, 64, 8) == backward(1 << 24, 3, 1 << 14) == NULL
+    assert backward(1 << 23, 8, 8) == backward(1 << 20, 64, 8) == backward(1 << 24, 4, 8) == SHAPE

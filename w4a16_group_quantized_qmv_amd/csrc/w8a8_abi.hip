@@ -413,11 +413,12 @@ int check_logits(const void* logits, int32_t type) {
     return aligned(logits, type == W8A8_FP32 ? 4 : 2) ? W4A16_OK : W4A16_ERR_ALIGN;
 }
 
-int check_combine(int64_t T, int64_t top_k, int64_t R, int64_t N) {
-    if (T < 1 || top_k < 1 || top_k > kMaxTopK || R < 1 || R > kMaxRows || N < 1 || N > kMaxRows) return W4A16_ERR_SHAPE;
-    // a thread per eight columns, a wave per token and expert
-    if (T > kMaxTokens || T * top_k >= kMaxThreads / 64 - 4 || T * ceil_div(N, 8) >= kMaxThreads - 256) return W4A16_ERR_SHAPE;
-    return W4A16_OK;
+int check_combine(int64_t T, int64_t top_k, int64_t R, int64_t N, bool backward) {
+    if (T < 1 || T > kMaxTokens || top_k < 1 || top_k > kMaxTopK || R < 1 || R > kMaxRows || N < 1 || N > kMaxRows)
+        return W4A16_ERR_SHAPE;
+    // a wave per token and expert backward, a thread per eight columns forward
+    const bool fits = backward ? T * top_k <= kMaxThreads / 64 - 4 : T * ceil_div(N, 8) <= kMaxThreads - 256;
+    return fits && T * top_k <= kMaxRows ? W4A16_OK : W4A16_ERR_SHAPE;
 }
 
 }  // namespace
@@ -647,7 +648,7 @@ int experts_route_backward(const void* logits, int32_t type, const int32_t* expe
 
 int experts_combine(const uint16_t* y, const int32_t* positions, const float* weights, uint16_t* out, int64_t T, int32_t top_k,
                     int64_t R, int64_t N, void* stream) {
-    const int st = check_combine(T, top_k, R, N);
+    const int st = check_combine(T, top_k, R, N, false);
     if (st != W4A16_OK) return st;
     if (!y || !positions || !out) return W4A16_ERR_NULL;
     if (!aligned(y, 2) || !aligned(out, 2) || !aligned(positions, 4) || !aligned(weights, 4)) return W4A16_ERR_ALIGN;
@@ -658,7 +659,7 @@ int experts_combine(const uint16_t* y, const int32_t* positions, const float* we
 
 int experts_combine_backward(const uint16_t* dout, const uint16_t* y, const int32_t* positions, const float* weights,
                              uint16_t* dy, float* dweights, int64_t T, int32_t top_k, int64_t R, int64_t N, void* stream) {
-    const int st = check_combine(T, top_k, R, N);
+    const int st = check_combine(T, top_k, R, N, true);
     if (st != W4A16_OK) return st;
     if (!dout || !y || !positions || !weights || !dy || !dweights) return W4A16_ERR_NULL;
     if (!aligned(dout, 2) || !aligned(y, 2) || !aligned(dy, 2) || !aligned(positions, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
