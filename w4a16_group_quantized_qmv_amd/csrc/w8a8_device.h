@@ -32,9 +32,9 @@ __device__ __forceinline__ void w8_loads_done_barrier() {
 }
 
 // The quantizer's rule for a row whose largest magnitude is a (a NaN counts as such): the factor that
-// takes values to codes and the scale that takes them back.  Below 2^-110, where 127 / a could pass the
-// largest fp32 number or a / 127 become subnormal, a row counts as zeros; a row with an infinity or a NaN
-// gets the scale NaN.  Both divisions are correctly rounded (the compiler's default).
+// takes values to codes and the scale that takes them back.  Below 2^-110 a row counts as zeros: the format's
+// own bound, a margin above 2^-119 and 2^-121, under which a / 127 is subnormal and 127 / a passes the largest
+// fp32 number; a row with an infinity or a NaN gets the scale NaN.  Both divisions are correctly rounded (the compiler's default).
 __device__ __forceinline__ void w8_row_scale(float a, float& inverse, float& scale) {
     const bool tiny = a < 0x1p-110f, finite = a < __builtin_inff();
     inverse = tiny || !finite ? 0.f : 127.f / a;
