@@ -65,8 +65,9 @@ struct Product {
 
 // Microseconds of one tile: `fixed` for the first loads and the epilogue, and per pipeline step `base` and `grain` for
 // every grain of its rows, alone on its compute unit; `beside` times that with a second one beside it (0: only one fits).
-// Fitted to sweeps of every tile, height, split and cut on MI355X.  Behind the best of such sweeps, on average: one matrix
-// (23 shapes) 3 to 6% from run to run, weights from the caches or from memory; experts (62 of shape and operator) 4%.
+// Fitted to sweeps of every tile, height, split and cut on MI355X.  Behind the best form of another sweep, on average and at
+// most: one matrix (22 shapes) 3.6 and 18% with weights from the caches, 3.3 and 19% from memory; transposed (12) 0.2 and 3%;
+// experts (71 of shape and operator, from the caches) 3.3 and 30%.
 struct TileCost {
     double fixed, base, grain, beside;
 };
