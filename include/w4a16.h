@@ -626,7 +626,9 @@ uint64_t experts_route_workspace_bytes(int64_t T, int64_t E);
  *
  * Logits of minus infinity, and NaN, are never chosen: a token with fewer than top_k others gets expert -1, weight 0
  * and position -1, and the entries of tokens behind offsets[E] are -1.  A token whose logits hold a NaN gets NaN
- * weights, and the position EXPERTS_NAN_ROW where it has no expert, so that what is made of it is NaN.  Rows of one expert are in the order of their tokens; a call repeats bit for bit.
+ * weights, and the position EXPERTS_NAN_ROW where it has no expert, so that what is made of it is NaN.  Beside a
+ * logit of plus infinity the softmax is NaN, as it is by its formula.  Rows of one expert are in the order of their
+ * tokens; a call repeats bit for bit.
  */
 int experts_route(const void* logits, int32_t type, float* weights, int32_t* experts, int32_t* positions, int32_t* tokens,
                   int32_t* offsets, int64_t T, int64_t E, int32_t top_k, int32_t renormalize, void* workspace,
@@ -665,7 +667,7 @@ int w8a8_experts_linear_backward(const uint16_t* dy, const int8_t* codes, const 
                                  size_t workspace_bytes, void* stream);
 
 /* Gated half of the experts' feed-forward blocks, h[r] = silu(Q(x) . Wg_e^T) * (Q(x) . Wu_e^T), both projections,
- * activation and product in one kernel. */
+ * activation and product in one kernel; x, tokens and T * K as for w8a8_experts_linear. */
 int w8a8_experts_gate_up_swiglu(const uint16_t* x, const int8_t* codes_gate, const float* scales_gate,
                                 const int8_t* codes_up, const float* scales_up, const int32_t* offsets,
                                 const int32_t* tokens, uint16_t* h, int64_t E, int64_t T, int64_t R, int64_t N, int64_t K,
